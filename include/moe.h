@@ -31,6 +31,11 @@
  *    I..2I-1 the up projection, w2 [E][H][I]. fp8 weights carry one fp32
  *    scale per 128x128 block ([E][2I/128][H/128], [E][H/128][I/128]); fp8
  *    activations one fp32 scale per 1x128 block of a row.
+ *  - mxfp4 is OCP MXFP4: E2M1 codes, two to a byte (element 2i of a row in the
+ *    low half of byte i), and one E8M0 byte per 32 elements of a row. Weights
+ *    w13 [E][2I][H/2] with scales [E][2I][H/32], w2 [E][H][I/2] with scales
+ *    [E][H][I/32]; activations [rows][H/2] with scales [rows][H/32]. Code
+ *    tensors are 16-byte, scale tensors 4-byte aligned.
  *  - Errors are reported synchronously by the return value; argument checks
  *    happen before anything is enqueued. Faults inside kernels surface at the
  *    caller's next synchronisation. Data values (NaN/Inf) are not checked.
@@ -53,7 +58,7 @@ typedef int moe_status;
 #define MOE_ERR_HIP 3          /* a HIP runtime call or kernel launch failed  */
 #define MOE_ERR_WORKSPACE 4    /* workspace null or smaller than required     */
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 } moe_dtype;
 typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_scoring;
 
 /* Gating ([Moreh-EP] Overview, Parallelization; remapped order after the
@@ -153,15 +158,17 @@ typedef struct moe_expert_weights {
  * E_local+1) the shared expert. fp32 accumulation. bf16: A is rounded to bf16
  * between the GEMMs. fp8: A is quantised per 1x128 block exactly like x_perm
  * (fp32 scale amax/448, round to nearest even), and block scales are applied
- * to each 128-deep partial product.
+ * to each 128-deep partial product. mxfp4: A is quantised from fp32 by the rule
+ * of moe_quantize_mxfp4, and the matrix cores apply the scales.
  *   x_perm [max_rows, H] (+ x_perm_scale [H/128, max_rows] for fp8, K-major
- *   as moe_permute writes it when max_rows = T*k+T),
+ *   as moe_permute writes it when max_rows = T*k+T; for mxfp4 codes
+ *   [max_rows, H/2] and E8M0 bytes [max_rows, H/32], cast to float*),
  *   expert_offsets [n_groups+1] (device; as written by moe_permute),
  *   y_perm [max_rows, H] (out): bf16 (fp32 for dt = MOE_F32).
  * max_rows bounds offsets[n_groups] (T*k+T for the maps of moe_permute).
  * Limits: bf16 needs H % 128 == 0 and I % 128 == 0; fp8 needs H % 256 == 0,
  * I % 128 == 0 and H, I <= 16384 (the per-item table of weight block
- * scales); E_local <= 1024; n_groups in {E_local, E_local+1} (the
+ * scales), mxfp4 the same; E_local <= 1024; n_groups in {E_local, E_local+1} (the
  * latter needs the shared weights).
  * workspace: moe_expert_ffn_workspace_size(w, max_rows) bytes. */
 size_t moe_expert_ffn_workspace_size(const moe_expert_weights* w, int max_rows);
@@ -258,6 +265,46 @@ moe_status moe_layer_fused(const void* x, const void* w_router, const float* bia
                            const moe_expert_weights* w, int32_t* topk_ids, float* topk_w,
                            void* out, void* workspace, size_t ws_bytes, void* stream);
 
+/* Microscaled 4-bit quantisation of rows, and reading it back.
+ * moe_quantize_mxfp4: x [rows, cols] (MOE_BF16 or MOE_F32) -> codes
+ *   [rows, cols/2] and scales [rows, cols/32] (out). Per block of 32 elements
+ *   of a row: e = floor(log2(max |v|)) - 2, clamped to [-127, 127]; scale byte
+ *   e + 127; code = the E2M1 value nearest to v / 2^e, ties to the even code,
+ *   saturating at 6 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives). A block of
+ *   zeros has byte 127; one with a NaN or an infinity has byte 255 (NaN) and
+ *   codes 0.
+ * moe_dequantize_mxfp4: out [rows, cols] (MOE_BF16 or MOE_F32) = E2M1(code) *
+ *   2^(byte - 127), exact in either type; NaN where the byte is 255.
+ * Limits: cols % 32 == 0; x and out 16-byte, codes 4-byte aligned. */
+moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_dt, int64_t rows, int cols, void* codes,
+                              uint8_t* scales, void* stream);
+moe_status moe_dequantize_mxfp4(const void* codes, const uint8_t* scales, int64_t rows, int cols, void* out,
+                                moe_dtype out_dt, void* stream);
+
+/* The whole layer for a few tokens with mxfp4 experts: gating as moe_route,
+ * the tokens quantised as moe_quantize_mxfp4, the picked experts that are local
+ * ([expert_base, expert_base + E_local)) and the shared expert (when the weights
+ * hold one), and the routing-weighted sum. Each distinct expert's weights are
+ * read once for all tokens. The intermediate A is quantised from fp32 as in
+ * moe_expert_ffn; the weighted sum is taken in fp32 over unrounded expert outputs
+ * and rounded once, so out differs from moe_expert_ffn + moe_combine by those
+ * roundings to bf16.
+ *   x [T,H] bf16, w_router [E,H] bf16 or NULL, bias [E] fp32 or NULL, w: dt =
+ *   MOE_MXFP4; topk_ids [T,k] int32 and topk_w [T,k] fp32: written by the call, or
+ *   read by it when w_router is NULL (E is then the number of experts that ids
+ *   count over; ids outside the local range add nothing, an id that stands
+ *   twice in a token's picks adds both weights); out [T,H] bf16 (may be x).
+ *   workspace: moe_layer_few_workspace_size(w, T, E, k) bytes of device memory,
+ *   256-byte aligned; its first 256 bytes must be zero before the first call, and
+ *   every completed call leaves them zero. Calls that overlap need a workspace each.
+ * Limits: T <= 16, k <= 8, k <= E, E <= 256 with a router, H % 256 == 0,
+ * H <= 8192, I % 128 == 0, I <= 16384. */
+size_t moe_layer_few_workspace_size(const moe_expert_weights* w, int T, int E, int k);
+moe_status moe_layer_few(const void* x, const void* w_router, const float* bias, int T, int E, int k,
+                         moe_scoring scoring, int renormalize, const moe_expert_weights* w, int expert_base,
+                         int32_t* topk_ids, float* topk_w, void* out, void* workspace, size_t ws_bytes,
+                         void* stream);
+
 /* Routing-weighted combine back to token order ([Moreh-EP] Overview:
  * dispatch/combine; the local half of it).
  *   out[t] = sum_{j: slot_to_row[t*k+j] >= 0} topk_w[t,j] * y_perm[slot_to_row[t*k+j]]
@@ -268,6 +315,27 @@ moe_status moe_layer_fused(const void* x, const void* w_router, const float* bia
 moe_status moe_combine(const void* y_perm, moe_dtype y_dt, const int32_t* slot_to_row,
                        const float* topk_w, int T, int k, int H, const int32_t* expert_offsets,
                        int shared_group, void* out, moe_dtype out_dt, void* stream);
+
+/* The block's residual and norms around the layer.
+ * moe_pre_norm:     h = x + delta_scale * delta (delta NULL: h = x)
+ *                   n = h / sqrt(mean(h^2) + eps) * gain (gain NULL: 1)
+ *   in fp32; h_out (NULL: not written; may be x or delta) and n_out get h and n rounded
+ *   once each, n from the unrounded h. x, delta, h_out, n_out [T,H] in dt
+ *   (MOE_BF16 or MOE_F32), gain [H] fp32.
+ * moe_combine_norm: c = moe_combine's sum, unrounded
+ *                   n = c / sqrt(mean(c^2) + eps) * gain (gain NULL: n = c)
+ *                   out = residual + alpha * gate * n (residual NULL: 0, gate NULL: 1)
+ *   in fp32, rounded once. gain [H] fp32; gate [gate_rows, H] with gate_rows 1
+ *   (one for all tokens) or T, residual [T,H] and out [T,H] (may be residual) in
+ *   out_dt; the other arguments as for moe_combine.
+ * Limits: 1 <= H <= 16384, eps >= 0. A row whose squares sum to 0 with eps = 0, or
+ * to more than fp32 holds, gives NaN or zeros as the formula does in fp32. */
+moe_status moe_pre_norm(const void* x, const void* delta, float delta_scale, const float* gain, float eps,
+                        moe_dtype dt, int T, int H, void* h_out, void* n_out, void* stream);
+moe_status moe_combine_norm(const void* y_perm, moe_dtype y_dt, const int32_t* slot_to_row, const float* topk_w,
+                            int T, int k, int H, const int32_t* expert_offsets, int shared_group,
+                            const float* gain, float eps, const void* gate, int gate_rows, float alpha,
+                            const void* residual, void* out, moe_dtype out_dt, void* stream);
 
 /* Host-only balanced partition of E experts into G sets of E/G with balanced
  * activation totals ([Moreh-EP] Inter-GPU load balancing: a balanced number

@@ -16,7 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # MOE_LIB_PATH selects another build of the same library (A/B comparisons)
 LIB_PATH = os.environ.get("MOE_LIB_PATH") or os.path.join(_HERE, "libmoe.so")
 
-F32, BF16, FP8_E4M3 = 0, 1, 2
+F32, BF16, FP8_E4M3, MXFP4 = 0, 1, 2, 3
 SOFTMAX, SIGMOID = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE = 0, 1, 2, 3, 4
 
@@ -25,6 +25,8 @@ EXPORTS = [
     "moe_expert_ffn", "moe_expert_ffn_gate_up", "moe_expert_ffn_down", "moe_expert_ffn_noalloc",
     "moe_quantize_tokens",
     "moe_expert_ffn_gate_up_tokens", "moe_layer_fused_workspace_size", "moe_layer_fused", "moe_combine",
+    "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_layer_few_workspace_size", "moe_layer_few",
+    "moe_pre_norm", "moe_combine_norm",
     "moe_balanced_partition", "moe_gather_rows",
     "moe_count_accumulate", "moe_coactivation", "moe_affinity_partition",
     "moe_status_string", "moe_last_error_message",
@@ -78,6 +80,14 @@ def lib() -> C.CDLL:
         L.moe_layer_fused.argtypes = [p, p, p, i, i, i, i, i, C.POINTER(moe_expert_weights), p, p, p, p,
                                       sz, p]
         L.moe_combine.argtypes = [p, i, p, p, i, i, i, p, i, p, i, p]
+        f = C.c_float
+        L.moe_quantize_mxfp4.argtypes = [p, i, C.c_int64, i, p, p, p]
+        L.moe_dequantize_mxfp4.argtypes = [p, p, C.c_int64, i, p, i, p]
+        L.moe_layer_few_workspace_size.argtypes = [C.POINTER(moe_expert_weights), i, i, i]
+        L.moe_layer_few_workspace_size.restype = sz
+        L.moe_layer_few.argtypes = [p, p, p, i, i, i, i, i, C.POINTER(moe_expert_weights), i, p, p, p, p, sz, p]
+        L.moe_pre_norm.argtypes = [p, p, f, p, f, i, i, i, p, p, p]
+        L.moe_combine_norm.argtypes = [p, i, p, p, i, i, i, p, i, p, f, p, i, f, p, p, i, p]
         L.moe_balanced_partition.argtypes = [p, i, i, p, p, p]
         L.moe_gather_rows.argtypes = [p, i, p, p, i, sz, p]
         L.moe_count_accumulate.argtypes = [p, i, p, p]
@@ -88,7 +98,8 @@ def lib() -> C.CDLL:
         L.moe_last_error_message.restype = C.c_char_p
         for f in ("moe_route", "moe_route_select", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_gate_up",
                   "moe_expert_ffn_down", "moe_expert_ffn_noalloc", "moe_quantize_tokens", "moe_expert_ffn_gate_up_tokens",
-                  "moe_layer_fused", "moe_combine",
+                  "moe_layer_fused", "moe_combine", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
+                  "moe_layer_few", "moe_pre_norm", "moe_combine_norm",
                   "moe_balanced_partition", "moe_gather_rows", "moe_count_accumulate",
                   "moe_coactivation", "moe_affinity_partition"):
             getattr(L, f).restype = C.c_int
@@ -253,6 +264,52 @@ def moe_combine(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shar
     _check("moe_combine", lib().moe_combine(
         _ptr(y_perm), y_dt, _ptr(slot_to_row), _ptr(topk_w), T, k, H, _ptr(expert_offsets),
         shared_group, _ptr(out), out_dt, _stream(stream)))
+
+
+def _here(*tensors):
+    """The calls launch on the current device: refuse tensors of another one."""
+    dev = torch.cuda.current_device() if any(isinstance(t, torch.Tensor) for t in tensors) else None
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+
+
+def moe_quantize_mxfp4(x, x_dt, rows, cols, codes, scales, stream=None):
+    _here(x, codes, scales)
+    _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
+        _ptr(x), x_dt, rows, cols, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_dequantize_mxfp4(codes, scales, rows, cols, out, out_dt, stream=None):
+    _here(codes, scales, out)
+    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(
+        _ptr(codes), _ptr(scales), rows, cols, _ptr(out), out_dt, _stream(stream)))
+
+
+def moe_layer_few_workspace_size(w: moe_expert_weights, T, E, k) -> int:
+    return int(lib().moe_layer_few_workspace_size(C.byref(w), T, E, k))
+
+
+def moe_layer_few(x, w_router, bias, T, E, k, scoring, renormalize, w: moe_expert_weights, expert_base, topk_ids,
+                  topk_w, out, workspace, ws_bytes, stream=None):
+    _here(x, w_router, bias, topk_ids, topk_w, out, workspace)
+    _check("moe_layer_few", lib().moe_layer_few(
+        _ptr(x), _ptr(w_router), _ptr(bias), T, E, k, scoring, int(bool(renormalize)), C.byref(w), expert_base,
+        _ptr(topk_ids), _ptr(topk_w), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def moe_pre_norm(x, delta, delta_scale, gain, eps, dt, T, H, h_out, n_out, stream=None):
+    _here(x, delta, gain, h_out, n_out)
+    _check("moe_pre_norm", lib().moe_pre_norm(
+        _ptr(x), _ptr(delta), delta_scale, _ptr(gain), eps, dt, T, H, _ptr(h_out), _ptr(n_out), _stream(stream)))
+
+
+def moe_combine_norm(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, gain, eps, gate,
+                     gate_rows, alpha, residual, out, out_dt, stream=None):
+    _here(y_perm, slot_to_row, topk_w, expert_offsets, gain, gate, residual, out)
+    _check("moe_combine_norm", lib().moe_combine_norm(
+        _ptr(y_perm), y_dt, _ptr(slot_to_row), _ptr(topk_w), T, k, H, _ptr(expert_offsets), shared_group,
+        _ptr(gain), eps, _ptr(gate), gate_rows, alpha, _ptr(residual), _ptr(out), out_dt, _stream(stream)))
 
 
 def moe_balanced_partition(counts, E, G, new_to_old, old_to_new, group_loads):

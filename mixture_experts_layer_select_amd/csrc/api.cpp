@@ -57,6 +57,8 @@ using namespace moe;
         if (!(cond)) return set_error(code, __VA_ARGS__); \
     } while (0)
 
+static bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
 extern "C" {
 
 const char* moe_status_string(moe_status s) {
@@ -173,15 +175,49 @@ static moe_status check_weights(const moe_expert_weights* w) {
         REQUIRE(w->H <= 16384 && w->I <= 16384, MOE_ERR_UNSUPPORTED,
                 "moe_expert_ffn: fp8 needs H, I <= 16384 (H=%d I=%d)", w->H, w->I);
         REQUIRE(w->w13_scale && w->w2_scale, MOE_ERR_INVALID_ARG, "moe_expert_ffn: fp8 needs scales");
+    } else if (w->dt == MOE_MXFP4) {
+        REQUIRE(w->H % 256 == 0 && w->I % 128 == 0, MOE_ERR_UNSUPPORTED,
+                "moe_expert_ffn: mxfp4 needs H %% 256 == 0 and I %% 128 == 0 (H=%d I=%d)", w->H, w->I);
+        REQUIRE(w->H <= 16384 && w->I <= 16384, MOE_ERR_UNSUPPORTED,
+                "moe_expert_ffn: mxfp4 needs H, I <= 16384 (H=%d I=%d)", w->H, w->I);
+        REQUIRE(w->w13_scale && w->w2_scale, MOE_ERR_INVALID_ARG, "moe_expert_ffn: mxfp4 needs scales");
+        REQUIRE(aligned(w->w13, 16) && aligned(w->w2, 16) && aligned(w->ws13, 16) && aligned(w->ws2, 16) &&
+                    aligned(w->w13_scale, 4) && aligned(w->w2_scale, 4) && aligned(w->ws13_scale, 4) &&
+                    aligned(w->ws2_scale, 4),
+                MOE_ERR_INVALID_ARG, "moe_expert_ffn: mxfp4 codes must be 16-byte and scales 4-byte aligned");
     } else {
         REQUIRE(w->dt == MOE_F32, MOE_ERR_UNSUPPORTED, "moe_expert_ffn: unknown dt %d", (int)w->dt);
     }
     return MOE_OK;
 }
 
+// fp8 and MXFP4 tensors come with a scale tensor
+static bool scaled(const moe_expert_weights* w) { return w->dt == MOE_FP8_E4M3 || w->dt == MOE_MXFP4; }
+
+static size_t ffn_bytes(const moe_expert_weights* w, int max_rows) {
+    return w->dt == MOE_MXFP4 ? mx_ffn_workspace_bytes(w, max_rows) : ffn_workspace_bytes(w, max_rows);
+}
+
+static moe_status run_gate_up(const moe_expert_weights* w, const void* x, const float* x_scale,
+                              const int32_t* offsets, int n_groups, int max_rows, void* ws, hipStream_t st,
+                              const ActSrc& src = ActSrc{nullptr, 0, 0, 0, 0}) {
+    if (w->dt != MOE_MXFP4) return launch_ffn_gate_up(w, x, x_scale, offsets, n_groups, max_rows, ws, st, src);
+    REQUIRE(aligned(x, 16) && aligned(x_scale, 4) && aligned(ws, 16), MOE_ERR_INVALID_ARG,
+            "moe_expert_ffn: mxfp4 activations and workspace must be 16-byte, their scales 4-byte aligned");
+    return launch_mx_gate_up(w, x, x_scale, offsets, n_groups, max_rows, ws, st, src);
+}
+
+static moe_status run_down(const moe_expert_weights* w, const int32_t* offsets, int n_groups, int max_rows,
+                           void* y, void* ws, hipStream_t st) {
+    if (w->dt != MOE_MXFP4) return launch_ffn_down(w, offsets, n_groups, max_rows, y, ws, st);
+    REQUIRE(aligned(y, 16) && aligned(ws, 16), MOE_ERR_INVALID_ARG,
+            "moe_expert_ffn: mxfp4 output and workspace must be 16-byte aligned");
+    return launch_mx_down(w, offsets, n_groups, max_rows, y, ws, st);
+}
+
 size_t moe_expert_ffn_workspace_size(const moe_expert_weights* w, int max_rows) {
     if (max_rows < 0 || check_weights(w) != MOE_OK) return 0;
-    return ffn_workspace_bytes(w, max_rows);
+    return ffn_bytes(w, max_rows);
 }
 
 static moe_status check_ffn_call(const char* fn, const moe_expert_weights* w, int n_groups,
@@ -194,12 +230,12 @@ static moe_status check_ffn_call(const char* fn, const moe_expert_weights* w, in
             "%s: n_groups=%d must be E_local or E_local+1", fn, n_groups);
     if (n_groups == w->E_local + 1) {
         REQUIRE(w->ws13 && w->ws2, MOE_ERR_INVALID_ARG, "%s: shared group without weights", fn);
-        REQUIRE(w->dt != MOE_FP8_E4M3 || (w->ws13_scale && w->ws2_scale), MOE_ERR_INVALID_ARG,
-                "%s: fp8 shared expert needs scales", fn);
+        REQUIRE(!scaled(w) || (w->ws13_scale && w->ws2_scale), MOE_ERR_INVALID_ARG,
+                "%s: fp8 and mxfp4 shared experts need scales", fn);
     }
     if (max_rows == 0) return MOE_OK;
     REQUIRE(expert_offsets, MOE_ERR_INVALID_ARG, "%s: null expert_offsets", fn);
-    const size_t need = ffn_workspace_bytes(w, max_rows);
+    const size_t need = ffn_bytes(w, max_rows);
     REQUIRE(workspace && ws_bytes >= need, MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn,
             ws_bytes, need);
     return MOE_OK;
@@ -214,9 +250,9 @@ moe_status moe_expert_ffn_gate_up(const moe_expert_weights* w, const void* x_per
                                   workspace, ws_bytes);
     if (s || max_rows == 0) return s;
     REQUIRE(x_perm, MOE_ERR_INVALID_ARG, "moe_expert_ffn_gate_up: null x_perm");
-    REQUIRE(w->dt != MOE_FP8_E4M3 || x_perm_scale, MOE_ERR_INVALID_ARG,
-            "moe_expert_ffn_gate_up: fp8 needs x_perm_scale");
-    return launch_ffn_gate_up(w, x_perm, x_perm_scale, expert_offsets, n_groups, max_rows, workspace,
+    REQUIRE(!scaled(w) || x_perm_scale, MOE_ERR_INVALID_ARG,
+            "moe_expert_ffn_gate_up: fp8 and mxfp4 need x_perm_scale");
+    return run_gate_up(w, x_perm, x_perm_scale, expert_offsets, n_groups, max_rows, workspace,
                               (hipStream_t)stream);
 }
 
@@ -241,14 +277,14 @@ moe_status moe_expert_ffn_gate_up_tokens(const moe_expert_weights* w, const void
     moe_status s = check_ffn_call("moe_expert_ffn_gate_up_tokens", w, n_groups, max_rows,
                                   expert_offsets, workspace, ws_bytes);
     if (s) return s;
-    REQUIRE(w->dt == MOE_FP8_E4M3, MOE_ERR_UNSUPPORTED, "moe_expert_ffn_gate_up_tokens: fp8 only");
+    REQUIRE(scaled(w), MOE_ERR_UNSUPPORTED, "moe_expert_ffn_gate_up_tokens: fp8 and mxfp4 only");
     REQUIRE(T >= 0 && k >= 1, MOE_ERR_INVALID_ARG, "moe_expert_ffn_gate_up_tokens: T=%d k=%d", T, k);
     REQUIRE((long)T * w->H < (1L << 31) && (long)T * (k + 1) < (1L << 31), MOE_ERR_UNSUPPORTED,
             "moe_expert_ffn_gate_up_tokens: T*H or T*(k+1) >= 2^31");
     if (max_rows == 0 || T == 0) return MOE_OK;
     REQUIRE(x_tokens && x_tokens_scale && row_to_slot, MOE_ERR_INVALID_ARG,
             "moe_expert_ffn_gate_up_tokens: null pointer");
-    return launch_ffn_gate_up(w, x_tokens, x_tokens_scale, expert_offsets, n_groups, max_rows,
+    return run_gate_up(w, x_tokens, x_tokens_scale, expert_offsets, n_groups, max_rows,
                               workspace, (hipStream_t)stream, ActSrc{row_to_slot, k, T * k, T, T});
 }
 
@@ -260,7 +296,7 @@ moe_status moe_expert_ffn_down(const moe_expert_weights* w, const int32_t* exper
                                   workspace, ws_bytes);
     if (s || max_rows == 0) return s;
     REQUIRE(y_perm, MOE_ERR_INVALID_ARG, "moe_expert_ffn_down: null y_perm");
-    return launch_ffn_down(w, expert_offsets, n_groups, max_rows, y_perm, workspace,
+    return run_down(w, expert_offsets, n_groups, max_rows, y_perm, workspace,
                            (hipStream_t)stream);
 }
 
@@ -272,12 +308,12 @@ moe_status moe_expert_ffn(const moe_expert_weights* w, const void* x_perm, const
                                   ws_bytes);
     if (s || max_rows == 0) return s;
     REQUIRE(x_perm && y_perm, MOE_ERR_INVALID_ARG, "moe_expert_ffn: null pointer");
-    REQUIRE(w->dt != MOE_FP8_E4M3 || x_perm_scale, MOE_ERR_INVALID_ARG,
-            "moe_expert_ffn: fp8 needs x_perm_scale");
-    s = launch_ffn_gate_up(w, x_perm, x_perm_scale, expert_offsets, n_groups, max_rows, workspace,
+    REQUIRE(!scaled(w) || x_perm_scale, MOE_ERR_INVALID_ARG,
+            "moe_expert_ffn: fp8 and mxfp4 need x_perm_scale");
+    s = run_gate_up(w, x_perm, x_perm_scale, expert_offsets, n_groups, max_rows, workspace,
                            (hipStream_t)stream);
     if (s) return s;
-    return launch_ffn_down(w, expert_offsets, n_groups, max_rows, y_perm, workspace,
+    return run_down(w, expert_offsets, n_groups, max_rows, y_perm, workspace,
                            (hipStream_t)stream);
 }
 
@@ -288,7 +324,7 @@ moe_status moe_expert_ffn_noalloc(const moe_expert_weights* w, const void* x_per
     moe_status s = check_weights(w);
     if (s) return s;
     REQUIRE(max_rows >= 0, MOE_ERR_INVALID_ARG, "moe_expert_ffn_noalloc: max_rows < 0");
-    const size_t need = ffn_workspace_bytes(w, max_rows);
+    const size_t need = ffn_bytes(w, max_rows);
     REQUIRE(need <= (size_t)MOE_NOALLOC_SCRATCH_BYTES, MOE_ERR_WORKSPACE,
             "moe_expert_ffn_noalloc: max_rows=%d needs %zu bytes of scratch, the static array "
             "holds %zu (use moe_expert_ffn with a workspace)",
@@ -299,12 +335,12 @@ moe_status moe_expert_ffn_noalloc(const moe_expert_weights* w, const void* x_per
                        (size_t)MOE_NOALLOC_SCRATCH_BYTES);
     if (s || max_rows == 0) return s;
     REQUIRE(x_perm && y_perm, MOE_ERR_INVALID_ARG, "moe_expert_ffn_noalloc: null pointer");
-    REQUIRE(w->dt != MOE_FP8_E4M3 || x_perm_scale, MOE_ERR_INVALID_ARG,
-            "moe_expert_ffn_noalloc: fp8 needs x_perm_scale");
-    s = launch_ffn_gate_up(w, x_perm, x_perm_scale, expert_offsets, n_groups, max_rows, scratch,
+    REQUIRE(!scaled(w) || x_perm_scale, MOE_ERR_INVALID_ARG,
+            "moe_expert_ffn_noalloc: fp8 and mxfp4 need x_perm_scale");
+    s = run_gate_up(w, x_perm, x_perm_scale, expert_offsets, n_groups, max_rows, scratch,
                            (hipStream_t)stream);
     if (s) return s;
-    return launch_ffn_down(w, expert_offsets, n_groups, max_rows, y_perm, scratch,
+    return run_down(w, expert_offsets, n_groups, max_rows, y_perm, scratch,
                            (hipStream_t)stream);
 }
 
@@ -343,6 +379,104 @@ moe_status moe_layer_fused(const void* x, const void* w_router, const float* bia
             ws_bytes, need);
     return launch_layer_fused(x, w_router, bias, T, E, k, scoring, renormalize ? 1 : 0, w, topk_ids,
                               topk_w, out, workspace, (hipStream_t)stream);
+}
+
+moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_dt, int64_t rows, int cols, void* codes,
+                              uint8_t* scales, void* stream) {
+    g_msg[0] = 0;
+    REQUIRE(rows >= 0 && cols >= 1, MOE_ERR_INVALID_ARG, "moe_quantize_mxfp4: rows=%ld cols=%d", (long)rows, cols);
+    REQUIRE(x_dt == MOE_BF16 || x_dt == MOE_F32, MOE_ERR_UNSUPPORTED, "moe_quantize_mxfp4: x must be bf16 or fp32");
+    REQUIRE(cols % 32 == 0, MOE_ERR_UNSUPPORTED, "moe_quantize_mxfp4: cols=%d not a multiple of 32", cols);
+    if (rows == 0) return MOE_OK;
+    REQUIRE(x && codes && scales, MOE_ERR_INVALID_ARG, "moe_quantize_mxfp4: null pointer");
+    REQUIRE(aligned(x, 16) && aligned(codes, 4), MOE_ERR_INVALID_ARG,
+            "moe_quantize_mxfp4: x must be 16-byte and codes 4-byte aligned");
+    return launch_mx_quantize(x, x_dt, (long)rows, cols, codes, scales, (hipStream_t)stream);
+}
+
+moe_status moe_dequantize_mxfp4(const void* codes, const uint8_t* scales, int64_t rows, int cols, void* out,
+                                moe_dtype out_dt, void* stream) {
+    g_msg[0] = 0;
+    REQUIRE(rows >= 0 && cols >= 1, MOE_ERR_INVALID_ARG, "moe_dequantize_mxfp4: rows=%ld cols=%d", (long)rows, cols);
+    REQUIRE(out_dt == MOE_BF16 || out_dt == MOE_F32, MOE_ERR_UNSUPPORTED,
+            "moe_dequantize_mxfp4: out must be bf16 or fp32");
+    REQUIRE(cols % 32 == 0, MOE_ERR_UNSUPPORTED, "moe_dequantize_mxfp4: cols=%d not a multiple of 32", cols);
+    if (rows == 0) return MOE_OK;
+    REQUIRE(codes && scales && out, MOE_ERR_INVALID_ARG, "moe_dequantize_mxfp4: null pointer");
+    REQUIRE(aligned(out, 16) && aligned(codes, 4), MOE_ERR_INVALID_ARG,
+            "moe_dequantize_mxfp4: out must be 16-byte and codes 4-byte aligned");
+    return launch_mx_dequantize(codes, scales, (long)rows, cols, out, out_dt, (hipStream_t)stream);
+}
+
+moe_status moe_pre_norm(const void* x, const void* delta, float delta_scale, const float* gain, float eps,
+                        moe_dtype dt, int T, int H, void* h_out, void* n_out, void* stream) {
+    g_msg[0] = 0;
+    REQUIRE(T >= 0 && H >= 1, MOE_ERR_INVALID_ARG, "moe_pre_norm: T=%d H=%d", T, H);
+    REQUIRE(dt == MOE_BF16 || dt == MOE_F32, MOE_ERR_UNSUPPORTED, "moe_pre_norm: dt must be MOE_BF16 or MOE_F32");
+    REQUIRE(norm_h_supported(H), MOE_ERR_UNSUPPORTED, "moe_pre_norm: H=%d > 16384", H);
+    REQUIRE(eps >= 0.0f, MOE_ERR_INVALID_ARG, "moe_pre_norm: eps must be >= 0");
+    if (T == 0) return MOE_OK;
+    REQUIRE(x && n_out, MOE_ERR_INVALID_ARG, "moe_pre_norm: null pointer");
+    REQUIRE(n_out != h_out, MOE_ERR_INVALID_ARG, "moe_pre_norm: h_out and n_out are the same buffer");
+    return launch_pre_norm(x, delta, delta_scale, gain, eps, dt, T, H, h_out, n_out, (hipStream_t)stream);
+}
+
+moe_status moe_combine_norm(const void* y_perm, moe_dtype y_dt, const int32_t* slot_to_row, const float* topk_w,
+                            int T, int k, int H, const int32_t* expert_offsets, int shared_group,
+                            const float* gain, float eps, const void* gate, int gate_rows, float alpha,
+                            const void* residual, void* out, moe_dtype out_dt, void* stream) {
+    g_msg[0] = 0;
+    REQUIRE(T >= 0 && k >= 1 && H >= 1, MOE_ERR_INVALID_ARG,
+            "moe_combine_norm: need T >= 0, k >= 1, H >= 1 (T=%d k=%d H=%d)", T, k, H);
+    REQUIRE(k <= 256, MOE_ERR_UNSUPPORTED, "moe_combine_norm: k=%d > 256", k);
+    REQUIRE((y_dt == MOE_BF16 || y_dt == MOE_F32) && (out_dt == MOE_BF16 || out_dt == MOE_F32),
+            MOE_ERR_UNSUPPORTED, "moe_combine_norm: dtypes must be MOE_BF16 or MOE_F32");
+    REQUIRE(norm_h_supported(H), MOE_ERR_UNSUPPORTED, "moe_combine_norm: H=%d > 16384", H);
+    REQUIRE(eps >= 0.0f, MOE_ERR_INVALID_ARG, "moe_combine_norm: eps must be >= 0");
+    REQUIRE(!gate || gate_rows == 1 || gate_rows == T, MOE_ERR_INVALID_ARG,
+            "moe_combine_norm: gate_rows=%d, must be 1 or T=%d", gate_rows, T);
+    if (T == 0) return MOE_OK;
+    REQUIRE(y_perm && slot_to_row && topk_w && out, MOE_ERR_INVALID_ARG, "moe_combine_norm: null pointer");
+    REQUIRE(shared_group < 0 || expert_offsets, MOE_ERR_INVALID_ARG,
+            "moe_combine_norm: shared_group without expert_offsets");
+    return launch_combine_norm(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, gain, eps,
+                               gate, gate_rows, alpha, residual, out, out_dt, (hipStream_t)stream);
+}
+
+size_t moe_layer_few_workspace_size(const moe_expert_weights* w, int T, int E, int k) {
+    if (T < 0 || E < 1 || k < 1 || check_weights(w) != MOE_OK) return 0;
+    return layer_few_workspace_bytes(w, T, E, k);
+}
+
+moe_status moe_layer_few(const void* x, const void* w_router, const float* bias, int T, int E, int k,
+                         moe_scoring scoring, int renormalize, const moe_expert_weights* w, int expert_base,
+                         int32_t* topk_ids, float* topk_w, void* out, void* workspace, size_t ws_bytes,
+                         void* stream) {
+    g_msg[0] = 0;
+    const moe_status s = check_weights(w);
+    if (s) return s;
+    REQUIRE(w->dt == MOE_MXFP4, MOE_ERR_UNSUPPORTED, "moe_layer_few: mxfp4 experts only");
+    REQUIRE(T >= 0 && E >= 1 && k >= 1 && k <= E, MOE_ERR_INVALID_ARG,
+            "moe_layer_few: need T >= 0, 1 <= k <= E (T=%d E=%d k=%d)", T, E, k);
+    REQUIRE(scoring == MOE_SOFTMAX || scoring == MOE_SIGMOID, MOE_ERR_INVALID_ARG,
+            "moe_layer_few: unknown scoring %d", (int)scoring);
+    REQUIRE(T <= 16 && k <= 8 && (E <= 256 || !w_router), MOE_ERR_UNSUPPORTED,
+            "moe_layer_few: needs T <= 16, k <= 8 and, with a router, E <= 256 (T=%d k=%d E=%d)", T, k, E);
+    REQUIRE(w->H <= 8192, MOE_ERR_UNSUPPORTED, "moe_layer_few: H=%d > 8192", w->H);
+    REQUIRE(expert_base >= 0 && w->E_local <= E && expert_base <= E - w->E_local, MOE_ERR_INVALID_ARG,
+            "moe_layer_few: experts [%d, +%d) outside the %d experts", expert_base, w->E_local, E);
+    REQUIRE(!w->ws13 == !w->ws2, MOE_ERR_INVALID_ARG, "moe_layer_few: shared w13 without w2 or back");
+    REQUIRE(!w->ws13 || (w->ws13_scale && w->ws2_scale), MOE_ERR_INVALID_ARG,
+            "moe_layer_few: the shared expert needs scales");
+    if (T == 0) return MOE_OK;
+    REQUIRE(x && topk_ids && topk_w && out, MOE_ERR_INVALID_ARG, "moe_layer_few: null pointer");
+    REQUIRE(aligned(x, 16) && aligned(w_router, 16) && aligned(workspace, 256), MOE_ERR_INVALID_ARG,
+            "moe_layer_few: x and w_router must be 16-byte, the workspace 256-byte aligned");
+    const size_t need = layer_few_workspace_bytes(w, T, E, k);
+    REQUIRE(workspace && ws_bytes >= need, MOE_ERR_WORKSPACE, "moe_layer_few: workspace %zu < %zu bytes", ws_bytes,
+            need);
+    return launch_layer_few(x, w_router, bias, T, E, k, scoring, renormalize ? 1 : 0, w, expert_base, topk_ids,
+                            topk_w, out, workspace, (hipStream_t)stream);
 }
 
 moe_status moe_combine(const void* y_perm, moe_dtype y_dt, const int32_t* slot_to_row,

@@ -115,6 +115,30 @@ moe_status launch_quantize_tokens(const void* x, int T, int H, void* codes, floa
 moe_status launch_ffn_down(const moe_expert_weights* w, const int32_t* offsets, int n_groups,
                            int max_rows, void* y_perm, void* ws, hipStream_t st);
 
+// MXFP4 rows and experts (mx.hip); scales are E8M0 bytes
+moe_status launch_mx_quantize(const void* x, moe_dtype x_dt, long rows, int cols, void* codes, void* scales,
+                              hipStream_t st);
+moe_status launch_mx_dequantize(const void* codes, const void* scales, long rows, int cols, void* out,
+                                moe_dtype out_dt, hipStream_t st);
+size_t mx_ffn_workspace_bytes(const moe_expert_weights* w, int max_rows);
+moe_status launch_mx_gate_up(const moe_expert_weights* w, const void* x, const void* x_scale,
+                             const int32_t* offsets, int n_groups, int max_rows, void* ws, hipStream_t st,
+                             const ActSrc& src);
+moe_status launch_mx_down(const moe_expert_weights* w, const int32_t* offsets, int n_groups, int max_rows,
+                          void* y_perm, void* ws, hipStream_t st);
+size_t layer_few_workspace_bytes(const moe_expert_weights* w, int T, int E, int k);
+moe_status launch_layer_few(const void* x, const void* w_router, const float* bias, int T, int E, int k,
+                            int scoring, int renorm, const moe_expert_weights* w, int base, int32_t* topk_ids,
+                            float* topk_w, void* out, void* ws, hipStream_t st);
+
+bool norm_h_supported(int H);
+moe_status launch_pre_norm(const void* x, const void* delta, float delta_scale, const float* gain, float eps,
+                           moe_dtype dt, int T, int H, void* h_out, void* n_out, hipStream_t st);
+moe_status launch_combine_norm(const void* y_perm, moe_dtype y_dt, const int32_t* slot_to_row,
+                               const float* topk_w, int T, int k, int H, const int32_t* offsets,
+                               int shared_group, const float* gain, float eps, const void* gate, int gate_rows,
+                               float alpha, const void* residual, void* out, moe_dtype out_dt, hipStream_t st);
+
 moe_status launch_combine(const void* y_perm, moe_dtype y_dt, const int32_t* slot_to_row,
                           const float* topk_w, int T, int k, int H, const int32_t* offsets,
                           int shared_group, void* out, moe_dtype out_dt, hipStream_t st);

@@ -1,0 +1,61 @@
+// Device code of the microscaled 4-bit format (OCP MXFP4: E2M1 elements, one
+// E8M0 scale per 32 of a row), shared by its kernels. Internal to libmoe.so.
+//
+// A block's scale is 2^e with e = floor(log2(amax)) - 2, so its largest
+// element lands in [4, 8) and is held as 4 or 6; e is clamped to the format's
+// -127..127 (byte e + 127). A code is the nearest E2M1 value of v / 2^e, ties
+// to the even code, saturating at 6: dividing by a power of two is exact and
+// v_cvt_scalef32_pk_fp4_f32 rounds this way (checked value by value, ties
+// included), so every code is exact. An all-zero block has byte 127; a block
+// with a NaN or an infinity has byte 255 (NaN in E8M0) and codes 0.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMxBlock = 32;
+constexpr uint32_t kMxNan = 255;
+
+// scale byte of a block from the bits of its largest |v| (integer maximum:
+// a NaN's bits are above an infinity's, which are above every number's)
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+    const int biased = (int)(amax_bits >> 23);  // 0 for denormals: below 2^-126, the clamp's side
+    const uint32_t b = (uint32_t)max(biased - 2, 0);
+    return biased == 255 ? kMxNan : amax_bits == 0 ? 127u : b;
+}
+// 2^-e of a scale byte (0..252 from mx_scale_byte); 0 for the NaN byte
+__device__ __forceinline__ float mx_inverse(uint32_t byte) {
+    return byte == kMxNan ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// eight values times inv = 2^-e -> eight codes, the first in the low nibble
+__device__ __forceinline__ uint32_t mx_pack8(const float* v, float inv) {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0] * inv, v[1] * inv, 1.0f, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2] * inv, v[3] * inv, 1.0f, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4] * inv, v[5] * inv, 1.0f, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6] * inv, v[7] * inv, 1.0f, 3);
+    return inv == 0.0f ? 0u : r;
+}
+
+// D += A B with both operands E2M1 (format 4): lane (l31, hi) holds row l31's
+// codes k = 32 hi + [0, 32) of A, and the same of B's column l31, each with
+// that block's scale byte; it receives D[8 (r / 4) + 4 hi + r % 4][l31].
+// kByte picks the byte of the scale registers. 32x32x64 rather than 16x16x128:
+// with register operands the former reached 6.8 PFLOP/s on random codes at one
+// wave per SIMD, the latter 4.8 (8.1 and 5.1 on zeros).
+template <int kByteA, int kByteB>
+__device__ __forceinline__ f32x16 mfma_fp4(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
+    const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, kByteA, (int)sa, kByteB, (int)sb);
+}
+
+}  // namespace
+}  // namespace moe
