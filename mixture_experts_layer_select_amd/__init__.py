@@ -16,7 +16,7 @@ from ._lib import (BF16, F32, FP8_E4M3, MXFP4, SIGMOID, SOFTMAX, EXPORTS, MoEErr
                    moe_layer_few, moe_layer_few_workspace_size, moe_layer_fused_workspace_size, moe_permute,
                    moe_permute_workspace_size, moe_pre_norm, moe_quantize_mxfp4, moe_quantize_tokens, moe_route, moe_route_select,
                    moe_route_select_workspace_size)
-from .layer import LayerBuffers, MoELayer
+from .layer import LayerBuffers, MoELayer, quantize_mxfp4
 
 
 def build(verbose: bool = False) -> str:

@@ -34,16 +34,23 @@ class LayerBuffers:
     ws_perm: torch.Tensor
     ws_ffn: torch.Tensor
     ws_route: Optional[torch.Tensor] = None  # moe_route_select's workspace (large batches)
-    x_tok: Optional[torch.Tensor] = None  # fp8 token codes [T, H] (moe_quantize_tokens)
-    x_tok_scale: Optional[torch.Tensor] = None  # their scales [H/128, T]
+    # fp8 token codes [T, H] and scales [H/128, T] (moe_quantize_tokens), or MXFP4
+    # codes [T, H/2] and scale bytes [T, H/32] (moe_quantize_mxfp4)
+    x_tok: Optional[torch.Tensor] = None
+    x_tok_scale: Optional[torch.Tensor] = None
+    h: Optional[torch.Tensor] = None  # forward_block: the residual stream before the layer
+    n: Optional[torch.Tensor] = None  # forward_block: the layer's normed input
 
 
 class MoELayer:
     """Weights of one GPU's expert share (+ optional shared expert and router).
 
-    fmt: "f32", "bf16" or "fp8". Expert weights are device tensors
+    fmt: "f32", "bf16", "fp8" or "mxfp4". Expert weights are device tensors
     w13 [E_local, 2I, H], w2 [E_local, H, I] (uint8 e4m3 codes for fp8, with
-    w13_scale [E_local, 2I/128, H/128], w2_scale [E_local, H/128, I/128]).
+    w13_scale [E_local, 2I/128, H/128], w2_scale [E_local, H/128, I/128];
+    uint8 codes [E_local, 2I, H/2], [E_local, H, I/2] for mxfp4, with scale
+    bytes w13_scale [E_local, 2I, H/32], w2_scale [E_local, H, I/32], as
+    quantize_mxfp4 makes them).
     router: dict(w=[E, H], bias=[E] or None, scoring, renormalize) or None
     when the routing is handed in (expert-parallel share).
     """
@@ -54,7 +61,7 @@ class MoELayer:
         self.H, self.I, self.k = H, I, k
         self.E_local = w13.shape[0]
         self.expert_base = expert_base
-        self.dt = {"f32": L.F32, "bf16": L.BF16, "fp8": L.FP8_E4M3}[fmt]
+        self.dt = {"f32": L.F32, "bf16": L.BF16, "fp8": L.FP8_E4M3, "mxfp4": L.MXFP4}[fmt]
         self.act_dt = L.F32 if fmt == "f32" else L.BF16
         self.w13, self.w2, self.w13_scale, self.w2_scale = w13, w2, w13_scale, w2_scale
         self.shared = shared
@@ -71,11 +78,12 @@ class MoELayer:
     # instead of copying every routed row into x_perm; the result is the same
     # bit for bit. Without a shared group moe_permute quantises each routed row
     # straight from x in one pass, and gate/up on the contiguous rows is faster
-    # than the gathered reads.
+    # than the gathered reads. mxfp4 layers always read token rows (a row is a
+    # quarter of its bf16 copy).
     FP8_FROM_TOKENS = True
 
     def uses_tokens(self) -> bool:
-        return self.fmt == "fp8" and self.FP8_FROM_TOKENS and self.shared is not None
+        return self.fmt == "mxfp4" or (self.fmt == "fp8" and self.FP8_FROM_TOKENS and self.shared is not None)
 
     # Batches of at least this many tokens route through moe_route_select
     # (same ids and weights as moe_route; faster once the MFMA pass has a few
@@ -123,8 +131,12 @@ class MoELayer:
             ws_ffn=torch.empty(max(ws_f, 1), dtype=torch.uint8, device=device),
         )
         if self.uses_tokens():
-            b.x_tok = torch.empty((T, H), dtype=torch.uint8, device=device)
-            b.x_tok_scale = torch.empty((H // 128, T), **f32)
+            if self.fmt == "mxfp4":
+                b.x_tok = torch.empty((T, H // 2), dtype=torch.uint8, device=device)
+                b.x_tok_scale = torch.empty((T, H // 32), dtype=torch.uint8, device=device)
+            else:
+                b.x_tok = torch.empty((T, H), dtype=torch.uint8, device=device)
+                b.x_tok_scale = torch.empty((H // 128, T), **f32)
         if self.uses_route_select(T):
             b.ws_route = torch.empty(L.moe_route_select_workspace_size(T, E), dtype=torch.uint8,
                                      device=device)
@@ -151,7 +163,9 @@ class MoELayer:
                       self.act_dt, self.H, self.dt if self.fmt == "fp8" else self.act_dt, b.counts,
                       b.offsets, b.row_to_slot, b.slot_to_row, b.x_perm, b.x_perm_scale, b.ws_perm,
                       b.ws_perm.numel(), stream)
-        if self.uses_tokens():
+        if self.fmt == "mxfp4":
+            L.moe_quantize_mxfp4(x, self.act_dt, T, self.H, b.x_tok, b.x_tok_scale, stream)
+        elif self.uses_tokens():
             L.moe_quantize_tokens(x, self.act_dt, T, self.H, b.x_tok, b.x_tok_scale, stream)
 
     def gate_up(self, b: LayerBuffers, stream=None):
@@ -222,6 +236,42 @@ class MoELayer:
                           ws.numel(), stream)
         return b
 
+    # batches of mxfp4 experts up to this size go through moe_layer_few
+    FEW_MAX_T = 16
+
+    def uses_few(self, T: int) -> bool:
+        """Whether forward_few takes T tokens (moe_layer_few's limits)."""
+        E = self.E_local if self.router is None else self.router["w"].shape[0]
+        return (self.fmt == "mxfp4" and T <= self.FEW_MAX_T and self.k <= 8 and self.H <= 8192
+                and (self.router is None or E <= 256))
+
+    def few_workspace(self, T: int) -> torch.Tensor:
+        """forward_few's workspace for T tokens, zeroed once at allocation
+        (its first 256 bytes must start at zero; every call leaves them so)."""
+        key = ("few", T)
+        if key not in self._bufs:
+            n = L.moe_layer_few_workspace_size(self.weights, T, self._n_experts(), self.k)
+            self._bufs[key] = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.w13.device)
+        return self._bufs[key]
+
+    def _n_experts(self) -> int:
+        return self.router["w"].shape[0] if self.router is not None else max(self.expert_base + self.E_local, self.k)
+
+    def forward_few(self, x: torch.Tensor, topk_ids=None, topk_w=None, stream=None) -> LayerBuffers:
+        """The layer for at most 16 tokens with mxfp4 experts (moe_layer_few):
+        forward's ids and weights, and its output without the expert outputs'
+        rounding to bf16."""
+        self.check_inputs(x, topk_ids, topk_w)
+        T = x.shape[0]
+        b = self.buffers(T, x.device)
+        ws = self.few_workspace(T)
+        r = self.router if topk_ids is None else None
+        L.moe_layer_few(x, r["w"] if r else None, r.get("bias") if r else None, T, self._n_experts(), self.k,
+                        r["scoring"] if r else L.SIGMOID, r.get("renormalize", True) if r else True, self.weights,
+                        self.expert_base, b.topk_ids if r else topk_ids, b.topk_w if r else topk_w, b.out, ws,
+                        ws.numel(), stream)
+        return b
+
     def forward(self, x: torch.Tensor, topk_ids=None, topk_w=None, stream=None) -> LayerBuffers:
         """The whole layer. Routing comes from the router unless given."""
         self.check_inputs(x, topk_ids, topk_w)
@@ -232,3 +282,46 @@ class MoELayer:
         self.ffn(b, stream)
         self.combine(b, topk_w, stream)
         return b
+
+    def forward_block(self, x: torch.Tensor, delta=None, *, delta_scale: float = 1.0, gain=None, post_gain=None,
+                      eps: float = 1e-6, gate=None, alpha: float = 1.0, stream=None) -> LayerBuffers:
+        """The block around the layer: h = x + delta_scale * delta and its RMS
+        norm with `gain` (moe_pre_norm), the layer on the normed rows, then
+        h + alpha * gate * norm(combine) (moe_combine_norm; no post norm when
+        post_gain is None). gain, post_gain [H] fp32; gate [1, H] or [T, H] in
+        the layer's activation dtype. b.h holds h, b.n the normed rows, b.out
+        the block's output."""
+        self.check_inputs(x)
+        act, dev = x.dtype, self.w13.device
+        for t, name, dt in ((delta, "delta", act), (gain, "gain", torch.float32),
+                            (post_gain, "post_gain", torch.float32), (gate, "gate", act)):
+            L.expect(t, name, (dt,), dev)
+        T, H = x.shape
+        for t, name, shapes in ((delta, "delta", ((T, H),)), (gain, "gain", ((H,),)), (post_gain, "post_gain", ((H,),)),
+                                (gate, "gate", ((1, H), (T, H)))):
+            if t is not None and tuple(t.shape) not in shapes:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected one of {shapes}")
+        b = self.buffers(T, x.device)
+        if b.h is None:
+            b.h, b.n = torch.empty_like(x), torch.empty_like(x)
+        L.moe_pre_norm(x, delta, delta_scale, gain, eps, self.act_dt, T, H, b.h, b.n, stream)
+        self.route(b.n, b, stream)
+        self.permute(b.n, b, None, stream)
+        self.ffn(b, stream)
+        L.moe_combine_norm(b.y_perm, self.act_dt, b.slot_to_row, b.topk_w, T, self.k, H, b.offsets,
+                           self.E_local if self.shared is not None else -1, post_gain, eps, gate,
+                           1 if gate is None else gate.shape[0], alpha, b.h, b.out, self.act_dt, stream)
+        return b
+
+
+def quantize_mxfp4(x: torch.Tensor, stream=None):
+    """(codes [..., K/2], scale bytes [..., K/32]) of a bf16 or fp32 tensor
+    [..., K] (moe_quantize_mxfp4), as MoELayer takes expert weights."""
+    L.expect(x, "x", (torch.float32, torch.bfloat16))
+    K = x.shape[-1]
+    if K % 32:
+        raise ValueError(f"x: last dimension {K} is not a multiple of 32")
+    codes = torch.empty(x.shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(x.shape[:-1] + (K // 32,), dtype=torch.uint8, device=x.device)
+    L.moe_quantize_mxfp4(x, L.dtype_code(x), x.numel() // K, K, codes, scales, stream)
+    return codes, scales
