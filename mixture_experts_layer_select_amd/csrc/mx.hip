@@ -89,32 +89,31 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 // ============================================================================ grouped GEMMs
 // Items are (m-tile of at most 256 rows, n-block of 256 weight rows); one
 // workgroup of 4 waves per CU walks them (item_at's order, a contiguous slice
-// per XCD). Both operands of each K step of 128 arrive in a 4-stage LDS ring
-// by direct global->LDS loads, three steps ahead; the E8M0 scales of four
-// steps come in one 16-byte piece per row and sit in registers for them.
+// per XCD). Both operands of each K step of 256 (128 bytes of a row) arrive in
+// LDS by direct global->LDS loads; the E8M0 scales of two steps come in one
+// 16-byte piece per row and sit in registers for them. A load takes 8 rows of
+// 128 bytes: 16 rows of 64 bytes moved 14 TB/s from L2 where these move 23.
 //
 // Waves form a 2 x 2 grid: wave (wm, wn) owns the 32-token blocks 2j + wm of
 // the tile and 128 weight rows, as 4 x NX blocks of 32x32 accumulators, NX =
-// 1, 2 or 4 by the tile's height (64, 128, 256 rows): a short tile loads only
-// its own rows, so a group of up to 256 rows reads its weights from HBM once
-// and little else.
+// 1 to 4 by the tile's height (64 rows each): a short tile loads only its own
+// rows, so a group of up to 256 rows reads its weights from HBM once and
+// little else. LDS holds two steps of a tile of more than 128 rows (64 KB
+// each), or three of a shorter one, which HBM bounds (48 KB each).
 //   SwiGLU: LDS rows q < 128 are gate rows nb*128 + q, q >= 128 the up rows I +
 //     nb*128 + q - 128; wave wn owns gate q = 64wn + [0, 64) (s = 0, 1) and
 //     the up rows 128 + the same (s = 2, 3).
 //   Down: q -> w2 row nb*256 + q; wave wn owns q = 128wn + 32s + [0, 32).
-// LDS rows are 64 bytes; chunk c of row q sits at chunk c ^ mx_swz(q), which
-// spreads the 16 rows that a quarter of a wave reads over all 64 banks.
+// LDS rows are 128 bytes; chunk c of row q sits at chunk c ^ swz(q), which
+// spreads the rows that 16 (and 8) consecutive lanes read over all banks.
 constexpr int kMxTM = 256;     // tokens per tile
 constexpr int kMxTN = 256;     // weight rows per tile
 constexpr int kMxThreads = 256;
-constexpr int kMxStepB = 64;   // bytes of a row per K step of 128
+constexpr int kMxStepB = 128;  // bytes of a row per K step of 256
 constexpr int kMxPanel = 4;    // m-tiles per item panel
+constexpr int kKB = 1024;
 
-struct MxStage {
-    uint8_t w[kMxTN * kMxStepB];  // 16 KB
-    uint8_t x[kMxTM * kMxStepB];  // 16 KB
-};
-struct MxScales {  // four K steps
+struct MxScales {  // two K steps
     uint8_t w[kMxTN * 16];
     uint8_t x[kMxTM * 16];
 };
@@ -124,8 +123,8 @@ struct MxScales {  // four K steps
 // it writes 16 neighbouring outputs
 __device__ __forceinline__ int mx_row_of(int rho) { return 16 * ((rho >> 2) & 1) + 4 * (rho >> 3) + (rho & 3); }
 // chunk swizzles: weight rows are read in mx_row_of's order, tokens in rows'
-__device__ __forceinline__ int mx_swz_w(int q) { return (((q >> 2) ^ (q >> 1)) & 1) | ((q >> 4) & 1) << 1; }
-__device__ __forceinline__ int mx_swz_x(int q) { return (((q >> 1) ^ (q >> 3)) & 1) | ((q >> 2) & 1) << 1; }
+__device__ __forceinline__ int mx_swz_w(int q) { return ((q & 3) ^ ((q >> 2) & 1)) | ((q >> 4) & 1) << 2; }
+__device__ __forceinline__ int mx_swz_x(int q) { return (q & 7) ^ ((q >> 3) & 1); }
 
 struct MxGemm {
     const uint8_t* x;         // activation codes, rows of K/2 bytes
@@ -140,11 +139,15 @@ struct MxGemm {
 
 template <bool kSwiGLU, bool kGather>
 __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
-    // one object per stage: the compiler tells the one being filled from the one being read
-    __shared__ __attribute__((aligned(1024))) MxStage st0;
-    __shared__ __attribute__((aligned(1024))) MxStage st1;
-    __shared__ __attribute__((aligned(1024))) MxStage st2;
-    __shared__ __attribute__((aligned(1024))) MxStage st3;
+    // The stages are whole objects, or fixed parts of them, so that the compiler tells the ones being filled
+    // from the one being read. Weights (32 KB) and tokens (16 KB for 128 rows) of a stage:
+    //   two stages:   w o0, tokens 0-127 o0 + 32 KB, 128-255 o1 | w o2, tokens o3
+    //   three stages: w o0, tokens o0 + 32 KB | w o2, tokens o1 | w o3, tokens o4
+    __shared__ __attribute__((aligned(1024))) uint8_t o0[48 * kKB];
+    __shared__ __attribute__((aligned(1024))) uint8_t o1[16 * kKB];
+    __shared__ __attribute__((aligned(1024))) uint8_t o2[32 * kKB];
+    __shared__ __attribute__((aligned(1024))) uint8_t o3[32 * kKB];
+    __shared__ __attribute__((aligned(1024))) uint8_t o4[16 * kKB];
     __shared__ __attribute__((aligned(1024))) MxScales sc;
     __shared__ TileMap tm;
     const int lane = threadIdx.x & 63;
@@ -152,7 +155,8 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     const int wm = wave & 1, wn = wave >> 1;
     const int l31 = lane & 31, hi = lane >> 5;
     const int K = p.K, kb = K / kMxBlock, rowb = K / 2;
-    const int nk = K / 128;
+    const int nk = (K + 255) / 256;
+    const bool half = K % 256 != 0;  // the last step holds 128 of K
     const int I = p.Nw / 2;  // SwiGLU: intermediate size
     const int n_items = build_tile_map(tm, p.offsets, p.n_groups, p.max_rows, kMxTM) * p.NB;
     const int xcd = blockIdx.x & 7;
@@ -160,11 +164,12 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     const int i_lo = (int)((long)n_items * xcd / 8);
     const int i_hi = (int)((long)n_items * (xcd + 1) / 8);
 
-    // fragment offsets in a stage: weight tile s at off + q0(s) * 64, token block j at off + j * 4096
+    // fragment offsets in a stage: weight tile s at offa + q0(s) * 128, token block j at offb + j * 8192;
+    // MFMA h of a step takes chunk 2h + hi of the row
     const int rw = mx_row_of(l31);
-    int offa[2], offb[2];
+    int offa[4], offb[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 4; ++h) {
         offa[h] = rw * kMxStepB + ((2 * h + hi) ^ mx_swz_w(rw)) * 16;
         offb[h] = (32 * wm + l31) * kMxStepB + ((2 * h + hi) ^ mx_swz_x(l31)) * 16;
     }
@@ -194,16 +199,16 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
             const int t = slot < p.src.S ? slot / p.src.k : slot - p.src.S;
             return (uint32_t)max(0, min(t, p.src.rows - 1));
         };
-        // piece 4i + wave of either operand holds LDS rows 16 (4i + wave) + [0, 16), four lanes a row. Piece
+        // piece 4i + wave of either operand holds LDS rows 8 (4i + wave) + [0, 8), eight lanes a row. Piece
         // i's weight rows lie a uniform distance behind piece 0's.
-        const int pr = 16 * wave + (lane >> 2);
-        const uint32_t woff = (uint32_t)((kSwiGLU ? nb * 128 : nb * 256) + pr) * rowb + ((lane & 3) ^ mx_swz_w(pr)) * 16;
+        const int pr = 8 * wave + (lane >> 3);
+        const uint32_t woff = (uint32_t)((kSwiGLU ? nb * 128 : nb * 256) + pr) * rowb + ((lane & 7) ^ mx_swz_w(pr)) * 16;
         auto wdist = [&](int i) -> uint32_t {
-            return (uint32_t)(kSwiGLU ? (i < 2 ? 64 * i : I + 64 * (i - 2)) : 64 * i) * rowb;
+            return (uint32_t)(kSwiGLU ? (i < 4 ? 32 * i : I + 32 * (i - 4)) : 32 * i) * rowb;
         };
-        uint32_t xoff[4];
+        uint32_t xoff[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xoff[i] = src_row(64 * i + pr) * rowb + ((lane & 3) ^ mx_swz_x(pr)) * 16;
+        for (int i = 0; i < 8; ++i) xoff[i] = src_row(32 * i + pr) * rowb + ((lane & 7) ^ mx_swz_x(pr)) * 16;
         // scales: wave w brings rows 64w + lane of both operands
         const uint32_t wsoff =
             (uint32_t)(kSwiGLU ? (wave >> 1) * I + nb * 128 + 64 * (wave & 1) : nb * 256 + 64 * wave) * kb + lane * kb;
@@ -211,15 +216,17 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
 
         auto run = [&](auto nx_c) {
             constexpr int NX = decltype(nx_c)::value;
-            auto issue = [&](int kc, MxStage& S) {  // steps past the end bring the last one again, unused
-                const uint32_t ko = (uint32_t)min(kc, nk - 1) * kMxStepB;
+            auto issue = [&](int kc, uint8_t* W, uint8_t* X01, uint8_t* X23) {
+                kc = min(kc, nk - 1);  // steps past the end bring the last one again, unused
+                const uint32_t ko = (uint32_t)kc * kMxStepB;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) lds_buf16(w_d, woff, wdist(i) + ko, &S.w[(4 * i + wave) * 1024]);
+                for (int i = 0; i < 8; ++i) lds_buf16(w_d, woff, wdist(i) + ko, W + (4 * i + wave) * 1024);
 #pragma unroll
-                for (int i = 0; i < NX; ++i) lds_buf16(x_d, xoff[i], ko, &S.x[(4 * i + wave) * 1024]);
+                for (int i = 0; i < 2 * NX; ++i)
+                    lds_buf16(x_d, xoff[i], ko, i < 4 ? X01 + (4 * i + wave) * 1024 : X23 + (4 * (i - 4) + wave) * 1024);
             };
             auto issue_scales = [&](int kc) {
-                const uint32_t so = (uint32_t)min(kc, nk - 1) / 4 * 16;
+                const uint32_t so = (uint32_t)min(kc, nk - 1) / 2 * 16;
                 lds_buf16(ws_d, wsoff, so, &sc.w[wave * 1024]);
                 lds_buf16(xs_d, xsoff, so, &sc.x[wave * 1024]);
             };
@@ -232,60 +239,100 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 for (int j = 0; j < NX; ++j)
                     sx[j] = *reinterpret_cast<const u32x4*>(&sc.x[(64 * j + 32 * wm + l31) * 16]);
             };
-            auto compute = [&](const MxStage& S, auto sub_c) {
+            // step kc from a stage; sub: its two dwords of the group's scales
+            auto compute = [&](int kc, auto sub_c, const uint8_t* W, const uint8_t* X01, const uint8_t* X23) {
                 constexpr int sub = decltype(sub_c)::value;
-                u32x4 a[4][2];
-                uint32_t sa[4];
+                auto part = [&](auto u_c) {  // 128 of K: MFMAs h = 2u, 2u + 1
+                    constexpr int u = decltype(u_c)::value;
+                    u32x4 a[4][2];
+                    uint32_t sa[4];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    sa[s] = sw[s][sub] >> (8 * hi);
+                    for (int s = 0; s < 4; ++s) {
+                        sa[s] = sw[s][2 * sub + u] >> (8 * hi);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        a[s][h] = *reinterpret_cast<const u32x4*>(&S.w[q0(s) * kMxStepB + offa[h]]);
-                }
+                        for (int h = 0; h < 2; ++h)
+                            a[s][h] = *reinterpret_cast<const u32x4*>(W + q0(s) * kMxStepB + offa[2 * u + h]);
+                    }
 #pragma unroll
-                for (int j = 0; j < NX; ++j) {
-                    const u32x4 b0 = *reinterpret_cast<const u32x4*>(&S.x[j * 4096 + offb[0]]);
-                    const u32x4 b1 = *reinterpret_cast<const u32x4*>(&S.x[j * 4096 + offb[1]]);
-                    const uint32_t sb = sx[j][sub] >> (8 * hi);
+                    for (int j = 0; j < NX; ++j) {
+                        const uint8_t* X = j < 2 ? X01 + j * 8192 : X23 + (j - 2) * 8192;
+                        const u32x4 b0 = *reinterpret_cast<const u32x4*>(X + offb[2 * u]);
+                        const u32x4 b1 = *reinterpret_cast<const u32x4*>(X + offb[2 * u + 1]);
+                        const uint32_t sb = sx[j][2 * sub + u] >> (8 * hi);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) acc[s][j] = mfma_fp4<0, 0>(a[s][0], b0, acc[s][j], sa[s], sb);
+                        for (int s = 0; s < 4; ++s) acc[s][j] = mfma_fp4<0, 0>(a[s][0], b0, acc[s][j], sa[s], sb);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) acc[s][j] = mfma_fp4<2, 2>(a[s][1], b1, acc[s][j], sa[s], sb);
-                }
+                        for (int s = 0; s < 4; ++s) acc[s][j] = mfma_fp4<2, 2>(a[s][1], b1, acc[s][j], sa[s], sb);
+                    }
+                };
+                part(std::integral_constant<int, 0>{});
+                if (!half || kc + 1 < nk) part(std::integral_constant<int, 1>{});
             };
             using C0 = std::integral_constant<int, 0>;
             using C1 = std::integral_constant<int, 1>;
-            using C2 = std::integral_constant<int, 2>;
-            using C3 = std::integral_constant<int, 3>;
-            // loads of a step: 4 + NX, and two scale pieces ahead of every fourth
-            constexpr int L = 4 + NX;
+            // A group's scales are issued in its last step but one, after the barrier behind which every wave
+            // holds the previous group's, and ahead of that step's own loads, so each wait below covers them.
             issue_scales(0);
-            issue(0, st0);
-            issue(1, st1);
-            issue(2, st2);
-            for (int j = 0; j < nk; j += 4) {
-                wait_vmcnt<2 * L>();  // step j and its scales have landed; j + 1 and j + 2 may fly
-                barrier_only();
-                issue(j + 3, st3);
-                read_scales();
-                compute(st0, C0{});
-                wait_vmcnt<2 * L>();
-                barrier_only();       // every wave holds the group's scales
-                issue_scales(j + 4);
-                issue(j + 4, st0);
-                if (j + 1 < nk) compute(st1, C1{});
-                wait_vmcnt<2 * L + 2>();
-                barrier_only();
-                issue(j + 5, st1);
-                if (j + 2 < nk) compute(st2, C2{});
-                wait_vmcnt<2 * L + 2>();
-                barrier_only();
-                issue(j + 6, st2);
-                if (j + 3 < nk) compute(st3, C3{});
+            if constexpr (NX > 2) {
+                auto S0 = [&](auto f) { f(o0, o0 + 32 * kKB, o1); };
+                auto S1 = [&](auto f) { f(o2, o3, o3 + 16 * kKB); };
+                auto load = [&](int kc, auto at) {
+                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) { issue(kc, W, X01, X23); });
+                };
+                auto work = [&](int kc, auto sub, auto at) {
+                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) { compute(kc, sub, W, X01, X23); });
+                };
+                load(0, S0);
+                for (int j = 0; j < nk; j += 2) {
+                    wait_vmcnt<0>();
+                    barrier_only();
+                    load(j + 1, S1);
+                    read_scales();
+                    work(j, C0{}, S0);
+                    wait_vmcnt<0>();
+                    barrier_only();
+                    issue_scales(j + 2);
+                    load(j + 2, S0);
+                    if (j + 1 < nk) work(j + 1, C1{}, S1);
+                }
+            } else {
+                constexpr int L = 8 + 2 * NX;  // a step's loads
+                auto S0 = [&](auto f) { f(o0, o0 + 32 * kKB); };
+                auto S1 = [&](auto f) { f(o2, o1); };
+                auto S2 = [&](auto f) { f(o3, o4); };
+                auto load = [&](int kc, auto at) { at([&](uint8_t* W, uint8_t* X) { issue(kc, W, X, X); }); };
+                auto work = [&](int kc, auto sub, auto at) {
+                    at([&](uint8_t* W, uint8_t* X) { compute(kc, sub, W, X, X); });
+                };
+                auto even = [&](int j, auto cur, auto next) {
+                    wait_vmcnt<L>();  // step j and its scales have landed; j + 1 may fly
+                    barrier_only();
+                    load(j + 2, next);
+                    if (j < nk) {
+                        read_scales();
+                        work(j, C0{}, cur);
+                    }
+                };
+                auto odd = [&](int j, auto cur, auto next) {
+                    wait_vmcnt<L>();
+                    barrier_only();
+                    issue_scales(j + 1);
+                    load(j + 2, next);
+                    if (j < nk) work(j, C1{}, cur);
+                };
+                load(0, S0);
+                load(1, S1);
+                for (int j = 0; j < nk; j += 6) {
+                    even(j, S0, S2);
+                    odd(j + 1, S1, S0);
+                    even(j + 2, S2, S1);
+                    odd(j + 3, S0, S2);
+                    even(j + 4, S1, S0);
+                    odd(j + 5, S2, S1);
+                }
             }
             wait_vmcnt<0>();
-            barrier_only();  // the ring is filled again by the next item
+            barrier_only();  // the stages are filled again by the next item
 
 #pragma unroll
             for (int j = 0; j < NX; ++j) {
@@ -298,7 +345,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                         uint32_t mx = 0;
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
-                            v[r] = silu_mul(acc[s][j][r], acc[s + 2][j][r]);
+                            v[r] = mx_silu_mul(acc[s][j][r], acc[s + 2][j][r]);
                             mx = max(mx, abs_bits(v[r]));
                         }
                         mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
@@ -319,8 +366,8 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                         for (int q = 0; q < 2; ++q) {
                             const f32x16& a = acc[s][j];
                             *reinterpret_cast<u32x4*>(y + 32 * s + 8 * q) = u32x4{
-                                pack_bf16x2(a[8 * q], a[8 * q + 1]), pack_bf16x2(a[8 * q + 2], a[8 * q + 3]),
-                                pack_bf16x2(a[8 * q + 4], a[8 * q + 5]), pack_bf16x2(a[8 * q + 6], a[8 * q + 7])};
+                                cvt_bf16x2(a[8 * q], a[8 * q + 1]), cvt_bf16x2(a[8 * q + 2], a[8 * q + 3]),
+                                cvt_bf16x2(a[8 * q + 4], a[8 * q + 5]), cvt_bf16x2(a[8 * q + 6], a[8 * q + 7])};
                         }
                 }
             }
@@ -329,6 +376,8 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
             run(std::integral_constant<int, 1>{});
         else if (tile.rows <= 128)
             run(std::integral_constant<int, 2>{});
+        else if (tile.rows <= 192)
+            run(std::integral_constant<int, 3>{});
         else
             run(std::integral_constant<int, 4>{});
     }
