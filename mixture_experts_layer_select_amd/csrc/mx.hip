@@ -88,27 +88,28 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 
 // ============================================================================ grouped GEMMs
 // Items are (m-tile of at most 256 rows, n-block of 256 weight rows); one
-// workgroup of 4 waves per CU walks them (item_at's order, a contiguous slice
+// workgroup of 8 waves per CU walks them (item_at's order, a contiguous slice
 // per XCD). Both operands of each K step of 256 (128 bytes of a row) arrive in
 // LDS by direct global->LDS loads; the E8M0 scales of two steps come in one
 // 16-byte piece per row and sit in registers for them. A load takes 8 rows of
 // 128 bytes: 16 rows of 64 bytes moved 14 TB/s from L2 where these move 23.
+// An item's first loads are issued before the previous item's epilogue.
 //
-// Waves form a 2 x 2 grid: wave (wm, wn) owns the 32-token blocks 2j + wm of
-// the tile and 128 weight rows, as 4 x NX blocks of 32x32 accumulators, NX =
+// Waves form a 2 x 4 grid: wave (wm, wn) owns the 32-token blocks 2j + wm of
+// the tile and 64 weight rows, as 2 x NX blocks of 32x32 accumulators, NX =
 // 1 to 4 by the tile's height (64 rows each): a short tile loads only its own
 // rows, so a group of up to 256 rows reads its weights from HBM once and
 // little else. LDS holds two steps of a tile of more than 128 rows (64 KB
 // each), or three of a shorter one, which HBM bounds (48 KB each).
 //   SwiGLU: LDS rows q < 128 are gate rows nb*128 + q, q >= 128 the up rows I +
-//     nb*128 + q - 128; wave wn owns gate q = 64wn + [0, 64) (s = 0, 1) and
-//     the up rows 128 + the same (s = 2, 3).
-//   Down: q -> w2 row nb*256 + q; wave wn owns q = 128wn + 32s + [0, 32).
+//     nb*128 + q - 128; wave wn owns gate q = 32wn + [0, 32) (s = 0) and the up
+//     rows 128 + the same (s = 1).
+//   Down: q -> w2 row nb*256 + q; wave wn owns q = 64wn + 32s + [0, 32).
 // LDS rows are 128 bytes; chunk c of row q sits at chunk c ^ swz(q), which
 // spreads the rows that 16 (and 8) consecutive lanes read over all banks.
 constexpr int kMxTM = 256;     // tokens per tile
 constexpr int kMxTN = 256;     // weight rows per tile
-constexpr int kMxThreads = 256;
+constexpr int kMxThreads = 512;
 constexpr int kMxStepB = 128;  // bytes of a row per K step of 256
 constexpr int kMxPanel = 4;    // m-tiles per item panel
 constexpr int kKB = 1024;
@@ -158,7 +159,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     const int nk = (K + 255) / 256;
     const bool half = K % 256 != 0;  // the last step holds 128 of K
     const int I = p.Nw / 2;  // SwiGLU: intermediate size
-    const int n_items = build_tile_map(tm, p.offsets, p.n_groups, p.max_rows, kMxTM) * p.NB;
+    // uniform, so that the item loop and the descriptors it carries stay scalar
+    const int n_items =
+        __builtin_amdgcn_readfirstlane(build_tile_map(tm, p.offsets, p.n_groups, p.max_rows, kMxTM)) * p.NB;
     const int xcd = blockIdx.x & 7;
     const int per_xcd = gridDim.x >> 3;
     const int i_lo = (int)((long)n_items * xcd / 8);
@@ -173,68 +176,111 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
         offa[h] = rw * kMxStepB + ((2 * h + hi) ^ mx_swz_w(rw)) * 16;
         offb[h] = (32 * wm + l31) * kMxStepB + ((2 * h + hi) ^ mx_swz_x(l31)) * 16;
     }
-    auto q0 = [&](int s) { return kSwiGLU ? 128 * (s >> 1) + 64 * wn + 32 * (s & 1) : 128 * wn + 32 * s; };
+    auto q0 = [&](int s) { return kSwiGLU ? 128 * s + 32 * wn : 64 * wn + 32 * s; };
+    // piece 8i + wave of either operand holds LDS rows 64i + pr, eight lanes a row
+    const int pr = 8 * wave + (lane >> 3);
+    // a piece's weight rows lie a uniform distance behind piece 0's
+    auto wdist = [&](int i) -> uint32_t {
+        return (uint32_t)(kSwiGLU ? (i < 2 ? 64 * i : I + 64 * (i - 2)) : 64 * i) * rowb;
+    };
 
-    for (int item = i_lo + (int)(blockIdx.x >> 3); item < i_hi; item += per_xcd) {
+    // what an item's loads go by: its tile and this lane's offsets, and the descriptors, which are made anew
+    // where they are used (carried through the item loop they would be kept in vector registers)
+    struct Item {
+        MTile tile;
+        int nb;
+        uint32_t woff, xoff[4], soff;
+    };
+    struct Desc {
+        __amdgpu_buffer_rsrc_t w, x, s;
+    };
+    auto desc_of = [&](const MTile& t) {
+        const int group = __builtin_amdgcn_readfirstlane(t.group), row0 = __builtin_amdgcn_readfirstlane(t.row0),
+                  rows = __builtin_amdgcn_readfirstlane(t.rows);
+        const bool routed = group < p.n_routed;
+        Desc d;
+        d.w = buffer_rsrc(routed ? p.w + (size_t)group * p.Nw * rowb : p.wsh, clamp_bytes((size_t)p.Nw * rowb));
+        d.x = kGather ? buffer_rsrc(p.x, clamp_bytes((size_t)p.src.rows * rowb))
+                      : buffer_rsrc(p.x + (size_t)row0 * rowb, clamp_bytes((size_t)rows * rowb));
+        // scales: waves 0..3 bring the weights', rows 64w + lane, waves 4..7 the tokens'
+        if (wave < 4)
+            d.s = buffer_rsrc(routed ? p.ws + (size_t)group * p.Nw * kb : p.wsh_s, clamp_bytes((size_t)p.Nw * kb));
+        else
+            d.s = kGather ? buffer_rsrc(p.xs, clamp_bytes((size_t)p.src.rows * kb))
+                          : buffer_rsrc(p.xs + (size_t)row0 * kb, clamp_bytes((size_t)rows * kb));
+        return d;
+    };
+    auto item_of = [&](int item) {
+        Item c;
         int nb_v;
-        const MTile tile_v = item_at(tm, p.offsets, p.n_groups, p.max_rows, item, p.NB, kMxTM, nb_v, kMxPanel);
-        const int nb = __builtin_amdgcn_readfirstlane(nb_v);
-        const MTile tile{__builtin_amdgcn_readfirstlane(tile_v.group), __builtin_amdgcn_readfirstlane(tile_v.row0),
-                         __builtin_amdgcn_readfirstlane(tile_v.rows)};
-        const bool routed = tile.group < p.n_routed;
-        const __amdgpu_buffer_rsrc_t w_d = buffer_rsrc(
-            routed ? p.w + (size_t)tile.group * p.Nw * rowb : p.wsh, clamp_bytes((size_t)p.Nw * rowb));
-        const __amdgpu_buffer_rsrc_t ws_d =
-            buffer_rsrc(routed ? p.ws + (size_t)tile.group * p.Nw * kb : p.wsh_s, clamp_bytes((size_t)p.Nw * kb));
-        const __amdgpu_buffer_rsrc_t x_d =
-            kGather ? buffer_rsrc(p.x, clamp_bytes((size_t)p.src.rows * rowb))
-                    : buffer_rsrc(p.x + (size_t)tile.row0 * rowb, clamp_bytes((size_t)tile.rows * rowb));
-        const __amdgpu_buffer_rsrc_t xs_d =
-            kGather ? buffer_rsrc(p.xs, clamp_bytes((size_t)p.src.rows * kb))
-                    : buffer_rsrc(p.xs + (size_t)tile.row0 * kb, clamp_bytes((size_t)tile.rows * kb));
+        const MTile t = item_at(tm, p.offsets, p.n_groups, p.max_rows, item, p.NB, kMxTM, nb_v, kMxPanel);
+        c.nb = __builtin_amdgcn_readfirstlane(nb_v);
+        c.tile = MTile{__builtin_amdgcn_readfirstlane(t.group), __builtin_amdgcn_readfirstlane(t.row0),
+                       __builtin_amdgcn_readfirstlane(t.rows)};
         auto src_row = [&](int r) -> uint32_t {  // the tile's row r, clamped to it
-            r = min(r, tile.rows - 1);
+            r = min(r, c.tile.rows - 1);
             if (!kGather) return (uint32_t)r;
-            const int slot = p.src.row_slot[tile.row0 + r];
-            const int t = slot < p.src.S ? slot / p.src.k : slot - p.src.S;
-            return (uint32_t)max(0, min(t, p.src.rows - 1));
+            const int slot = p.src.row_slot[c.tile.row0 + r];
+            const int tk = slot < p.src.S ? slot / p.src.k : slot - p.src.S;
+            return (uint32_t)max(0, min(tk, p.src.rows - 1));
         };
-        // piece 4i + wave of either operand holds LDS rows 8 (4i + wave) + [0, 8), eight lanes a row. Piece
-        // i's weight rows lie a uniform distance behind piece 0's.
-        const int pr = 8 * wave + (lane >> 3);
-        const uint32_t woff = (uint32_t)((kSwiGLU ? nb * 128 : nb * 256) + pr) * rowb + ((lane & 7) ^ mx_swz_w(pr)) * 16;
-        auto wdist = [&](int i) -> uint32_t {
-            return (uint32_t)(kSwiGLU ? (i < 4 ? 32 * i : I + 32 * (i - 4)) : 32 * i) * rowb;
-        };
-        uint32_t xoff[8];
+        c.woff = (uint32_t)((kSwiGLU ? c.nb * 128 : c.nb * 256) + pr) * rowb + ((lane & 7) ^ mx_swz_w(pr)) * 16;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xoff[i] = src_row(32 * i + pr) * rowb + ((lane & 7) ^ mx_swz_x(pr)) * 16;
-        // scales: wave w brings rows 64w + lane of both operands
-        const uint32_t wsoff =
-            (uint32_t)(kSwiGLU ? (wave >> 1) * I + nb * 128 + 64 * (wave & 1) : nb * 256 + 64 * wave) * kb + lane * kb;
-        const uint32_t xsoff = src_row(64 * wave + lane) * kb;
+        for (int i = 0; i < 4; ++i) c.xoff[i] = src_row(64 * i + pr) * rowb + ((lane & 7) ^ mx_swz_x(pr)) * 16;
+        const int w4 = wave & 3;
+        c.soff = wave < 4
+                     ? (uint32_t)((kSwiGLU ? (w4 >> 1) * I + c.nb * 128 + 64 * (w4 & 1) : c.nb * 256 + 64 * w4) + lane) * kb
+                     : src_row(64 * w4 + lane) * kb;
+        return c;
+    };
+    auto issue = [&](const Item& c, const Desc& d, auto nx_c, int kc, uint8_t* W, uint8_t* X01, uint8_t* X23) {
+        constexpr int NX = decltype(nx_c)::value;
+        const uint32_t ko = (uint32_t)min(kc, nk - 1) * kMxStepB;  // steps past the end bring the last one again, unused
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds_buf16(d.w, c.woff, wdist(i) + ko, W + (8 * i + wave) * 1024);
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+            lds_buf16(d.x, c.xoff[i], ko, i < 2 ? X01 + (8 * i + wave) * 1024 : X23 + (8 * (i - 2) + wave) * 1024);
+    };
+    auto issue_scales = [&](const Item& c, const Desc& d, int kc) {
+        lds_buf16(d.s, c.soff, (uint32_t)min(kc, nk - 1) / 2 * 16, (wave < 4 ? sc.w : sc.x) + (wave & 3) * 1024);
+    };
+    auto with_nx = [&](int rows, auto f) {
+        if (rows <= 64) f(std::integral_constant<int, 1>{});
+        else if (rows <= 128) f(std::integral_constant<int, 2>{});
+        else if (rows <= 192) f(std::integral_constant<int, 3>{});
+        else f(std::integral_constant<int, 4>{});
+    };
+    auto first_loads = [&](const Item& c) {
+        const Desc d = desc_of(c.tile);
+        issue_scales(c, d, 0);
+        with_nx(__builtin_amdgcn_readfirstlane(c.tile.rows), [&](auto nx_c) {
+            if constexpr (decltype(nx_c)::value > 2) {
+                issue(c, d, nx_c, 0, o0, o0 + 32 * kKB, o1);
+            } else {
+                issue(c, d, nx_c, 0, o0, o0 + 32 * kKB, nullptr);
+                issue(c, d, nx_c, 1, o2, o1, nullptr);
+            }
+        });
+    };
 
+    int item = i_lo + (int)(blockIdx.x >> 3);
+    if (item >= i_hi) return;
+    Item cur = item_of(item);
+    first_loads(cur);
+    for (;;) {
+        const bool more = item + per_xcd < i_hi;
+        const MTile tile{__builtin_amdgcn_readfirstlane(cur.tile.group), __builtin_amdgcn_readfirstlane(cur.tile.row0),
+                         __builtin_amdgcn_readfirstlane(cur.tile.rows)};
+        const int nb = __builtin_amdgcn_readfirstlane(cur.nb);
+        const Desc d = desc_of(tile);
         auto run = [&](auto nx_c) {
             constexpr int NX = decltype(nx_c)::value;
-            auto issue = [&](int kc, uint8_t* W, uint8_t* X01, uint8_t* X23) {
-                kc = min(kc, nk - 1);  // steps past the end bring the last one again, unused
-                const uint32_t ko = (uint32_t)kc * kMxStepB;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) lds_buf16(w_d, woff, wdist(i) + ko, W + (4 * i + wave) * 1024);
-#pragma unroll
-                for (int i = 0; i < 2 * NX; ++i)
-                    lds_buf16(x_d, xoff[i], ko, i < 4 ? X01 + (4 * i + wave) * 1024 : X23 + (4 * (i - 4) + wave) * 1024);
-            };
-            auto issue_scales = [&](int kc) {
-                const uint32_t so = (uint32_t)min(kc, nk - 1) / 2 * 16;
-                lds_buf16(ws_d, wsoff, so, &sc.w[wave * 1024]);
-                lds_buf16(xs_d, xsoff, so, &sc.x[wave * 1024]);
-            };
-            f32x16 acc[4][NX] = {};
-            u32x4 sw[4], sx[NX];
+            f32x16 acc[2][NX] = {};
+            u32x4 sw[2], sx[NX];
             auto read_scales = [&]() {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) sw[s] = *reinterpret_cast<const u32x4*>(&sc.w[(q0(s) + rw) * 16]);
+                for (int s = 0; s < 2; ++s) sw[s] = *reinterpret_cast<const u32x4*>(&sc.w[(q0(s) + rw) * 16]);
 #pragma unroll
                 for (int j = 0; j < NX; ++j)
                     sx[j] = *reinterpret_cast<const u32x4*>(&sc.x[(64 * j + 32 * wm + l31) * 16]);
@@ -244,10 +290,10 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 constexpr int sub = decltype(sub_c)::value;
                 auto part = [&](auto u_c) {  // 128 of K: MFMAs h = 2u, 2u + 1
                     constexpr int u = decltype(u_c)::value;
-                    u32x4 a[4][2];
-                    uint32_t sa[4];
+                    u32x4 a[2][2];
+                    uint32_t sa[2];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int s = 0; s < 2; ++s) {
                         sa[s] = sw[s][2 * sub + u] >> (8 * hi);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
@@ -260,9 +306,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                         const u32x4 b1 = *reinterpret_cast<const u32x4*>(X + offb[2 * u + 1]);
                         const uint32_t sb = sx[j][2 * sub + u] >> (8 * hi);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) acc[s][j] = mfma_fp4<0, 0>(a[s][0], b0, acc[s][j], sa[s], sb);
+                        for (int s = 0; s < 2; ++s) acc[s][j] = mfma_fp4<0, 0>(a[s][0], b0, acc[s][j], sa[s], sb);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) acc[s][j] = mfma_fp4<2, 2>(a[s][1], b1, acc[s][j], sa[s], sb);
+                        for (int s = 0; s < 2; ++s) acc[s][j] = mfma_fp4<2, 2>(a[s][1], b1, acc[s][j], sa[s], sb);
                     }
                 };
                 part(std::integral_constant<int, 0>{});
@@ -272,17 +318,15 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
             using C1 = std::integral_constant<int, 1>;
             // A group's scales are issued in its last step but one, after the barrier behind which every wave
             // holds the previous group's, and ahead of that step's own loads, so each wait below covers them.
-            issue_scales(0);
             if constexpr (NX > 2) {
                 auto S0 = [&](auto f) { f(o0, o0 + 32 * kKB, o1); };
                 auto S1 = [&](auto f) { f(o2, o3, o3 + 16 * kKB); };
                 auto load = [&](int kc, auto at) {
-                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) { issue(kc, W, X01, X23); });
+                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) { issue(cur, d, nx_c, kc, W, X01, X23); });
                 };
                 auto work = [&](int kc, auto sub, auto at) {
                     at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) { compute(kc, sub, W, X01, X23); });
                 };
-                load(0, S0);
                 for (int j = 0; j < nk; j += 2) {
                     wait_vmcnt<0>();
                     barrier_only();
@@ -291,37 +335,37 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                     work(j, C0{}, S0);
                     wait_vmcnt<0>();
                     barrier_only();
-                    issue_scales(j + 2);
+                    issue_scales(cur, d, j + 2);
                     load(j + 2, S0);
                     if (j + 1 < nk) work(j + 1, C1{}, S1);
                 }
             } else {
-                constexpr int L = 8 + 2 * NX;  // a step's loads
+                constexpr int L = 4 + NX;  // a step's loads
                 auto S0 = [&](auto f) { f(o0, o0 + 32 * kKB); };
                 auto S1 = [&](auto f) { f(o2, o1); };
                 auto S2 = [&](auto f) { f(o3, o4); };
-                auto load = [&](int kc, auto at) { at([&](uint8_t* W, uint8_t* X) { issue(kc, W, X, X); }); };
-                auto work = [&](int kc, auto sub, auto at) {
-                    at([&](uint8_t* W, uint8_t* X) { compute(kc, sub, W, X, X); });
+                auto load = [&](int kc, auto at) {
+                    at([&](uint8_t* W, uint8_t* X) { issue(cur, d, nx_c, kc, W, X, nullptr); });
                 };
-                auto even = [&](int j, auto cur, auto next) {
+                auto work = [&](int kc, auto sub, auto at) {
+                    at([&](uint8_t* W, uint8_t* X) { compute(kc, sub, W, X, nullptr); });
+                };
+                auto even = [&](int j, auto cur_s, auto next_s) {
                     wait_vmcnt<L>();  // step j and its scales have landed; j + 1 may fly
                     barrier_only();
-                    load(j + 2, next);
+                    load(j + 2, next_s);
                     if (j < nk) {
                         read_scales();
-                        work(j, C0{}, cur);
+                        work(j, C0{}, cur_s);
                     }
                 };
-                auto odd = [&](int j, auto cur, auto next) {
+                auto odd = [&](int j, auto cur_s, auto next_s) {
                     wait_vmcnt<L>();
                     barrier_only();
-                    issue_scales(j + 1);
-                    load(j + 2, next);
-                    if (j < nk) work(j, C1{}, cur);
+                    issue_scales(cur, d, j + 1);
+                    load(j + 2, next_s);
+                    if (j < nk) work(j, C1{}, cur_s);
                 };
-                load(0, S0);
-                load(1, S1);
                 for (int j = 0; j < nk; j += 6) {
                     even(j, S0, S2);
                     odd(j + 1, S1, S0);
@@ -332,36 +376,37 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 }
             }
             wait_vmcnt<0>();
-            barrier_only();  // the stages are filled again by the next item
+            barrier_only();  // no stage is read any more
+            if (more) {
+                cur = item_of(item + per_xcd);
+                first_loads(cur);
+            }
 
 #pragma unroll
             for (int j = 0; j < NX; ++j) {
                 const int m = 64 * j + 32 * wm + l31;
                 const size_t row = (size_t)tile.row0 + m;
                 if constexpr (kSwiGLU) {
+                    float v[16];
+                    uint32_t mx = 0;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        float v[16];
-                        uint32_t mx = 0;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            v[r] = mx_silu_mul(acc[s][j][r], acc[s + 2][j][r]);
-                            mx = max(mx, abs_bits(v[r]));
-                        }
-                        mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
-                        const uint32_t byte = mx_scale_byte(mx);
-                        const float inv = mx_inverse(byte);
-                        if (m < tile.rows) {
-                            const int n0 = nb * 128 + 64 * wn + 32 * s;
-                            *reinterpret_cast<uint2*>(p.out + row * (I / 2) + n0 / 2 + 8 * hi) =
-                                make_uint2(mx_pack8(v, inv), mx_pack8(v + 8, inv));
-                            if (hi == 0) p.out_scale[row * (I / kMxBlock) + n0 / kMxBlock] = (uint8_t)byte;
-                        }
+                    for (int r = 0; r < 16; ++r) {
+                        v[r] = mx_silu_mul(acc[0][j][r], acc[1][j][r]);
+                        mx = max(mx, abs_bits(v[r]));
+                    }
+                    mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
+                    const uint32_t byte = mx_scale_byte(mx);
+                    const float inv = mx_inverse(byte);
+                    if (m < tile.rows) {
+                        const int n0 = nb * 128 + 32 * wn;
+                        *reinterpret_cast<uint2*>(p.out + row * (I / 2) + n0 / 2 + 8 * hi) =
+                            make_uint2(mx_pack8(v, inv), mx_pack8(v + 8, inv));
+                        if (hi == 0) p.out_scale[row * (I / kMxBlock) + n0 / kMxBlock] = (uint8_t)byte;
                     }
                 } else if (m < tile.rows) {
-                    uint16_t* y = reinterpret_cast<uint16_t*>(p.out) + row * p.Nw + nb * 256 + 128 * wn + 16 * hi;
+                    uint16_t* y = reinterpret_cast<uint16_t*>(p.out) + row * p.Nw + nb * 256 + 64 * wn + 16 * hi;
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
+                    for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const f32x16& a = acc[s][j];
@@ -372,14 +417,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 }
             }
         };
-        if (tile.rows <= 64)
-            run(std::integral_constant<int, 1>{});
-        else if (tile.rows <= 128)
-            run(std::integral_constant<int, 2>{});
-        else if (tile.rows <= 192)
-            run(std::integral_constant<int, 3>{});
-        else
-            run(std::integral_constant<int, 4>{});
+        with_nx(tile.rows, run);
+        if (!more) break;
+        item += per_xcd;
     }
 }
 
