@@ -168,8 +168,9 @@ typedef struct moe_expert_weights {
  * max_rows bounds offsets[n_groups] (T*k+T for the maps of moe_permute).
  * Limits: bf16 needs H % 128 == 0 and I % 128 == 0; fp8 needs H % 256 == 0,
  * I % 128 == 0 and H, I <= 16384 (the per-item table of weight block
- * scales), mxfp4 the same; E_local <= 1024; n_groups in {E_local, E_local+1} (the
- * latter needs the shared weights).
+ * scales), mxfp4 the same; E_local <= 1024, for mxfp4 <= 512 (every workgroup
+ * keeps the groups' tiles); n_groups in {E_local, E_local+1} (the latter needs
+ * the shared weights).
  * workspace: moe_expert_ffn_workspace_size(w, max_rows) bytes. */
 size_t moe_expert_ffn_workspace_size(const moe_expert_weights* w, int max_rows);
 moe_status moe_expert_ffn(const moe_expert_weights* w, const void* x_perm,

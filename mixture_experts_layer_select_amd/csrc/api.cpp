@@ -180,6 +180,7 @@ static moe_status check_weights(const moe_expert_weights* w) {
                 "moe_expert_ffn: mxfp4 needs H %% 256 == 0 and I %% 128 == 0 (H=%d I=%d)", w->H, w->I);
         REQUIRE(w->H <= 16384 && w->I <= 16384, MOE_ERR_UNSUPPORTED,
                 "moe_expert_ffn: mxfp4 needs H, I <= 16384 (H=%d I=%d)", w->H, w->I);
+        REQUIRE(w->E_local <= 512, MOE_ERR_UNSUPPORTED, "moe_expert_ffn: mxfp4 needs E_local <= 512");
         REQUIRE(w->w13_scale && w->w2_scale, MOE_ERR_INVALID_ARG, "moe_expert_ffn: mxfp4 needs scales");
         REQUIRE(aligned(w->w13, 16) && aligned(w->w2, 16) && aligned(w->ws13, 16) && aligned(w->ws2, 16) &&
                     aligned(w->w13_scale, 4) && aligned(w->w2_scale, 4) && aligned(w->ws13_scale, 4) &&

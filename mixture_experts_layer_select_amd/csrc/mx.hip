@@ -119,6 +119,66 @@ struct MxScales {  // two K steps
     uint8_t x[kMxTM * 16];
 };
 
+// Tiles and rows of the groups, built by every workgroup once from the
+// device-resident offsets: first tile (tile_start) and first row (row0, clamped
+// to the buffer) of each group. A group's nt = ceil(m / 256) tiles split its m
+// rows evenly. Looked up from LDS alone, since every item's start waits for it.
+constexpr int kMxMaxGroups = 513;  // E_local <= 512 and a shared group: checked by the C entry
+struct MxTiles {
+    int tile_start[kMxMaxGroups + 1];
+    int row0[kMxMaxGroups + 1];
+};
+
+// all threads call (it holds barriers); returns the number of tiles
+__device__ __forceinline__ int mx_build_tiles(MxTiles& tm, const int32_t* __restrict__ offsets, int n_groups,
+                                              int max_rows) {
+    for (int g = threadIdx.x; g <= n_groups; g += kMxThreads) tm.row0[g] = clamp_row(offsets[g], max_rows);
+    __syncthreads();
+    if (threadIdx.x < 64) {  // one wave: 64 groups at a time
+        int run = 0;
+        for (int g0 = 0; g0 < n_groups; g0 += 64) {
+            const int g = g0 + (int)threadIdx.x;
+            const int nt = g < n_groups ? max(0, tm.row0[g + 1] - tm.row0[g] + kMxTM - 1) / kMxTM : 0;
+            int sum = nt;
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) {
+                const int o = __shfl_up(sum, s);
+                if ((int)threadIdx.x >= s) sum += o;
+            }
+            if (g < n_groups) tm.tile_start[g] = run + sum - nt;
+            run += __shfl(sum, 63);
+        }
+        if (threadIdx.x == 0) tm.tile_start[n_groups] = run;
+    }
+    __syncthreads();
+    return tm.tile_start[n_groups];
+}
+
+// Item -> tile and n-block, in panels of kMxPanel m-tiles of a group (the last
+// one may be shorter): all n-blocks of a panel, its m-tiles fastest, so the
+// workgroups of one XCD share both operands' slices of a K step through L2.
+__device__ __forceinline__ MTile mx_item_at(const MxTiles& tm, int n_groups, int item, int NB, int& nb) {
+    const int mt = item / NB;
+    int lo = 0, hi = n_groups - 1;  // the group: the last g with tile_start[g] <= mt
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tm.tile_start[mid] <= mt) lo = mid;
+        else hi = mid - 1;
+    }
+    const int t0 = __builtin_amdgcn_readfirstlane(tm.tile_start[lo]);
+    const int nt = __builtin_amdgcn_readfirstlane(tm.tile_start[lo + 1]) - t0;
+    const int r0 = __builtin_amdgcn_readfirstlane(tm.row0[lo]);
+    const int m = __builtin_amdgcn_readfirstlane(tm.row0[lo + 1]) - r0;
+    const int local = item - t0 * NB;
+    const int pi = local / (kMxPanel * NB);  // never past the last panel
+    const int ph = min(kMxPanel, nt - pi * kMxPanel);
+    const int idx = local - pi * kMxPanel * NB;
+    nb = idx / ph;
+    const int i = pi * kMxPanel + idx - nb * ph;
+    const int a = (int)((long)i * m / nt), b = (int)((long)(i + 1) * m / nt);
+    return MTile{__builtin_amdgcn_readfirstlane(lo), r0 + a, b - a};
+}
+
 // weight row (within the wave's 32) that MFMA row rho reads: lane (l31, hi)
 // then holds the D values of 16 consecutive weight rows 16 hi + [0, 16), so
 // it writes 16 neighbouring outputs
@@ -126,6 +186,17 @@ __device__ __forceinline__ int mx_row_of(int rho) { return 16 * ((rho >> 2) & 1)
 // chunk swizzles: weight rows are read in mx_row_of's order, tokens in rows'
 __device__ __forceinline__ int mx_swz_w(int q) { return ((q & 3) ^ ((q >> 2) & 1)) | ((q >> 4) & 1) << 2; }
 __device__ __forceinline__ int mx_swz_x(int q) { return (q & 7) ^ ((q >> 3) & 1); }
+
+// a large kernel's lambdas are otherwise left as calls with their captures in memory
+#define MX_INLINE __attribute__((always_inline))
+
+// The workgroup barrier of the load ring: this wave's LDS reads are done and no
+// memory access moves across it at compile time, but loads stay in flight.
+__device__ __forceinline__ void mx_barrier() {
+    asm volatile("" ::: "memory");
+    barrier_only();
+    asm volatile("" ::: "memory");
+}
 
 struct MxGemm {
     const uint8_t* x;         // activation codes, rows of K/2 bytes
@@ -150,18 +221,18 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     __shared__ __attribute__((aligned(1024))) uint8_t o3[32 * kKB];
     __shared__ __attribute__((aligned(1024))) uint8_t o4[16 * kKB];
     __shared__ __attribute__((aligned(1024))) MxScales sc;
-    __shared__ TileMap tm;
+    __shared__ MxTiles tm;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave & 1, wn = wave >> 1;
     const int l31 = lane & 31, hi = lane >> 5;
     const int K = p.K, kb = K / kMxBlock, rowb = K / 2;
     const int nk = (K + 255) / 256;
-    const bool half = K % 256 != 0;  // the last step holds 128 of K
+    const int nk2 = K / 128;  // its halves: odd where the last step holds 128 of K
     const int I = p.Nw / 2;  // SwiGLU: intermediate size
     // uniform, so that the item loop and the descriptors it carries stay scalar
     const int n_items =
-        __builtin_amdgcn_readfirstlane(build_tile_map(tm, p.offsets, p.n_groups, p.max_rows, kMxTM)) * p.NB;
+        __builtin_amdgcn_readfirstlane(mx_build_tiles(tm, p.offsets, p.n_groups, p.max_rows)) * p.NB;
     const int xcd = blockIdx.x & 7;
     const int per_xcd = gridDim.x >> 3;
     const int i_lo = (int)((long)n_items * xcd / 8);
@@ -176,11 +247,11 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
         offa[h] = rw * kMxStepB + ((2 * h + hi) ^ mx_swz_w(rw)) * 16;
         offb[h] = (32 * wm + l31) * kMxStepB + ((2 * h + hi) ^ mx_swz_x(l31)) * 16;
     }
-    auto q0 = [&](int s) { return kSwiGLU ? 128 * s + 32 * wn : 64 * wn + 32 * s; };
+    auto q0 = [&](int s) MX_INLINE { return kSwiGLU ? 128 * s + 32 * wn : 64 * wn + 32 * s; };
     // piece 8i + wave of either operand holds LDS rows 64i + pr, eight lanes a row
     const int pr = 8 * wave + (lane >> 3);
     // a piece's weight rows lie a uniform distance behind piece 0's
-    auto wdist = [&](int i) -> uint32_t {
+    auto wdist = [&](int i) MX_INLINE -> uint32_t {
         return (uint32_t)(kSwiGLU ? (i < 2 ? 64 * i : I + 64 * (i - 2)) : 64 * i) * rowb;
     };
 
@@ -194,7 +265,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     struct Desc {
         __amdgpu_buffer_rsrc_t w, x, s;
     };
-    auto desc_of = [&](const MTile& t) {
+    auto desc_of = [&](const MTile& t) MX_INLINE {
         const int group = __builtin_amdgcn_readfirstlane(t.group), row0 = __builtin_amdgcn_readfirstlane(t.row0),
                   rows = __builtin_amdgcn_readfirstlane(t.rows);
         const bool routed = group < p.n_routed;
@@ -210,14 +281,10 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                           : buffer_rsrc(p.xs + (size_t)row0 * kb, clamp_bytes((size_t)rows * kb));
         return d;
     };
-    auto item_of = [&](int item) {
+    auto item_of = [&](int item) MX_INLINE {
         Item c;
-        int nb_v;
-        const MTile t = item_at(tm, p.offsets, p.n_groups, p.max_rows, item, p.NB, kMxTM, nb_v, kMxPanel);
-        c.nb = __builtin_amdgcn_readfirstlane(nb_v);
-        c.tile = MTile{__builtin_amdgcn_readfirstlane(t.group), __builtin_amdgcn_readfirstlane(t.row0),
-                       __builtin_amdgcn_readfirstlane(t.rows)};
-        auto src_row = [&](int r) -> uint32_t {  // the tile's row r, clamped to it
+        c.tile = mx_item_at(tm, p.n_groups, item, p.NB, c.nb);
+        auto src_row = [&](int r) MX_INLINE -> uint32_t {  // the tile's row r, clamped to it
             r = min(r, c.tile.rows - 1);
             if (!kGather) return (uint32_t)r;
             const int slot = p.src.row_slot[c.tile.row0 + r];
@@ -233,7 +300,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                      : src_row(64 * w4 + lane) * kb;
         return c;
     };
-    auto issue = [&](const Item& c, const Desc& d, auto nx_c, int kc, uint8_t* W, uint8_t* X01, uint8_t* X23) {
+    auto issue = [&](const Item& c, const Desc& d, auto nx_c, int kc, uint8_t* W, uint8_t* X01, uint8_t* X23) MX_INLINE {
         constexpr int NX = decltype(nx_c)::value;
         const uint32_t ko = (uint32_t)min(kc, nk - 1) * kMxStepB;  // steps past the end bring the last one again, unused
 #pragma unroll
@@ -242,19 +309,19 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
         for (int i = 0; i < NX; ++i)
             lds_buf16(d.x, c.xoff[i], ko, i < 2 ? X01 + (8 * i + wave) * 1024 : X23 + (8 * (i - 2) + wave) * 1024);
     };
-    auto issue_scales = [&](const Item& c, const Desc& d, int kc) {
+    auto issue_scales = [&](const Item& c, const Desc& d, int kc) MX_INLINE {
         lds_buf16(d.s, c.soff, (uint32_t)min(kc, nk - 1) / 2 * 16, (wave < 4 ? sc.w : sc.x) + (wave & 3) * 1024);
     };
-    auto with_nx = [&](int rows, auto f) {
+    auto with_nx = [&](int rows, auto f) MX_INLINE {
         if (rows <= 64) f(std::integral_constant<int, 1>{});
         else if (rows <= 128) f(std::integral_constant<int, 2>{});
         else if (rows <= 192) f(std::integral_constant<int, 3>{});
         else f(std::integral_constant<int, 4>{});
     };
-    auto first_loads = [&](const Item& c) {
+    auto first_loads = [&](const Item& c) MX_INLINE {
         const Desc d = desc_of(c.tile);
         issue_scales(c, d, 0);
-        with_nx(__builtin_amdgcn_readfirstlane(c.tile.rows), [&](auto nx_c) {
+        with_nx(__builtin_amdgcn_readfirstlane(c.tile.rows), [&](auto nx_c) MX_INLINE {
             if constexpr (decltype(nx_c)::value > 2) {
                 issue(c, d, nx_c, 0, o0, o0 + 32 * kKB, o1);
             } else {
@@ -270,15 +337,16 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     first_loads(cur);
     for (;;) {
         const bool more = item + per_xcd < i_hi;
+        const Item next = more ? item_of(item + per_xcd) : cur;
         const MTile tile{__builtin_amdgcn_readfirstlane(cur.tile.group), __builtin_amdgcn_readfirstlane(cur.tile.row0),
                          __builtin_amdgcn_readfirstlane(cur.tile.rows)};
         const int nb = __builtin_amdgcn_readfirstlane(cur.nb);
         const Desc d = desc_of(tile);
-        auto run = [&](auto nx_c) {
+        auto run = [&](auto nx_c) MX_INLINE {
             constexpr int NX = decltype(nx_c)::value;
             f32x16 acc[2][NX] = {};
             u32x4 sw[2], sx[NX];
-            auto read_scales = [&]() {
+            auto read_scales = [&]() MX_INLINE {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) sw[s] = *reinterpret_cast<const u32x4*>(&sc.w[(q0(s) + rw) * 16]);
 #pragma unroll
@@ -286,15 +354,17 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                     sx[j] = *reinterpret_cast<const u32x4*>(&sc.x[(64 * j + 32 * wm + l31) * 16]);
             };
             // step kc from a stage; sub: its two dwords of the group's scales
-            auto compute = [&](int kc, auto sub_c, const uint8_t* W, const uint8_t* X01, const uint8_t* X23) {
+            auto compute = [&](int kc, auto sub_c, const uint8_t* W, const uint8_t* X01, const uint8_t* X23) MX_INLINE {
                 constexpr int sub = decltype(sub_c)::value;
-                auto part = [&](auto u_c) {  // 128 of K: MFMAs h = 2u, 2u + 1
+                auto part = [&](auto u_c) MX_INLINE {  // 128 of K: MFMAs h = 2u, 2u + 1
                     constexpr int u = decltype(u_c)::value;
+                    // the half past an odd end multiplies by scales of 2^-127
+                    const uint32_t on = 2 * kc + u < nk2 ? ~0u : 0u;
                     u32x4 a[2][2];
                     uint32_t sa[2];
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        sa[s] = sw[s][2 * sub + u] >> (8 * hi);
+                        sa[s] = (sw[s][2 * sub + u] >> (8 * hi)) & on;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             a[s][h] = *reinterpret_cast<const u32x4*>(W + q0(s) * kMxStepB + offa[2 * u + h]);
@@ -304,7 +374,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                         const uint8_t* X = j < 2 ? X01 + j * 8192 : X23 + (j - 2) * 8192;
                         const u32x4 b0 = *reinterpret_cast<const u32x4*>(X + offb[2 * u]);
                         const u32x4 b1 = *reinterpret_cast<const u32x4*>(X + offb[2 * u + 1]);
-                        const uint32_t sb = sx[j][2 * sub + u] >> (8 * hi);
+                        const uint32_t sb = (sx[j][2 * sub + u] >> (8 * hi)) & on;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) acc[s][j] = mfma_fp4<0, 0>(a[s][0], b0, acc[s][j], sa[s], sb);
 #pragma unroll
@@ -312,56 +382,56 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                     }
                 };
                 part(std::integral_constant<int, 0>{});
-                if (!half || kc + 1 < nk) part(std::integral_constant<int, 1>{});
+                part(std::integral_constant<int, 1>{});
             };
             using C0 = std::integral_constant<int, 0>;
             using C1 = std::integral_constant<int, 1>;
             // A group's scales are issued in its last step but one, after the barrier behind which every wave
             // holds the previous group's, and ahead of that step's own loads, so each wait below covers them.
             if constexpr (NX > 2) {
-                auto S0 = [&](auto f) { f(o0, o0 + 32 * kKB, o1); };
-                auto S1 = [&](auto f) { f(o2, o3, o3 + 16 * kKB); };
-                auto load = [&](int kc, auto at) {
-                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) { issue(cur, d, nx_c, kc, W, X01, X23); });
+                auto S0 = [&](auto f) MX_INLINE { f(o0, o0 + 32 * kKB, o1); };
+                auto S1 = [&](auto f) MX_INLINE { f(o2, o3, o3 + 16 * kKB); };
+                auto load = [&](int kc, auto at) MX_INLINE {
+                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) MX_INLINE { issue(cur, d, nx_c, kc, W, X01, X23); });
                 };
-                auto work = [&](int kc, auto sub, auto at) {
-                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) { compute(kc, sub, W, X01, X23); });
+                auto work = [&](int kc, auto sub, auto at) MX_INLINE {
+                    at([&](uint8_t* W, uint8_t* X01, uint8_t* X23) MX_INLINE { compute(kc, sub, W, X01, X23); });
                 };
                 for (int j = 0; j < nk; j += 2) {
                     wait_vmcnt<0>();
-                    barrier_only();
+                    mx_barrier();
                     load(j + 1, S1);
                     read_scales();
                     work(j, C0{}, S0);
                     wait_vmcnt<0>();
-                    barrier_only();
+                    mx_barrier();
                     issue_scales(cur, d, j + 2);
                     load(j + 2, S0);
                     if (j + 1 < nk) work(j + 1, C1{}, S1);
                 }
             } else {
                 constexpr int L = 4 + NX;  // a step's loads
-                auto S0 = [&](auto f) { f(o0, o0 + 32 * kKB); };
-                auto S1 = [&](auto f) { f(o2, o1); };
-                auto S2 = [&](auto f) { f(o3, o4); };
-                auto load = [&](int kc, auto at) {
-                    at([&](uint8_t* W, uint8_t* X) { issue(cur, d, nx_c, kc, W, X, nullptr); });
+                auto S0 = [&](auto f) MX_INLINE { f(o0, o0 + 32 * kKB); };
+                auto S1 = [&](auto f) MX_INLINE { f(o2, o1); };
+                auto S2 = [&](auto f) MX_INLINE { f(o3, o4); };
+                auto load = [&](int kc, auto at) MX_INLINE {
+                    at([&](uint8_t* W, uint8_t* X) MX_INLINE { issue(cur, d, nx_c, kc, W, X, nullptr); });
                 };
-                auto work = [&](int kc, auto sub, auto at) {
-                    at([&](uint8_t* W, uint8_t* X) { compute(kc, sub, W, X, nullptr); });
+                auto work = [&](int kc, auto sub, auto at) MX_INLINE {
+                    at([&](uint8_t* W, uint8_t* X) MX_INLINE { compute(kc, sub, W, X, nullptr); });
                 };
-                auto even = [&](int j, auto cur_s, auto next_s) {
+                auto even = [&](int j, auto cur_s, auto next_s) MX_INLINE {
                     wait_vmcnt<L>();  // step j and its scales have landed; j + 1 may fly
-                    barrier_only();
+                    mx_barrier();
                     load(j + 2, next_s);
                     if (j < nk) {
                         read_scales();
                         work(j, C0{}, cur_s);
                     }
                 };
-                auto odd = [&](int j, auto cur_s, auto next_s) {
+                auto odd = [&](int j, auto cur_s, auto next_s) MX_INLINE {
                     wait_vmcnt<L>();
-                    barrier_only();
+                    mx_barrier();
                     issue_scales(cur, d, j + 1);
                     load(j + 2, next_s);
                     if (j < nk) work(j, C1{}, cur_s);
@@ -376,10 +446,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 }
             }
             wait_vmcnt<0>();
-            barrier_only();  // no stage is read any more
+            mx_barrier();  // no stage is read any more
             if (more) {
-                cur = item_of(item + per_xcd);
-                first_loads(cur);
+                first_loads(next);
             }
 
 #pragma unroll
@@ -420,6 +489,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
         with_nx(tile.rows, run);
         if (!more) break;
         item += per_xcd;
+        cur = next;
     }
 }
 

@@ -257,3 +257,41 @@ def test_noalloc_equals_workspace():
     y = torch.zeros_like(want)
     L.moe_expert_ffn_noalloc(ex.w, x, xs, torch.tensor(offsets, dtype=torch.int32, device=DEV), 4, 120, y)
     assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_expert_ffn_with_the_most_experts(shared):
+    """512 local experts, nearly all of them empty, with and without the shared group behind them."""
+    H, I, E = 256, 128, 512
+    ex = Experts(H, I, E, shared, 15)
+    rows = [0] * (E + shared)
+    for e, r in ((0, 3), (63, 1), (64, 70), (255, 2), (510, 257), (511, 5)):
+        rows[e] = r
+    if shared:
+        rows[E] = 9
+    offsets = [0] + np.cumsum(rows).tolist()
+    R = offsets[-1]
+    x, xs, xv = quantized((R, H), 1.0, 26)
+    y = run_ffn(x, xs, ex, offsets, R)
+    for e in range(len(rows)):
+        if rows[e]:
+            a, b = offsets[e], offsets[e + 1]
+            want, bound = ex.reference(xv[a:b], e)
+            check(f"group {e} of {b - a}", y[a:b], want, bound)
+
+
+@pytest.mark.parametrize("R", [20, 100, 200])
+def test_nan_of_the_next_row_stays_out_of_an_odd_last_half(R):
+    """I % 256 = 128: the last K step of the down product holds only 128 of I; the row behind is all NaN."""
+    H, I = 256, 384
+    ex = Experts(H, I, 1, False, 16)
+    x, xs, _ = quantized((R, H), 1.0, 27)
+    clean = run_ffn(x, xs, ex, [0, R], R)
+    bad = xs.clone()
+    bad[1::2] = 255                                 # every other intermediate row is NaN
+    ex.w._tensors[3][0, 8::16] = 255                # ... and output columns 8, 24, ...
+    y = run_ffn(x, bad, ex, [0, R], R).float()
+    keep = torch.ones(H, dtype=torch.bool, device=DEV)
+    keep[8::16] = False
+    assert torch.equal(y[0::2][:, keep], clean[0::2][:, keep].float())
+    assert bool(torch.isnan(y[1::2]).all()) and bool(torch.isnan(y[:, 8::16]).all())

@@ -59,6 +59,8 @@ def test_ffn_refusals(L):
     for H, I in ((384, 256), (512, 192), (16640, 256), (512, 16512)):
         refused(L, "MOE_ERR_UNSUPPORTED", f, w(H, I), P, P, P, 4, 100, P, P, 1 << 40, 0)
         assert L.moe_expert_ffn_workspace_size(w(H, I), 100) == 0
+    refused(L, "MOE_ERR_UNSUPPORTED", f, w(E=513), P, P, P, 513, 100, P, P, 1 << 40, 0)
+    assert L.moe_expert_ffn_workspace_size(w(E=512), 100) == n
     g = L.moe_expert_ffn_gate_up_tokens
     refused(L, "MOE_ERR_INVALID_ARG", g, w(), P, P, 10, 2, None, P, 4, 100, P, n, 0)
     refused(L, "MOE_ERR_UNSUPPORTED", g, w(), P, P, 1 << 23, 2, P, P, 4, 100, P, n, 0)  # T*H = 2^32
