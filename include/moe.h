@@ -296,8 +296,7 @@ moe_status moe_dequantize_mxfp4(const void* codes, const uint8_t* scales, int64_
  *   count over; ids outside the local range add nothing, an id that stands
  *   twice in a token's picks adds both weights); out [T,H] bf16 (may be x).
  *   workspace: moe_layer_few_workspace_size(w, T, E, k) bytes of device memory,
- *   256-byte aligned; its first 256 bytes must be zero before the first call, and
- *   every completed call leaves them zero. Calls that overlap need a workspace each.
+ *   256-byte aligned, of any contents. Calls that overlap need a workspace each.
  * Limits: T <= 16, k <= 8, k <= E, E <= 256 with a router, H % 256 == 0,
  * H <= 8192, I % 128 == 0, I <= 16384. */
 size_t moe_layer_few_workspace_size(const moe_expert_weights* w, int T, int E, int k);

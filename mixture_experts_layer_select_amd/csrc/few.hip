@@ -3,19 +3,31 @@
 // HBM once whatever the number of tokens that picked it, and an expert's
 // product is taken for all 16 columns at no extra cost; only picked
 // (token, expert) pairs are kept. Bound by HBM: 3 H I (1/2 + 1/32) bytes per
-// distinct hit expert.
+// distinct hit expert. Three kernels:
 //
-//   gate/up: an item is 8 intermediate columns of one expert (8 gate and 8 up
-//     rows, one MFMA operand); the 8 waves split K and add their partial sums
-//     through LDS. Items are I/8 per hit expert, so with one workgroup per CU
-//     the load is even for any number of experts. The quantised tokens stay in
-//     registers for the whole kernel.
-//   down + combine: a workgroup owns 32 columns of the output for every hit
-//     expert; the waves split K, quantise the fp32 intermediate as they read it
-//     (a lane holds a whole block of 32, so its largest needs no exchange), and
-//     add each expert's product, times its routing weight, in fp32. One rounding
-//     at the end, no atomics: the result does not depend on the schedule.
+//   logits: one wave per (token, expert), the same bits as moe_route's.
+//   gate/up: every workgroup picks the experts from the logits itself (one wave
+//     per token), which costs less than a kernel of its own. An item is 8
+//     intermediate columns of one expert (8 gate and 8 up rows, one MFMA
+//     operand); the 8 waves split K and add their partial sums through LDS.
+//     Items are I/8 per hit expert, so with one workgroup per CU the load is
+//     even for any number of experts. The quantised tokens stay in registers
+//     for the whole kernel. Items of the shared expert come first: the load of
+//     the first one does not wait for the routing.
+//   down + combine: a workgroup owns up to 32 columns of the output for every
+//     hit expert; the waves split K and add each expert's product, times its
+//     routing weight, in fp32 registers until the end. One rounding, no
+//     atomics, and a token's sum depends neither on the schedule nor on the
+//     other tokens. The intermediate is quantised into LDS, as many
+//     (expert, token) rows at a time as fit.
+//
+// Both products stream the weights from HBM into LDS with direct loads, each
+// wave for itself: 8 rows of 128 bytes per load, the next item's or the next
+// two units' loads in flight while one is multiplied, so no wave waits for
+// another's data. Weights read straight into the MFMA's registers (16 rows of
+// 64 bytes per load, waited for before each product) reached 2.7 and 2.0 TB/s.
 #include "mx_dev.h"
+#include "route_dev.h"
 
 namespace moe {
 namespace {
@@ -23,79 +35,121 @@ namespace {
 constexpr int kFewT = 16;      // tokens: the columns of one MFMA
 constexpr int kFewK = 8;       // picks per token
 constexpr int kFewSlots = kFewT * kFewK;
+constexpr int kFewGroups = kFewSlots + 1;
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / 64;
-constexpr int kFewMaxE = 1024;
-constexpr int kFewSteps = 8;   // K steps of 128 per wave: H <= 8192
+constexpr int kFewPairs = 4;   // K steps of 256 per wave of the gate/up kernel: H <= 8192
 
 struct FewArgs {
     const uint16_t* x;         // [T][H] bf16
-    const int32_t* ids;        // [T][k]
-    const float* topk_w;       // [T][k]
-    int T, k, H, I, base, E_local, has_shared;
+    const float* logits;       // [T][E], or null: ids and weights are given
+    int32_t* ids;              // [T][k]
+    float* topk_w;             // [T][k]
+    int T, k, E, scoring, renorm, H, I, base, E_local, has_shared;
     const uint8_t *w13, *w13s, *w2, *w2s, *ws13, *ws13s, *ws2, *ws2s;
     float* a;                  // [T*k + T][I] fp32 intermediate, row = slot (T*k + t: shared)
     uint16_t* out;             // [T][H] bf16
+    int cols;                  // output columns per workgroup of the down kernel
 };
 
-// The distinct local experts among the picks, ascending, the shared expert
-// behind them; and for each (group, token) the first slot that picked it and
-// the sum of the weights of all that did (an id may stand twice in a row).
+// The groups: the shared expert (if any), then the distinct local experts among
+// the picks, ascending.
 struct FewMap {
-    uint32_t hit[kFewMaxE / 32];
-    int ids[kFewSlots];
-    int expert[kFewSlots + 1];
-    short slot[(kFewSlots + 1) * kFewT];   // -1: not picked
-    float weight[(kFewSlots + 1) * kFewT];
-    int n;
+    __attribute__((aligned(16))) int id[kFewSlots];   // local expert of a slot, -1: none
+    __attribute__((aligned(16))) int key[kFewSlots];  // the expert at its first slot, INT_MAX elsewhere
+    float w[kFewSlots];
+    int expert[kFewGroups];              // -1: the shared one
+    uint32_t mask[kFewGroups];           // the tokens that picked it
+    short slot[kFewGroups * kFewT];      // the first slot of a token that did, -1: none
+};
+// ... and what the down kernel needs besides
+struct FewSum {
+    float weight[kFewGroups * kFewT];    // the sum of a token's weights (an id may stand twice in a row)
+    int pre[kFewGroups + 1];             // picked (group, token) pairs before each group
+    short pair_slot[kFewSlots + kFewT];  // the pairs in order: slot and group
+    short pair_group[kFewSlots + kFewT];
 };
 
-__device__ __forceinline__ int build_few_map(FewMap& m, const FewArgs& p) {
-    const int tid = threadIdx.x, S = p.T * p.k;
-    for (int i = tid; i < kFewMaxE / 32; i += kFewThreads) m.hit[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < S; i += kFewThreads) {
-        const int id = p.ids[i];  // any value: compared before the subtraction can overflow
-        const int e = id >= p.base && id - p.base < p.E_local ? id - p.base : -1;
-        m.ids[i] = e;
-        if (e >= 0) atomicOr(&m.hit[e >> 5], 1u << (e & 31));
+__device__ __forceinline__ int few_local(const FewArgs& p, int id) {  // any value: no overflow
+    return id >= p.base && id - p.base < p.E_local ? id - p.base : -1;
+}
+
+// Builds the map from m.id and m.w (S = T k slots, visible to all threads) and
+// returns the number of groups. All threads call; ends with a barrier.
+template <bool kSum>
+__device__ __forceinline__ int build_few_map(FewMap& m, FewSum* s, const FewArgs& p) {
+    const int tid = threadIdx.x, S = p.T * p.k, sh = p.has_shared ? 1 : 0;
+    for (int i = tid; i < kFewGroups * kFewT; i += kFewThreads) {
+        m.slot[i] = (short)(sh && i < p.T ? S + i : -1);
+        if (kSum) s->weight[i] = sh && i < p.T ? 1.0f : 0.0f;
     }
-    __syncthreads();
-    for (int e = tid; e < p.E_local; e += kFewThreads) {
-        if (m.hit[e >> 5] >> (e & 31) & 1) {
-            int pos = __popc(m.hit[e >> 5] & ((1u << (e & 31)) - 1));
-            for (int w = 0; w < e >> 5; ++w) pos += __popc(m.hit[w]);
-            m.expert[pos] = e;
+    for (int i = tid; i < kFewGroups; i += kFewThreads) m.mask[i] = sh && i == 0 ? (1u << p.T) - 1 : 0;
+    if (sh && tid == 0) m.expert[0] = -1;
+    int e = -1;
+    bool first = false, first_of_token = false;
+    if (tid < kFewSlots) {
+        e = tid < S ? m.id[tid] : -1;
+        first = first_of_token = e >= 0;
+        const int t0 = tid - tid % p.k;
+        for (int j = 0; j < min(tid, S); ++j)
+            if (m.id[j] == e) {
+                first = false;
+                if (j >= t0) first_of_token = false;
+            }
+        m.key[tid] = first ? e : 0x7fffffff;
+    }
+    mx_barrier();
+    int n = sh, rank = sh;
+    for (int j = 0; j < S; j += 4) {  // the slots from S on hold INT_MAX
+        const i32x4 key = *reinterpret_cast<const i32x4*>(&m.key[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            n += key[i] != 0x7fffffff;
+            rank += key[i] < e;
         }
     }
-    if (tid == 0) {
-        int n = 0;
-        for (int w = 0; w < kFewMaxE / 32; ++w) n += __popc(m.hit[w]);
-        if (p.has_shared) m.expert[n++] = -1;
-        m.n = n;
-    }
-    __syncthreads();
-    for (int i = tid; i < m.n * kFewT; i += kFewThreads) {
-        const int e = m.expert[i / kFewT], t = i % kFewT;
-        int slot = -1;
+    if (first) m.expert[rank] = e;
+    if (first_of_token) {
+        const int t = tid / p.k;
         float w = 0.f;
-        if (t < p.T) {
-            if (e < 0) {
-                slot = S + t;
-                w = 1.0f;
-            } else {
-                for (int j = p.k - 1; j >= 0; --j)
-                    if (m.ids[t * p.k + j] == e) {
-                        slot = t * p.k + j;
-                        w += p.topk_w[slot];
-                    }
+        for (int j = t * p.k + p.k - 1; j >= tid; --j)
+            if (m.id[j] == e) w += m.w[j];
+        m.slot[rank * kFewT + t] = (short)tid;
+        if (kSum) s->weight[rank * kFewT + t] = w;
+        atomicOr(&m.mask[rank], 1u << t);
+    }
+    mx_barrier();
+    n = __builtin_amdgcn_readfirstlane(n);
+    if (kSum) {
+        if (tid < 64) {
+            int run = 0;
+            for (int g0 = 0; g0 < n; g0 += 64) {
+                const int g = g0 + tid;
+                const int c = g < n ? __popc(m.mask[g]) : 0;
+                int sum = c;
+#pragma unroll
+                for (int d = 1; d < 64; d <<= 1) {
+                    const int o = __shfl_up(sum, d);
+                    if (tid >= d) sum += o;
+                }
+                if (g < n) s->pre[g] = run + sum - c;
+                run += __shfl(sum, 63);
+            }
+            if (tid == 0) s->pre[n] = run;
+        }
+        mx_barrier();
+        for (int i = tid; i < n * kFewT; i += kFewThreads) {
+            const int g = i / kFewT, t = i % kFewT;
+            const uint32_t mask = m.mask[g];
+            if (mask >> t & 1) {
+                const int at = s->pre[g] + __popc(mask & ((1u << t) - 1));
+                s->pair_slot[at] = m.slot[i];
+                s->pair_group[at] = (short)g;
             }
         }
-        m.slot[i] = (short)slot;
-        m.weight[i] = w;
+        mx_barrier();
     }
-    __syncthreads();
-    return m.n;
+    return n;
 }
 
 __device__ __forceinline__ f32x4 mfma16_fp4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
@@ -104,147 +158,336 @@ __device__ __forceinline__ f32x4 mfma16_fp4(u32x4 a, u32x4 b, f32x4 c, uint32_t 
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
+// LDS rows of 128 bytes: chunk c (16 bytes) of row r sits at chunk c ^ (r & 7),
+// so the 16 rows of one MFMA operand spread over the banks
+__device__ __forceinline__ uint32_t few_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// ---------------------------------------------------------------- gate/up
+constexpr int kGuCodes = 16 * 128 * kFewPairs;  // a wave's share of one item
+constexpr int kGuStage = kGuCodes + 16 * 8 * kFewPairs;  // ... and its scales
+constexpr int kGuLoads = 2 * kFewPairs + 2;     // its loads: codes, and two for the scales
+
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
+    // a stage is an object of its own, so that reads of one do not wait for loads into the other
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[kFewWaves][kGuStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t s1[kFewWaves][kGuStage];
+    __shared__ __attribute__((aligned(16))) float red[2][kFewWaves][kFewT][16];
     __shared__ FewMap m;
-    __shared__ float red[kFewWaves][16][17];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lk = lane >> 4;
-    const int nk = p.H / 128, ns = (nk + kFewWaves - 1) / kFewWaves;
-    const int s0 = wave * ns, s1 = min(nk, s0 + ns);
-    const int kb = p.H / kMxBlock;
-    const int n = build_few_map(m, p);
+    const int rowb = p.H / 2, kb = p.H / kMxBlock;
+    const int np = p.H / 256, p0 = wave * np / kFewWaves, cnt = (wave + 1) * np / kFewWaves - p0;
+    const int S = p.T * p.k, sh = p.has_shared ? 1 : 0;
+    const int per = p.I / 8, G = gridDim.x;
 
-    // the tokens, quantised as moe_quantize_mxfp4 does: lane (li, lk) holds
-    // token li's block 4 step + lk
-    u32x4 b[kFewSteps];
-    uint32_t sb[kFewSteps];
+    // a load: the 8 gate or the 8 up rows of an item for one K step
+    const uint32_t wv = (uint32_t)((lane >> 3) * rowb + p0 * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
+    const uint32_t up = (uint32_t)p.I * rowb;
+    const uint32_t sv = (uint32_t)((lane >> 3) * kb + p0 * 8 + (lane & 7) * 4), sup = (uint32_t)p.I * kb;
+    auto issue = [&](int it, int n, uint8_t (&st)[kFewWaves][kGuStage]) MX_INLINE {
+        const bool on = it < n * per;  // items past the end load nothing, but count
+        const int g = on ? it / per : 0, i0 = on ? it % per * 8 : 0;
+        const int e = on && g >= sh ? __builtin_amdgcn_readfirstlane(m.expert[g]) : 0;
+        const size_t rows = 2 * (size_t)p.I;
+        const uint8_t* W = (g < sh ? p.ws13 : p.w13 + e * rows * rowb) + (size_t)i0 * rowb;
+        const uint8_t* Ws = (g < sh ? p.ws13s : p.w13s + e * rows * kb) + (size_t)i0 * kb;
+        const uint32_t left = (uint32_t)(rows - i0), c = on ? cnt : 0;  // K steps past this wave's neither
+        const __amdgpu_buffer_rsrc_t sd = buffer_rsrc(Ws, on ? left * kb : 0);
+        lds_buf4(sd, sv, 0, st[wave] + kGuCodes);
+        lds_buf4(sd, sv, sup, st[wave] + kGuCodes + 256);
 #pragma unroll
-    for (int q = 0; q < kFewSteps; ++q) {
-        b[q] = u32x4{0, 0, 0, 0};
-        sb[q] = 127;
-        if (s0 + q < s1 && li < p.T) {
-            const u32x4* src = reinterpret_cast<const u32x4*>(p.x + (size_t)li * p.H + (4 * (s0 + q) + lk) * kMxBlock);
-            float v[32];
-            uint32_t mx = 0;
+        for (uint32_t j = 0; j < kFewPairs; ++j) {
+            const __amdgpu_buffer_rsrc_t wd = buffer_rsrc(W, j < c ? left * rowb : 0);
+            lds_buf16(wd, wv, j * 128, st[wave] + j * 2048);
+            lds_buf16(wd, wv, j * 128 + up, st[wave] + j * 2048 + 1024);
+        }
+    };
+
+    u32x4 raw[2 * kFewPairs][4];  // the tokens: lane (li, lk) holds token li's block lk of each half step
+    {
+        const __amdgpu_buffer_rsrc_t xd = buffer_rsrc(p.x, (uint32_t)(p.T * p.H * 2));  // rows past T are zeros
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const u32x4 w = src[c];
+        for (int q = 0; q < 2 * kFewPairs; ++q) {
+            const uint32_t at = q < 2 * cnt ? (uint32_t)(li * p.H + (2 * p0 + q) * 128 + lk * kMxBlock) * 2 : 0xffffff00u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[8 * c + 2 * i] = bf16_lo(w[i]);
-                    v[8 * c + 2 * i + 1] = bf16_hi(w[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx = max(mx, abs_bits(v[i]));
-            sb[q] = mx_scale_byte(mx);
-            const float inv = mx_inverse(sb[q]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) b[q][c] = mx_pack8(v + 8 * c, inv);
+            for (int c = 0; c < 4; ++c) raw[q][c] = buffer_load16(xd, at, 16 * c);
         }
     }
-
-    const int per = p.I / 8, n_items = n * per;
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const int g = item / per, i0 = item % per * 8;
-        const int e = m.expert[g];
-        const uint8_t* W = e < 0 ? p.ws13 : p.w13 + (size_t)e * 2 * p.I * (p.H / 2);
-        const uint8_t* Ws = e < 0 ? p.ws13s : p.w13s + (size_t)e * 2 * p.I * kb;
-        const int row = i0 + (li & 7) + (li >> 3) * p.I;  // MFMA rows 0..7 gate, 8..15 up
-        const uint8_t* wr = W + (size_t)row * (p.H / 2) + 16 * lk;
-        const uint8_t* sr = Ws + (size_t)row * kb + lk;
-        u32x4 a[kFewSteps];
-        uint32_t sa[kFewSteps];
-#pragma unroll
-        for (int q = 0; q < kFewSteps; ++q)
-            if (s0 + q < s1) {
-                a[q] = *reinterpret_cast<const u32x4*>(wr + 64 * (s0 + q));
-                sa[q] = sr[4 * (s0 + q)];
-            }
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < kFewSteps; ++q)
-            if (s0 + q < s1) acc = mfma16_fp4(a[q], b[q], acc, sa[q], sb[q]);
-        __syncthreads();  // the last item's sums have been read
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave][4 * lk + r][li] = acc[r];
+    int it = blockIdx.x;
+    // an item of the shared expert needs no routing; the waves that pick experts first wait for logits alone
+    const bool early = it < sh * per && !(p.logits && wave < p.T);
+    if (early) issue(it, 1, s0);
+    if (p.logits) {
+        for (int t = wave; t < p.T; t += kFewWaves)
+            route_topk_token(p.logits, p.T, p.E, p.k, p.scoring, p.renorm, m.id, m.w, t);
         __syncthreads();
-        if (threadIdx.x < 8 * kFewT) {
-            const int i = threadIdx.x & 7, t = threadIdx.x >> 3;
-            const int slot = m.slot[g * kFewT + t];
-            if (slot >= 0) {
-                float gs = 0.f, us = 0.f;
+        if (threadIdx.x < S) {
+            const int id = m.id[threadIdx.x];
+            if (blockIdx.x == 0) {
+                p.ids[threadIdx.x] = id;
+                p.topk_w[threadIdx.x] = m.w[threadIdx.x];
+            }
+            m.id[threadIdx.x] = few_local(p, id);
+        }
+    } else if (threadIdx.x < S) {
+        m.id[threadIdx.x] = few_local(p, p.ids[threadIdx.x]);
+    }
+    mx_barrier();
+    const int n = build_few_map<false>(m, nullptr, p);
+    if (!early) issue(it, n, s0);
+
+    // quantised as moe_quantize_mxfp4 does
+    u32x4 b[2 * kFewPairs];
+    uint32_t sb[2 * kFewPairs];
 #pragma unroll
-                for (int w = 0; w < kFewWaves; ++w) {
-                    gs += red[w][i][t];
-                    us += red[w][8 + i][t];
-                }
-                p.a[(size_t)slot * p.I + i0 + i] = silu_mul(gs, us);
+    for (int q = 0; q < 2 * kFewPairs; ++q) {
+        float v[32];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[8 * c + 2 * i] = bf16_lo(raw[q][c][i]);
+                v[8 * c + 2 * i + 1] = bf16_hi(raw[q][c][i]);
+            }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx = max(mx, abs_bits(v[i]));
+        sb[q] = mx_scale_byte(mx);
+        const float inv = mx_inverse(sb[q]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[q][c] = mx_pack8(v + 8 * c, inv);
+    }
+    issue(it + G, n, s1);
+
+    // the intermediate of the item before from the waves' partial sums
+    int prev = -1;
+    auto finish = [&](int par) MX_INLINE {
+        const int i = threadIdx.x & 7, t = threadIdx.x >> 3;
+        const int g = prev / per, i0 = prev % per * 8;
+        const int slot = threadIdx.x < 8 * kFewT && prev >= 0 ? m.slot[g * kFewT + t] : -1;
+        if (slot >= 0) {
+            float gs = 0.f, us = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w) {
+                gs += red[par][w][t][i];
+                us += red[par][w][t][8 + i];
+            }
+            p.a[(size_t)slot * p.I + i0 + i] = silu_mul(gs, us);
+        }
+    };
+    auto body = [&](uint8_t (&st)[kFewWaves][kGuStage], auto par_c) MX_INLINE {
+        constexpr int par = decltype(par_c)::value;
+        wait_vmcnt<kGuLoads>();  // this item has landed; the next one may fly
+        finish(par ^ 1);
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        u32x4 sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            sc[i] = *reinterpret_cast<const u32x4*>(st[wave] + kGuCodes + li * 8 * kFewPairs + 16 * i);
+#pragma unroll
+        for (int j = 0; j < kFewPairs; ++j) {
+            const uint32_t own = j < cnt ? ~0u : 0u;  // zeros times 2^-127 in the steps past this wave's
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const u32x4 a = *reinterpret_cast<const u32x4*>(st[wave] + j * 2048 + few_at(li, 4 * u + lk));
+                acc = mfma16_fp4(a, b[2 * j + u], acc, (sc[j >> 1][2 * (j & 1) + u] >> (8 * lk)) & own, sb[2 * j + u]);
             }
         }
+        *reinterpret_cast<f32x4*>(&red[par][wave][li][4 * lk]) = acc;
+        mx_barrier();
+        issue(it + 2 * G, n, st);
+        prev = it;
+        it += G;
+    };
+    const int n_items = n * per;
+    if (it < n_items) {
+        int par;
+        for (;;) {
+            body(s0, std::integral_constant<int, 0>{});
+            par = 0;
+            if (it >= n_items) break;
+            body(s1, std::integral_constant<int, 1>{});
+            par = 1;
+            if (it >= n_items) break;
+        }
+        finish(par);
     }
+    wait_vmcnt<0>();
 }
 
-constexpr int kFewCols = 32;  // output columns per workgroup of the down kernel
+// ---------------------------------------------------------------- down + combine
+constexpr int kDnCols = 32;                        // output columns of a workgroup, at most
+constexpr int kDnUnit = kDnCols * 128 + kDnCols * 8;  // 256 of K for each: codes, then scales
+constexpr int kDnLoads = kDnCols / 8 + 1;
+constexpr int kSegK = 256 * kFewWaves;             // a segment of K: one unit per wave
+constexpr int kActPitch = kSegK / 2 + kSegK / kMxBlock + 16;
+constexpr int kActRows = 38;                       // >= kFewT: a group fits
 
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[kFewWaves][kDnUnit];
+    __shared__ __attribute__((aligned(1024))) uint8_t s1[kFewWaves][kDnUnit];
+    __shared__ __attribute__((aligned(1024))) uint8_t s2[kFewWaves][kDnUnit];
+    __shared__ __attribute__((aligned(16))) uint8_t act[kActRows * kActPitch];  // quantised rows of the intermediate
     __shared__ FewMap m;
-    __shared__ float red[kFewWaves][kFewCols][17];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ FewSum fs;
+    static_assert(sizeof(float) * kFewWaves * kDnCols * (kFewT + 1) <= sizeof(act), "the last sums reuse act");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lk = lane >> 4;
-    const int nk = p.I / 128, kb = p.I / kMxBlock;
-    const int h0 = blockIdx.x * kFewCols;
-    const int n = build_few_map(m, p);
-    f32x4 total[2] = {};
-    for (int g = 0; g < n; ++g) {
-        const int e = m.expert[g];
-        const uint8_t* W = (e < 0 ? p.ws2 : p.w2 + (size_t)e * p.H * (p.I / 2)) + (size_t)(h0 + li) * (p.I / 2) + 16 * lk;
-        const uint8_t* Ws = (e < 0 ? p.ws2s : p.w2s + (size_t)e * p.H * kb) + (size_t)(h0 + li) * kb + lk;
-        const int slot = m.slot[g * kFewT + li];
-        const float* ar = p.a + (size_t)max(slot, 0) * p.I + lk * kMxBlock;
-        f32x4 acc[2] = {};
-        for (int s = wave; s < nk; s += kFewWaves) {
-            u32x4 b = {0, 0, 0, 0};
-            uint32_t sb = 127;
-            if (slot >= 0) {
-                float v[32];
-                uint32_t mx = 0;
+    const int rowb = p.I / 2, kb = p.I / kMxBlock, nk = p.I / 128, np = (nk + 1) / 2;
+    const int nseg = (p.I + kSegK - 1) / kSegK;
+    const int h0 = blockIdx.x * p.cols, cols = min(p.cols, p.H - h0);
+    const int S = p.T * p.k, sh = p.has_shared ? 1 : 0;
+    if (threadIdx.x < S) {
+        m.id[threadIdx.x] = few_local(p, p.ids[threadIdx.x]);
+        m.w[threadIdx.x] = p.topk_w[threadIdx.x];
+    }
+    mx_barrier();
+    const int n = build_few_map<true>(m, &fs, p);
+    const int nsg = n * nseg;  // sub-groups: a segment of a group
+
+    // rows past cols are past the descriptors' end and read zeros
+    const uint32_t wv = (uint32_t)((lane >> 3) * rowb + wave * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
+    const uint32_t sv = (uint32_t)((lane >> 1) * kb + wave * 8 + (lane & 1) * 4);
+    auto issue = [&](int sg, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
+        const int g = sg / nseg, seg = sg - g * nseg;
+        const bool on = sg < nsg && kFewWaves * seg + wave < np;
+        const bool shared = g < sh;
+        const int e = shared || !on ? 0 : __builtin_amdgcn_readfirstlane(m.expert[g]);
+        const uint8_t* W = (shared ? p.ws2 : p.w2 + (size_t)e * p.H * rowb) + (size_t)h0 * rowb;
+        const uint8_t* Ws = (shared ? p.ws2s : p.w2s + (size_t)e * p.H * kb) + (size_t)h0 * kb;
+        const __amdgpu_buffer_rsrc_t wd = buffer_rsrc(W, on ? (uint32_t)cols * rowb : 0),
+                                     sd = buffer_rsrc(Ws, on ? (uint32_t)cols * kb : 0);
+        lds_buf4(sd, sv, (uint32_t)seg * (kSegK / kMxBlock), st[wave] + kDnCols * 128);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const f32x4 q = *reinterpret_cast<const f32x4*>(ar + 128 * s + 4 * c);
+        for (int i = 0; i < kDnCols / 8; ++i)
+            lds_buf16(wd, wv, (uint32_t)seg * (kSegK / 2) + (uint32_t)(8 * i * rowb), st[wave] + i * 1024);
+    };
+    issue(0, s0);
+    issue(1, s1);
+    issue(2, s2);
+
+    // act holds the rows of the sub-groups [.., c_end): row_of(sg) - c_row on
+    int c_end = 0, c_row = 0;
+    auto row_of = [&](int sg) MX_INLINE {
+        const int g = sg / nseg;
+        return nseg * fs.pre[g] + (sg - g * nseg) * (sg < nsg ? __popc(m.mask[g]) : 0);
+    };
+    auto refill = [&](int sg) MX_INLINE {
+        mx_barrier();  // the rows before have been read
+        c_row = __builtin_amdgcn_readfirstlane(row_of(sg));
+        // a sub-group has at least one row, so at most kActRows < 64 of them fit
+        const int to = min(sg + 1 + lane, nsg);
+        const uint64_t fit = __ballot(sg + 1 + lane <= nsg && row_of(to) - c_row <= kActRows);
+        c_end = sg + __popcll(fit);
+        const int rows = __builtin_amdgcn_readfirstlane(row_of(c_end)) - c_row;
+        constexpr int kBatch = 3;
+        for (int r0 = wave; r0 < rows; r0 += kBatch * kFewWaves) {
+            f32x4 v[kBatch][8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[4 * c + i] = q[i];
+            for (int q = 0; q < kBatch; ++q) {
+                const int r = r0 + q * kFewWaves;
+                if (r < rows) {
+                    const int at = c_row + r, g = fs.pair_group[at / nseg];
+                    const int rem = at - nseg * fs.pre[g], c = __popc(m.mask[g]);
+                    const int seg = rem / c, slot = fs.pair_slot[fs.pre[g] + rem - seg * c];
+                    const int blk = seg * (kSegK / kMxBlock) + lane;
+                    if (blk < kb) {
+                        const f32x4* src = reinterpret_cast<const f32x4*>(p.a + (size_t)slot * p.I + blk * kMxBlock);
+#pragma unroll
+                        for (int c8 = 0; c8 < 8; ++c8) v[q][c8] = src[c8];
+                    } else {
+#pragma unroll
+                        for (int c8 = 0; c8 < 8; ++c8) v[q][c8] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mx = max(mx, abs_bits(v[i]));
-                sb = mx_scale_byte(mx);
-                const float inv = mx_inverse(sb);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) b[c] = mx_pack8(v + 8 * c, inv);
             }
 #pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int r = r0 + q * kFewWaves;
+                if (r < rows) {
+                    float f[32];
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        f[i] = v[q][i >> 2][i & 3];
+                        mx = max(mx, abs_bits(f[i]));
+                    }
+                    const uint32_t sb = mx_scale_byte(mx);
+                    const float inv = mx_inverse(sb);
+                    u32x4 code;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) code[c] = mx_pack8(f + 8 * c, inv);
+                    *reinterpret_cast<u32x4*>(&act[r * kActPitch + lane * 16]) = code;
+                    act[r * kActPitch + kSegK / 2 + lane] = (uint8_t)sb;
+                }
+            }
+        }
+        wait_vmcnt<0>();  // said once here, or the compiler says it before every unit's reads
+        mx_barrier();
+    };
+
+    f32x4 total[2] = {};
+    auto body = [&](int sg, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
+        if (sg == c_end) refill(sg);
+        wait_vmcnt<2 * kDnLoads>();  // this unit has landed; the next two may fly
+        const int g = sg / nseg, seg = sg - g * nseg;
+        const int left = nk - 2 * (kFewWaves * seg + wave);  // halves of this wave's unit that are there
+        const uint32_t mask = m.mask[g];
+        const bool on = left > 0 && mask >> li & 1;
+        const int sg_row = row_of(sg) - c_row;
+        const float w = fs.weight[g * kFewT + li];
+        // a column that nobody picked multiplies row 0's values and is dropped
+        const int row = on ? sg_row + __popc(mask & ((1u << li) - 1)) : 0;
+        const uint8_t* ar = act + row * kActPitch;
+        const uint64_t as = *reinterpret_cast<const uint64_t*>(ar + kSegK / 2 + 8 * wave) >> (8 * lk);
+        f32x4 acc[2] = {};
+        uint64_t ws[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            ws[q] = *reinterpret_cast<const uint64_t*>(st[wave] + kDnCols * 128 + (16 * q + li) * 8) >> (8 * lk);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            // past the end of K: scales of 2^-127 on both sides, and the codes are numbers whatever they are
+            const uint32_t own = u < left ? 0xffu : 0u;
+            const u32x4 b = *reinterpret_cast<const u32x4*>(ar + (8 * wave + 4 * u + lk) * 16);
+            const uint32_t sb = (uint32_t)(as >> (32 * u)) & own;
+#pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(W + (size_t)16 * q * (p.I / 2) + 64 * s);
-                const uint32_t sa = Ws[(size_t)16 * q * kb + 4 * s];
-                acc[q] = mfma16_fp4(a, b, acc[q], sa, sb);
+                const u32x4 a = *reinterpret_cast<const u32x4*>(st[wave] + few_at(16 * q + li, 4 * u + lk));
+                acc[q] = mfma16_fp4(a, b, acc[q], (uint32_t)(ws[q] >> (32 * u)) & own, sb);
             }
         }
         // a token that did not pick this expert takes nothing from it, not even a NaN
-        const float w = m.weight[g * kFewT + li];
-        if (slot >= 0) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) total[q][r] = __builtin_fmaf(w, acc[q][r], total[q][r]);
-        }
+            for (int r = 0; r < 4; ++r) total[q][r] = on ? __builtin_fmaf(w, acc[q][r], total[q][r]) : total[q][r];
+        asm volatile("" ::: "memory");
+        wait_lds();  // this stage has been read
+        asm volatile("" ::: "memory");
+        issue(sg + 3, st);
+    };
+    refill(0);
+    for (int sg = 0; sg < nsg;) {
+        body(sg, s0);
+        if (++sg >= nsg) break;
+        body(sg, s1);
+        if (++sg >= nsg) break;
+        body(sg, s2);
+        ++sg;
     }
+    wait_vmcnt<0>();
+    mx_barrier();  // act is free
+    float(*red)[kDnCols][kFewT + 1] = reinterpret_cast<float(*)[kDnCols][kFewT + 1]>(act);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int r = 0; r < 4; ++r) red[wave][16 * q + 4 * lk + r][li] = total[q][r];
     __syncthreads();
     const int c = threadIdx.x & 31, t = threadIdx.x >> 5;
-    if (t < p.T) {
+    if (t < p.T && c < cols) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kFewWaves; ++w) s += red[w][c][t];
@@ -253,7 +496,6 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
 }
 
 struct FewWs {
-    uint32_t* sync;
     float* logits;
     float* a;
     size_t bytes;
@@ -267,7 +509,6 @@ FewWs carve_few(const moe_expert_weights* w, int T, int E, int k, void* base) {
         return base ? (void*)((uint8_t*)base + o) : nullptr;
     };
     FewWs r{};
-    r.sync = (uint32_t*)take(256);
     r.logits = (float*)take((size_t)T * E * 4);
     r.a = (float*)take(((size_t)T * k + T) * w->I * 4);
     r.bytes = off;
@@ -285,16 +526,19 @@ moe_status launch_layer_few(const void* x, const void* w_router, const float* bi
                             float* topk_w, void* out, void* ws, hipStream_t st) {
     const FewWs s = carve_few(w, T, E, k, ws);
     if (w_router) {
-        const moe_status r = launch_route(x, w_router, bias, MOE_BF16, T, w->H, E, k, scoring, renorm, s.logits,
-                                          topk_ids, topk_w, st);
+        const moe_status r = launch_route_logits_rows(x, w_router, bias, T, w->H, E, s.logits, st);
         if (r) return r;
     }
     FewArgs p{};
     p.x = (const uint16_t*)x;
+    p.logits = w_router ? s.logits : nullptr;
     p.ids = topk_ids;
     p.topk_w = topk_w;
     p.T = T;
     p.k = k;
+    p.E = E;
+    p.scoring = scoring;
+    p.renorm = renorm;
     p.H = w->H;
     p.I = w->I;
     p.base = base;
@@ -310,10 +554,14 @@ moe_status launch_layer_few(const void* x, const void* w_router, const float* bi
     p.ws2s = (const uint8_t*)w->ws2_scale;
     p.a = s.a;
     p.out = (uint16_t*)out;
-    hipLaunchKernelGGL(few_gate_up_kernel, dim3(device_info().cu_count), dim3(kFewThreads), 0, st, p);
+    const int cu = device_info().cu_count;
+    // 8 columns are one load: as many workgroups as the CUs, or 32 columns each
+    p.cols = std::min(kDnCols, (int)align_up((size_t)(w->H + cu - 1) / cu, 8));
+    const long items = ((long)std::min(T * k, w->E_local) + p.has_shared) * (w->I / 8);
+    hipLaunchKernelGGL(few_gate_up_kernel, dim3((int)std::min<long>(cu, items)), dim3(kFewThreads), 0, st, p);
     const moe_status r = check_launch("few_gate_up_kernel");
     if (r) return r;
-    hipLaunchKernelGGL(few_down_kernel, dim3(w->H / kFewCols), dim3(kFewThreads), 0, st, p);
+    hipLaunchKernelGGL(few_down_kernel, dim3((w->H + p.cols - 1) / p.cols), dim3(kFewThreads), 0, st, p);
     return check_launch("few_down_kernel");
 }
 

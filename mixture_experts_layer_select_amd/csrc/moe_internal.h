@@ -76,6 +76,9 @@ moe_status check_launch(const char* what);
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- launchers
+// bf16 logits of a few tokens, bit for bit launch_route's; H % 8 == 0, H <= 8192
+moe_status launch_route_logits_rows(const void* x, const void* w, const float* bias, int T, int H, int E,
+                                    float* logits, hipStream_t st);
 moe_status launch_route(const void* x, const void* w, const float* bias, moe_dtype dt, int T, int H,
                         int E, int k, int scoring, int renorm, float* logits, int32_t* ids,
                         float* topk_w, hipStream_t st);

@@ -187,17 +187,6 @@ __device__ __forceinline__ int mx_row_of(int rho) { return 16 * ((rho >> 2) & 1)
 __device__ __forceinline__ int mx_swz_w(int q) { return ((q & 3) ^ ((q >> 2) & 1)) | ((q >> 4) & 1) << 2; }
 __device__ __forceinline__ int mx_swz_x(int q) { return (q & 7) ^ ((q >> 3) & 1); }
 
-// a large kernel's lambdas are otherwise left as calls with their captures in memory
-#define MX_INLINE __attribute__((always_inline))
-
-// The workgroup barrier of the load ring: this wave's LDS reads are done and no
-// memory access moves across it at compile time, but loads stay in flight.
-__device__ __forceinline__ void mx_barrier() {
-    asm volatile("" ::: "memory");
-    barrier_only();
-    asm volatile("" ::: "memory");
-}
-
 struct MxGemm {
     const uint8_t* x;         // activation codes, rows of K/2 bytes
     const uint8_t* xs;        // their scales, rows of K/32 bytes

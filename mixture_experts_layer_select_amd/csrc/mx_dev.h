@@ -10,7 +10,7 @@
 // with a NaN or an infinity has byte 255 (NaN in E8M0) and codes 0.
 #pragma once
 
-#include "moe_internal.h"
+#include "ffn_dev.h"
 
 namespace moe {
 namespace {
@@ -67,6 +67,17 @@ __device__ __forceinline__ f32x16 mfma_fp4(u32x4 a, u32x4 b, f32x16 c, uint32_t 
     const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
     const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, kByteA, (int)sa, kByteB, (int)sb);
+}
+
+// a large kernel's lambdas are otherwise left as calls with their captures in memory
+#define MX_INLINE __attribute__((always_inline))
+
+// The workgroup barrier of the load ring: this wave's LDS reads are done and no
+// memory access moves across it at compile time, but loads stay in flight.
+__device__ __forceinline__ void mx_barrier() {
+    asm volatile("" ::: "memory");
+    barrier_only();
+    asm volatile("" ::: "memory");
 }
 
 }  // namespace

@@ -471,18 +471,23 @@ __global__ __launch_bounds__(256) void route_refine_kernel(const uint16_t* __res
 #endif
 constexpr int kRowsMaxT = MOE_ROUTE_ROWS_MAX_T;
 
+moe_status launch_route_logits_rows(const void* x, const void* w, const float* bias, int T, int H, int E,
+                                    float* logits, hipStream_t st) {
+    const int nsteps = (H + kStep - 1) / kStep;
+    auto kern = nsteps <= 4    ? route_logits_rows_kernel<4>
+                : nsteps <= 8  ? route_logits_rows_kernel<8>
+                : nsteps <= 14 ? route_logits_rows_kernel<14>
+                               : route_logits_rows_kernel<16>;
+    hipLaunchKernelGGL(kern, dim3((E + 3) / 4, T), dim3(256), 0, st, (const uint16_t*)x,
+                       (const uint16_t*)w, bias, H, E, logits);
+    return check_launch("route_logits_rows_kernel");
+}
+
 moe_status launch_route(const void* x, const void* w, const float* bias, moe_dtype dt, int T, int H,
                         int E, int k, int scoring, int renorm, float* logits, int32_t* ids,
                         float* topk_w, hipStream_t st) {
     if (dt == MOE_BF16 && T <= kRowsMaxT && H % 8 == 0 && H <= 16 * kStep) {
-        const int nsteps = (H + kStep - 1) / kStep;
-        auto kern = nsteps <= 4    ? route_logits_rows_kernel<4>
-                    : nsteps <= 8  ? route_logits_rows_kernel<8>
-                    : nsteps <= 14 ? route_logits_rows_kernel<14>
-                                   : route_logits_rows_kernel<16>;
-        hipLaunchKernelGGL(kern, dim3((E + 3) / 4, T), dim3(256), 0, st, (const uint16_t*)x,
-                           (const uint16_t*)w, bias, H, E, logits);
-        moe_status s = check_launch("route_logits_rows_kernel");
+        moe_status s = launch_route_logits_rows(x, w, bias, T, H, E, logits, st);
         if (s != MOE_OK) return s;
         hipLaunchKernelGGL(route_topk_kernel, dim3((T + 3) / 4), dim3(256), 0, st, logits, T, E, k,
                            scoring, renorm, ids, topk_w);

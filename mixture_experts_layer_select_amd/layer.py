@@ -246,12 +246,11 @@ class MoELayer:
                 and (self.router is None or E <= 256))
 
     def few_workspace(self, T: int) -> torch.Tensor:
-        """forward_few's workspace for T tokens, zeroed once at allocation
-        (its first 256 bytes must start at zero; every call leaves them so)."""
+        """forward_few's workspace for T tokens."""
         key = ("few", T)
         if key not in self._bufs:
             n = L.moe_layer_few_workspace_size(self.weights, T, self._n_experts(), self.k)
-            self._bufs[key] = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.w13.device)
+            self._bufs[key] = torch.empty(max(n, 256), dtype=torch.uint8, device=self.w13.device)
         return self._bufs[key]
 
     def _n_experts(self) -> int:

@@ -45,14 +45,12 @@ def few(ex, x, ids=None, w=None, router=None, bias=None, k=None, E=None, base=0,
     k = ids.shape[1] if ids is not None else k
     if ws is None:
         ws = torch.full((L.moe_layer_few_workspace_size(ex.w, T, E, k),), 0xFF, dtype=torch.uint8, device=DEV)
-        ws[:256] = 0
     i = torch.full((T, k), -7, dtype=torch.int32, device=DEV) if ids is None else ids.to(torch.int32).to(DEV)
     v = torch.zeros((T, k), device=DEV) if w is None else w.to(DEV)
     out = torch.full((T, H), 9.0, dtype=torch.bfloat16, device=DEV)
     L.moe_layer_few(x.to(DEV), router, bias, T, E, k, L.SIGMOID if scoring is None else scoring, renorm, ex.w, base, i, v,
                     out, ws, ws.numel())
     torch.cuda.synchronize()
-    assert int(ws[:256].long().sum()) == 0, "the first 256 bytes are not zero after the call"
     return i.cpu(), v.cpu(), out
 
 
