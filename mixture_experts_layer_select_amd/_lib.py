@@ -117,9 +117,7 @@ def _ptr(t):
     """Raw pointer of a tensor (or an int address). The library reads every
     buffer as dense row-major memory, so a strided view is refused rather
     than read as raw memory."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     if not t.is_contiguous():
         raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not "
@@ -141,8 +139,8 @@ def expect(t, name: str, dtypes, device=None):
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle itself: a Stream object made per call costs more than the launch it is for
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -267,23 +265,29 @@ def moe_combine(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shar
 
 
 def _here(*tensors):
-    """The calls launch on the current device: refuse tensors of another one."""
-    dev = torch.cuda.current_device() if any(isinstance(t, torch.Tensor) for t in tensors) else None
+    """Raw pointers, as _ptr gives them. The calls launch on the current
+    device: tensors of another one are refused."""
+    dev, out = None, []
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+        if isinstance(t, torch.Tensor):
+            if dev is None:
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev:
+                raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+            out.append(t.data_ptr() if t.is_contiguous() else _ptr(t))
+        else:
+            out.append(t)
+    return out
 
 
 def moe_quantize_mxfp4(x, x_dt, rows, cols, codes, scales, stream=None):
-    _here(x, codes, scales)
-    _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
-        _ptr(x), x_dt, rows, cols, _ptr(codes), _ptr(scales), _stream(stream)))
+    x, codes, scales = _here(x, codes, scales)
+    _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(x, x_dt, rows, cols, codes, scales, _stream(stream)))
 
 
 def moe_dequantize_mxfp4(codes, scales, rows, cols, out, out_dt, stream=None):
-    _here(codes, scales, out)
-    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(
-        _ptr(codes), _ptr(scales), rows, cols, _ptr(out), out_dt, _stream(stream)))
+    codes, scales, out = _here(codes, scales, out)
+    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(codes, scales, rows, cols, out, out_dt, _stream(stream)))
 
 
 def moe_layer_few_workspace_size(w: moe_expert_weights, T, E, k) -> int:
@@ -292,24 +296,25 @@ def moe_layer_few_workspace_size(w: moe_expert_weights, T, E, k) -> int:
 
 def moe_layer_few(x, w_router, bias, T, E, k, scoring, renormalize, w: moe_expert_weights, expert_base, topk_ids,
                   topk_w, out, workspace, ws_bytes, stream=None):
-    _here(x, w_router, bias, topk_ids, topk_w, out, workspace)
+    x, w_router, bias, topk_ids, topk_w, out, workspace = _here(x, w_router, bias, topk_ids, topk_w, out, workspace)
     _check("moe_layer_few", lib().moe_layer_few(
-        _ptr(x), _ptr(w_router), _ptr(bias), T, E, k, scoring, int(bool(renormalize)), C.byref(w), expert_base,
-        _ptr(topk_ids), _ptr(topk_w), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)))
+        x, w_router, bias, T, E, k, scoring, int(bool(renormalize)), C.byref(w), expert_base, topk_ids, topk_w, out,
+        workspace, ws_bytes, _stream(stream)))
 
 
 def moe_pre_norm(x, delta, delta_scale, gain, eps, dt, T, H, h_out, n_out, stream=None):
-    _here(x, delta, gain, h_out, n_out)
-    _check("moe_pre_norm", lib().moe_pre_norm(
-        _ptr(x), _ptr(delta), delta_scale, _ptr(gain), eps, dt, T, H, _ptr(h_out), _ptr(n_out), _stream(stream)))
+    x, delta, gain, h_out, n_out = _here(x, delta, gain, h_out, n_out)
+    _check("moe_pre_norm", lib().moe_pre_norm(x, delta, delta_scale, gain, eps, dt, T, H, h_out, n_out,
+                                              _stream(stream)))
 
 
 def moe_combine_norm(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, gain, eps, gate,
                      gate_rows, alpha, residual, out, out_dt, stream=None):
-    _here(y_perm, slot_to_row, topk_w, expert_offsets, gain, gate, residual, out)
+    y_perm, slot_to_row, topk_w, expert_offsets, gain, gate, residual, out = _here(
+        y_perm, slot_to_row, topk_w, expert_offsets, gain, gate, residual, out)
     _check("moe_combine_norm", lib().moe_combine_norm(
-        _ptr(y_perm), y_dt, _ptr(slot_to_row), _ptr(topk_w), T, k, H, _ptr(expert_offsets), shared_group,
-        _ptr(gain), eps, _ptr(gate), gate_rows, alpha, _ptr(residual), _ptr(out), out_dt, _stream(stream)))
+        y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, gain, eps, gate, gate_rows, alpha,
+        residual, out, out_dt, _stream(stream)))
 
 
 def moe_balanced_partition(counts, E, G, new_to_old, old_to_new, group_loads):
