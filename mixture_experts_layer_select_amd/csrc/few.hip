@@ -36,6 +36,7 @@ constexpr int kFewT = 16;      // tokens: the columns of one MFMA
 constexpr int kFewK = 8;       // picks per token
 constexpr int kFewSlots = kFewT * kFewK;
 constexpr int kFewGroups = kFewSlots + 1;
+constexpr int kFewMaxE = 512;  // local experts: checked by the C entry
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / 64;
 constexpr int kFewPairs = 4;   // K steps of 256 per wave of the gate/up kernel: H <= 8192
@@ -55,9 +56,9 @@ struct FewArgs {
 // The groups: the shared expert (if any), then the distinct local experts among
 // the picks, ascending.
 struct FewMap {
-    __attribute__((aligned(16))) int id[kFewSlots];   // local expert of a slot, -1: none
-    __attribute__((aligned(16))) int key[kFewSlots];  // the expert at its first slot, INT_MAX elsewhere
-    float w[kFewSlots];
+    __attribute__((aligned(16))) uint32_t hit[kFewMaxE / 32];  // the local experts among the picks
+    int id[kFewSlots + kFewK];           // local expert of a slot, -1: none
+    float w[kFewSlots + kFewK];
     int expert[kFewGroups];              // -1: the shared one
     uint32_t mask[kFewGroups];           // the tokens that picked it
     short slot[kFewGroups * kFewT];      // the first slot of a token that did, -1: none
@@ -74,49 +75,51 @@ __device__ __forceinline__ int few_local(const FewArgs& p, int id) {  // any val
     return id >= p.base && id - p.base < p.E_local ? id - p.base : -1;
 }
 
-// Builds the map from m.id and m.w (S = T k slots, visible to all threads) and
-// returns the number of groups. All threads call; ends with a barrier.
+// Before the barrier behind which m.id (-1 behind the T k slots) and m.w are seen
+template <bool kSum>
+__device__ __forceinline__ void init_few_map(FewMap& m, FewSum* s, const FewArgs& p) {
+    const int tid = threadIdx.x, S = p.T * p.k;
+    if (tid < kFewMaxE / 32) m.hit[tid] = 0;
+    for (int i = tid; i < kFewGroups * kFewT; i += kFewThreads) {
+        m.slot[i] = (short)(p.has_shared && i < p.T ? S + i : -1);
+        if (kSum) s->weight[i] = p.has_shared && i < p.T ? 1.0f : 0.0f;
+    }
+    for (int i = tid; i < kFewGroups; i += kFewThreads) m.mask[i] = p.has_shared && i == 0 ? (1u << p.T) - 1 : 0;
+}
+
+// Builds the map behind that barrier and returns the number of groups. All
+// threads call; ends with a barrier.
 template <bool kSum>
 __device__ __forceinline__ int build_few_map(FewMap& m, FewSum* s, const FewArgs& p) {
-    const int tid = threadIdx.x, S = p.T * p.k, sh = p.has_shared ? 1 : 0;
-    for (int i = tid; i < kFewGroups * kFewT; i += kFewThreads) {
-        m.slot[i] = (short)(sh && i < p.T ? S + i : -1);
-        if (kSum) s->weight[i] = sh && i < p.T ? 1.0f : 0.0f;
-    }
-    for (int i = tid; i < kFewGroups; i += kFewThreads) m.mask[i] = sh && i == 0 ? (1u << p.T) - 1 : 0;
-    if (sh && tid == 0) m.expert[0] = -1;
-    int e = -1;
-    bool first = false, first_of_token = false;
-    if (tid < kFewSlots) {
-        e = tid < S ? m.id[tid] : -1;
-        first = first_of_token = e >= 0;
-        const int t0 = tid - tid % p.k;
-        for (int j = 0; j < min(tid, S); ++j)
-            if (m.id[j] == e) {
-                first = false;
-                if (j >= t0) first_of_token = false;
-            }
-        m.key[tid] = first ? e : 0x7fffffff;
-    }
+    const int tid = threadIdx.x, sh = p.has_shared ? 1 : 0;
+    const int e = tid < kFewSlots ? m.id[tid] : -1;
+    if (e >= 0) atomicOr(&m.hit[e >> 5], 1u << (e & 31));
     mx_barrier();
-    int n = sh, rank = sh;
-    for (int j = 0; j < S; j += 4) {  // the slots from S on hold INT_MAX
-        const i32x4 key = *reinterpret_cast<const i32x4*>(&m.key[j]);
+    int n = sh, rank = sh;  // an expert's rank: the hit ones below it
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            n += key[i] != 0x7fffffff;
-            rank += key[i] < e;
-        }
+    for (int w = 0; w < kFewMaxE / 32; ++w) {
+        const uint32_t hit = m.hit[w];
+        const int below = min(max(e - 32 * w, 0), 32);
+        rank += __popc(below < 32 ? hit & ((1u << below) - 1) : hit);
+        n += __popc(hit);
     }
-    if (first) m.expert[rank] = e;
-    if (first_of_token) {
-        const int t = tid / p.k;
+    if (tid == 0 && sh) m.expert[0] = -1;
+    if (e >= 0) {
+        const int t = tid / p.k, j0 = tid - t * p.k;
+        bool first = true;  // of its token's picks
         float w = 0.f;
-        for (int j = t * p.k + p.k - 1; j >= tid; --j)
-            if (m.id[j] == e) w += m.w[j];
-        m.slot[rank * kFewT + t] = (short)tid;
-        if (kSum) s->weight[rank * kFewT + t] = w;
-        atomicOr(&m.mask[rank], 1u << t);
+#pragma unroll
+        for (int j = kFewK - 1; j >= 0; --j) {
+            const bool same = j < p.k && m.id[tid - j0 + j] == e;
+            if (same && j < j0) first = false;
+            if (kSum && same) w += m.w[tid - j0 + j];
+        }
+        m.expert[rank] = e;
+        if (first) {
+            m.slot[rank * kFewT + t] = (short)tid;
+            if (kSum) s->weight[rank * kFewT + t] = w;
+            atomicOr(&m.mask[rank], 1u << t);
+        }
     }
     mx_barrier();
     n = __builtin_amdgcn_readfirstlane(n);
@@ -162,6 +165,14 @@ __device__ __forceinline__ f32x4 mfma16_fp4(u32x4 a, u32x4 b, f32x4 c, uint32_t 
 // so the 16 rows of one MFMA operand spread over the banks
 __device__ __forceinline__ uint32_t few_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// A byte offset of which the compiler knows nothing. A direct load to LDS
+// counts as a store of one lane's bytes at its first address; a read that is
+// proven apart from every such store is made to wait for all loads in flight.
+__device__ __forceinline__ uint32_t few_opaque(uint32_t v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
 // ---------------------------------------------------------------- gate/up
 constexpr int kGuCodes = 16 * 128 * kFewPairs;  // a wave's share of one item
 constexpr int kGuStage = kGuCodes + 16 * 8 * kFewPairs;  // ... and its scales
@@ -202,64 +213,74 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
             lds_buf16(wd, wv, j * 128, st[wave] + j * 2048);
             lds_buf16(wd, wv, j * 128 + up, st[wave] + j * 2048 + 1024);
         }
+        asm volatile("" ::: "memory");  // loads of different stages stay in order: the waits count them
     };
 
-    u32x4 raw[2 * kFewPairs][4];  // the tokens: lane (li, lk) holds token li's block lk of each half step
-    {
-        const __amdgpu_buffer_rsrc_t xd = buffer_rsrc(p.x, (uint32_t)(p.T * p.H * 2));  // rows past T are zeros
-#pragma unroll
-        for (int q = 0; q < 2 * kFewPairs; ++q) {
-            const uint32_t at = q < 2 * cnt ? (uint32_t)(li * p.H + (2 * p0 + q) * 128 + lk * kMxBlock) * 2 : 0xffffff00u;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) raw[q][c] = buffer_load16(xd, at, 16 * c);
-        }
-    }
     int it = blockIdx.x;
-    // an item of the shared expert needs no routing; the waves that pick experts first wait for logits alone
+    // an item of the shared expert needs no routing; a wave that picks experts waits for its logits alone first
     const bool early = it < sh * per && !(p.logits && wave < p.T);
     if (early) issue(it, 1, s0);
-    if (p.logits) {
+    if (p.logits)
         for (int t = wave; t < p.T; t += kFewWaves)
-            route_topk_token(p.logits, p.T, p.E, p.k, p.scoring, p.renorm, m.id, m.w, t);
-        __syncthreads();
-        if (threadIdx.x < S) {
-            const int id = m.id[threadIdx.x];
-            if (blockIdx.x == 0) {
-                p.ids[threadIdx.x] = id;
-                p.topk_w[threadIdx.x] = m.w[threadIdx.x];
+            route_topk_token<1>(p.logits, p.T, p.E, p.k, p.scoring, p.renorm, m.id, m.w, t);
+    // The tokens, quantised as moe_quantize_mxfp4 does, eight values per thread, into the stage that is filled last:
+    // codes, then scales. (A lane that reads a block of its own costs the address unit a line per lane: four times
+    // the time.)
+    uint8_t* const xq = &s1[0][0];
+    const int blocks = p.T * kb;
+    static_assert(kFewT * kFewPairs * kFewWaves * 256 / kMxBlock * 17 <= sizeof(s1), "the tokens fit the stage");
+    const __amdgpu_buffer_rsrc_t xd = buffer_rsrc(p.x, (uint32_t)(p.T * p.H * 2));
+    constexpr int kBatch = 4;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < 4 * blocks; i0 += kBatch * kFewThreads) {
+        u32x4 raw[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) raw[q] = buffer_load16(xd, (uint32_t)(i0 + q * kFewThreads) * 16, 0);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int i = i0 + q * kFewThreads;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = bf16_lo(raw[q][j]);
+                v[2 * j + 1] = bf16_hi(raw[q][j]);
             }
-            m.id[threadIdx.x] = few_local(p, id);
+            uint32_t byte;
+            const uint32_t code = mx_quantise8(v, byte);
+            if (i < 4 * blocks) {
+                *reinterpret_cast<uint32_t*>(xq + i * 4) = code;
+                if ((i & 3) == 0) xq[blocks * 16 + (i >> 2)] = (uint8_t)byte;
+            }
         }
-    } else if (threadIdx.x < S) {
-        m.id[threadIdx.x] = few_local(p, p.ids[threadIdx.x]);
     }
+    init_few_map<false>(m, nullptr, p);
+    if (!p.logits && threadIdx.x < kFewSlots)
+        m.id[threadIdx.x] = threadIdx.x < S ? few_local(p, p.ids[threadIdx.x]) : -1;
     mx_barrier();
-    const int n = build_few_map<false>(m, nullptr, p);
-    if (!early) issue(it, n, s0);
-
-    // quantised as moe_quantize_mxfp4 does
+    // lane (li, lk) holds token li's block lk of each of its wave's half steps; columns past T repeat the last token
     u32x4 b[2 * kFewPairs];
     uint32_t sb[2 * kFewPairs];
 #pragma unroll
     for (int q = 0; q < 2 * kFewPairs; ++q) {
-        float v[32];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[8 * c + 2 * i] = bf16_lo(raw[q][c][i]);
-                v[8 * c + 2 * i + 1] = bf16_hi(raw[q][c][i]);
-            }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) mx = max(mx, abs_bits(v[i]));
-        sb[q] = mx_scale_byte(mx);
-        const float inv = mx_inverse(sb[q]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) b[q][c] = mx_pack8(v + 8 * c, inv);
+        const int at = min(li, p.T - 1) * kb + min(2 * p0 + q, 2 * np - 1) * 4 + lk;
+        b[q] = *reinterpret_cast<const u32x4*>(xq + at * 16);
+        sb[q] = xq[blocks * 16 + at] & (q < 2 * cnt ? 0xffu : 0u);
     }
+    if (p.logits && threadIdx.x < kFewSlots) {
+        const int id = threadIdx.x < S ? m.id[threadIdx.x] : -1;
+        if (blockIdx.x == 0 && threadIdx.x < S) {
+            p.ids[threadIdx.x] = id;
+            p.topk_w[threadIdx.x] = m.w[threadIdx.x];
+        }
+        m.id[threadIdx.x] = threadIdx.x < S ? few_local(p, id) : -1;
+    }
+    mx_barrier();
+    const int n = build_few_map<false>(m, nullptr, p);
+    if (!early) issue(it, n, s0);
+    wait_vmcnt<0>();  // said once here, or the compiler says it in the loop, before the first stage's reads
     issue(it + G, n, s1);
 
+    const uint32_t srow = few_opaque(kGuCodes + li * 8 * kFewPairs);
     // the intermediate of the item before from the waves' partial sums
     int prev = -1;
     auto finish = [&](int par) MX_INLINE {
@@ -284,7 +305,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
         u32x4 sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            sc[i] = *reinterpret_cast<const u32x4*>(st[wave] + kGuCodes + li * 8 * kFewPairs + 16 * i);
+            sc[i] = *reinterpret_cast<const u32x4*>(st[wave] + srow + 16 * i);
 #pragma unroll
         for (int j = 0; j < kFewPairs; ++j) {
             const uint32_t own = j < cnt ? ~0u : 0u;  // zeros times 2^-127 in the steps past this wave's
@@ -339,19 +360,21 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     const int nseg = (p.I + kSegK - 1) / kSegK;
     const int h0 = blockIdx.x * p.cols, cols = min(p.cols, p.H - h0);
     const int S = p.T * p.k, sh = p.has_shared ? 1 : 0;
-    if (threadIdx.x < S) {
-        m.id[threadIdx.x] = few_local(p, p.ids[threadIdx.x]);
-        m.w[threadIdx.x] = p.topk_w[threadIdx.x];
+    init_few_map<true>(m, &fs, p);
+    if (threadIdx.x < kFewSlots) {
+        m.id[threadIdx.x] = threadIdx.x < S ? few_local(p, p.ids[threadIdx.x]) : -1;
+        m.w[threadIdx.x] = threadIdx.x < S ? p.topk_w[threadIdx.x] : 0.f;
     }
     mx_barrier();
     const int n = build_few_map<true>(m, &fs, p);
     const int nsg = n * nseg;  // sub-groups: a segment of a group
+    auto group_of = [&](int sg) MX_INLINE { return nseg == 1 ? sg : sg / nseg; };
 
     // rows past cols are past the descriptors' end and read zeros
     const uint32_t wv = (uint32_t)((lane >> 3) * rowb + wave * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
     const uint32_t sv = (uint32_t)((lane >> 1) * kb + wave * 8 + (lane & 1) * 4);
     auto issue = [&](int sg, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
-        const int g = sg / nseg, seg = sg - g * nseg;
+        const int g = group_of(sg), seg = sg - g * nseg;
         const bool on = sg < nsg && kFewWaves * seg + wave < np;
         const bool shared = g < sh;
         const int e = shared || !on ? 0 : __builtin_amdgcn_readfirstlane(m.expert[g]);
@@ -363,76 +386,87 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
 #pragma unroll
         for (int i = 0; i < kDnCols / 8; ++i)
             lds_buf16(wd, wv, (uint32_t)seg * (kSegK / 2) + (uint32_t)(8 * i * rowb), st[wave] + i * 1024);
+        asm volatile("" ::: "memory");  // loads of different stages stay in order: the waits count them
     };
-    issue(0, s0);
-    issue(1, s1);
-    issue(2, s2);
-
     // act holds the rows of the sub-groups [.., c_end): row_of(sg) - c_row on
     int c_end = 0, c_row = 0;
     auto row_of = [&](int sg) MX_INLINE {
-        const int g = sg / nseg;
+        const int g = group_of(sg);
         return nseg * fs.pre[g] + (sg - g * nseg) * (sg < nsg ? __popc(m.mask[g]) : 0);
     };
-    auto refill = [&](int sg) MX_INLINE {
-        mx_barrier();  // the rows before have been read
+    // The rows from sub-group sg on, as many whole sub-groups as fit, eight values per thread at a time. begin() loads
+    // the first ones.
+    int rows = 0;
+    constexpr int kBatch = 4, kEights = kSegK / 8;
+    f32x4 v[kBatch][2];
+    const __amdgpu_buffer_rsrc_t ad = buffer_rsrc(p.a, (uint32_t)((S + p.T) * p.I * 4));
+    const int e8 = threadIdx.x % kEights;
+    auto load_rows = [&](int r0) MX_INLINE {  // zeros past the last row and past I
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int r = r0 + q * (kFewThreads / kEights);
+            int pair = c_row + min(r, max(rows - 1, 0)), seg = 0;
+            if (nseg > 1) {
+                const int g = fs.pair_group[pair / nseg], rem = pair - nseg * fs.pre[g], c = max(__popc(m.mask[g]), 1);
+                seg = rem / c;
+                pair = fs.pre[g] + rem - seg * c;
+            }
+            const int k0 = seg * kSegK + e8 * 8;
+            const uint32_t off = r < rows && k0 < p.I ? (uint32_t)(fs.pair_slot[pair] * p.I + k0) * 4 : 0xffffff00u;
+            v[q][0] = __builtin_bit_cast(f32x4, buffer_load16(ad, off, 0));
+            v[q][1] = __builtin_bit_cast(f32x4, buffer_load16(ad, off, 16));
+        }
+    };
+    auto begin = [&](int sg) MX_INLINE {
         c_row = __builtin_amdgcn_readfirstlane(row_of(sg));
         // a sub-group has at least one row, so at most kActRows < 64 of them fit
         const int to = min(sg + 1 + lane, nsg);
         const uint64_t fit = __ballot(sg + 1 + lane <= nsg && row_of(to) - c_row <= kActRows);
         c_end = sg + __popcll(fit);
-        const int rows = __builtin_amdgcn_readfirstlane(row_of(c_end)) - c_row;
-        constexpr int kBatch = 3;
-        for (int r0 = wave; r0 < rows; r0 += kBatch * kFewWaves) {
-            f32x4 v[kBatch][8];
+        rows = __builtin_amdgcn_readfirstlane(row_of(c_end)) - c_row;
+        load_rows(threadIdx.x / kEights);
+    };
+    auto quantise = [&]() MX_INLINE {
+        mx_barrier();  // the rows before have been read
+#pragma unroll 1
+        for (int r0 = threadIdx.x / kEights; r0 < rows; r0 += kBatch * (kFewThreads / kEights)) {
+            uint32_t code[kBatch], byte[kBatch];
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-                const int r = r0 + q * kFewWaves;
-                if (r < rows) {
-                    const int at = c_row + r, g = fs.pair_group[at / nseg];
-                    const int rem = at - nseg * fs.pre[g], c = __popc(m.mask[g]);
-                    const int seg = rem / c, slot = fs.pair_slot[fs.pre[g] + rem - seg * c];
-                    const int blk = seg * (kSegK / kMxBlock) + lane;
-                    if (blk < kb) {
-                        const f32x4* src = reinterpret_cast<const f32x4*>(p.a + (size_t)slot * p.I + blk * kMxBlock);
+                float f[8];
 #pragma unroll
-                        for (int c8 = 0; c8 < 8; ++c8) v[q][c8] = src[c8];
-                    } else {
-#pragma unroll
-                        for (int c8 = 0; c8 < 8; ++c8) v[q][c8] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    }
-                }
+                for (int i = 0; i < 8; ++i) f[i] = v[q][i >> 2][i & 3];
+                code[q] = mx_quantise8(f, byte[q]);
             }
+            load_rows(r0 + kBatch * (kFewThreads / kEights));
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-                const int r = r0 + q * kFewWaves;
+                const int r = r0 + q * (kFewThreads / kEights);
                 if (r < rows) {
-                    float f[32];
-                    uint32_t mx = 0;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        f[i] = v[q][i >> 2][i & 3];
-                        mx = max(mx, abs_bits(f[i]));
-                    }
-                    const uint32_t sb = mx_scale_byte(mx);
-                    const float inv = mx_inverse(sb);
-                    u32x4 code;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) code[c] = mx_pack8(f + 8 * c, inv);
-                    *reinterpret_cast<u32x4*>(&act[r * kActPitch + lane * 16]) = code;
-                    act[r * kActPitch + kSegK / 2 + lane] = (uint8_t)sb;
+                    *reinterpret_cast<uint32_t*>(&act[r * kActPitch + e8 * 4]) = code[q];
+                    if ((e8 & 3) == 0) act[r * kActPitch + kSegK / 2 + (e8 >> 2)] = (uint8_t)byte[q];
                 }
             }
         }
-        wait_vmcnt<0>();  // said once here, or the compiler says it before every unit's reads
+        wait_vmcnt<0>();  // said once here, or the compiler says it in the loop, before its stages' reads
         mx_barrier();
     };
 
+    begin(0);  // ahead of the weights, which would be waited for with it
+    issue(0, s0);
+    issue(1, s1);
+    issue(2, s2);
+    quantise();
+
+    const uint32_t srow = few_opaque(kDnCols * 128 + li * 8);
     f32x4 total[2] = {};
     auto body = [&](int sg, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
-        if (sg == c_end) refill(sg);
+        if (sg == c_end) {
+            begin(sg);
+            quantise();
+        }
         wait_vmcnt<2 * kDnLoads>();  // this unit has landed; the next two may fly
-        const int g = sg / nseg, seg = sg - g * nseg;
+        const int g = group_of(sg), seg = sg - g * nseg;
         const int left = nk - 2 * (kFewWaves * seg + wave);  // halves of this wave's unit that are there
         const uint32_t mask = m.mask[g];
         const bool on = left > 0 && mask >> li & 1;
@@ -446,7 +480,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         uint64_t ws[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            ws[q] = *reinterpret_cast<const uint64_t*>(st[wave] + kDnCols * 128 + (16 * q + li) * 8) >> (8 * lk);
+            ws[q] = *reinterpret_cast<const uint64_t*>(st[wave] + srow + 128 * q) >> (8 * lk);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             // past the end of K: scales of 2^-127 on both sides, and the codes are numbers whatever they are
@@ -469,7 +503,6 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         asm volatile("" ::: "memory");
         issue(sg + 3, st);
     };
-    refill(0);
     for (int sg = 0; sg < nsg;) {
         body(sg, s0);
         if (++sg >= nsg) break;

@@ -32,12 +32,6 @@ __device__ __forceinline__ void load_eight<float>(const float* p, float* v) {
     }
 }
 
-template <int kCtrl>
-__device__ __forceinline__ uint32_t dpp_max_u32(uint32_t v) {
-    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false);
-    return o > v ? o : v;
-}
-
 template <typename TIn>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const TIn* __restrict__ x, long n_eight,
                                                           uint32_t* __restrict__ codes,
@@ -45,13 +39,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const TIn* __restrict_
     for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n_eight; i += (long)gridDim.x * 256) {
         float v[8];
         load_eight<TIn>(x + i * 8, v);
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-        m = dpp_max_u32<0xb1>(m);  // lane ^ 1; n_eight is a multiple of 4, so the four lanes run together
-        m = dpp_max_u32<0x4e>(m);  // lane ^ 2
-        const uint32_t byte = mx_scale_byte(m);
-        codes[i] = mx_pack8(v, mx_inverse(byte));
+        uint32_t byte;
+        codes[i] = mx_quantise8(v, byte);  // n_eight is a multiple of 4, so the four lanes run together
         if ((i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
     }
 }

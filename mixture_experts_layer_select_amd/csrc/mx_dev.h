@@ -44,6 +44,24 @@ __device__ __forceinline__ uint32_t mx_pack8(const float* v, float inv) {
     return inv == 0.0f ? 0u : r;
 }
 
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_max_u32(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false);
+    return o > v ? o : v;
+}
+
+// The codes of this lane's eight values of a block that lies in four
+// neighbouring lanes (aligned to 4, all of them active), and the block's scale byte.
+__device__ __forceinline__ uint32_t mx_quantise8(const float* v, uint32_t& byte) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+    m = dpp_max_u32<0xb1>(m);  // lane ^ 1
+    m = dpp_max_u32<0x4e>(m);  // lane ^ 2
+    byte = mx_scale_byte(m);
+    return mx_pack8(v, mx_inverse(byte));
+}
+
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 // two fp32 -> packed bf16, round to nearest even (v_cvt_pk_bf16_f32)

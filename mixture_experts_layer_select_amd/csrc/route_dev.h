@@ -238,7 +238,8 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// selection and weights of token t (one wave); E <= 256, k <= E
+// selection and weights of token t (one wave); E <= 256, k <= E, k <= 64 kPicks
+template <int kPicks = 4>
 __device__ __forceinline__ void route_topk_token(const float* __restrict__ logits, int T, int E, int k,
                                                  int scoring, int renorm, int32_t* __restrict__ ids,
                                                  float* __restrict__ topk_w, int t) {
@@ -248,13 +249,15 @@ __device__ __forceinline__ void route_topk_token(const float* __restrict__ logit
     uint64_t key[4];
     float lv[4];
 #pragma unroll
+    for (int i = 0; i < 4; ++i) lv[i] = l[min(lane + 64 * i, E - 1)];  // no branches: the loads overlap
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         int e = lane + 64 * i;
-        lv[i] = e < E ? l[e] : 0.0f;
+        lv[i] = e < E ? lv[i] : 0.0f;
         key[i] = e < E ? (((uint64_t)ordered_bits(lv[i]) << 32) | (0xffffffffu - (uint32_t)e)) : 0;
     }
-    int my_id[4] = {0, 0, 0, 0};
-    float my_l[4] = {0.f, 0.f, 0.f, 0.f};
+    int my_id[kPicks] = {};
+    float my_l[kPicks] = {};
     float lmax = 0.0f;
     for (int j = 0; j < k; ++j) {
         uint64_t best = key[0];
@@ -271,9 +274,9 @@ __device__ __forceinline__ void route_topk_token(const float* __restrict__ logit
         }
     }
     // weights
-    float num[4], part = 0.0f;
+    float num[kPicks], part = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPicks; ++i) {
         const bool mine = lane + 64 * i < k;
         float v;
         if (scoring == MOE_SIGMOID) v = 1.0f / (1.0f + expf(-my_l[i]));
@@ -294,7 +297,7 @@ __device__ __forceinline__ void route_topk_token(const float* __restrict__ logit
         den = 1.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPicks; ++i) {
         const int j = lane + 64 * i;
         if (j < k) {
             ids[(size_t)t * k + j] = my_id[i];
