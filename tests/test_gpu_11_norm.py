@@ -35,8 +35,8 @@ def rms(v, eps):
     return 1 / torch.sqrt((v * v).mean(1, keepdim=True) + eps)
 
 
-SHAPES = [(1, 1), (3, 7), (2, 64), (5, 100), (1, 2048), (2, 2049), (17, 2056), (3, 7168), (2, 8192), (2, 8200),
-          (1, 16384), (2, 16383), (300, 1280)]
+SHAPES = [(1, 1), (3, 7), (2, 64), (5, 100), (4, 512), (9, 513), (3, 3001), (2, 4096), (2, 4104), (1, 2048), (2, 2049),
+          (17, 2056), (3, 7168), (2, 8192), (2, 8200), (1, 16384), (2, 16383), (300, 1280)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -105,7 +105,8 @@ def test_pre_norm_extremes():
 @pytest.mark.parametrize("T,k,H,shared,parts", [
     (1, 1, 1, False, "ngr"), (3, 2, 7, True, "ngr"), (5, 8, 64, True, "n"), (2, 8, 7168, True, "ngr"),
     (4, 3, 2050, False, "gr"), (2, 256, 128, True, "nr"), (3, 4, 8200, True, "ng"), (1, 2, 16384, False, "ngr"),
-    (130, 8, 1024, True, "ngr"), (6, 9, 520, False, "")])
+    (130, 8, 1024, True, "ngr"), (6, 9, 520, False, ""), (4, 2, 512, True, "ngr"), (3, 2, 3001, True, "ngr"),
+    (2, 3, 4096, False, "nr")])
 def test_combine_norm(T, k, H, shared, parts, y_dt, out_dt):
     """parts: n = post norm, g = gate, r = residual. Every third token has no local pick."""
     L = _lib()
