@@ -295,3 +295,76 @@ def test_nan_of_the_next_row_stays_out_of_an_odd_last_half(R):
     keep[8::16] = False
     assert torch.equal(y[0::2][:, keep], clean[0::2][:, keep].float())
     assert bool(torch.isnan(y[1::2]).all()) and bool(torch.isnan(y[:, 8::16]).all())
+
+
+def test_two_graphs_share_a_workspace():
+    """Quantisation and both products captured twice over one workspace; replays alternate with eager calls."""
+    L = _lib()
+    H, I, T = 768, 384, 150
+    ex = Experts(H, I, 3, True, 17)
+    off = torch.tensor([0, 40, 40, 150, 300], dtype=torch.int32, device=DEV)
+    n = L.moe_expert_ffn_workspace_size(ex.w, 300)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    slots = torch.cat([torch.randperm(T, generator=torch.Generator().manual_seed(1)), T + torch.arange(T)])
+    slots = slots.to(torch.int32).to(DEV)
+
+    class Side:
+        def __init__(self):
+            self.x = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+            self.codes = torch.empty((T, H // 2), dtype=torch.uint8, device=DEV)
+            self.scales = torch.empty((T, H // 32), dtype=torch.uint8, device=DEV)
+            self.y = torch.empty((300, H), dtype=torch.bfloat16, device=DEV)
+
+        def call(self):
+            L.moe_quantize_mxfp4(self.x, L.BF16, T, H, self.codes, self.scales)
+            L.moe_expert_ffn_gate_up_tokens(ex.w, self.codes, self.scales, T, 1, slots, off, 4, 300, ws, n)
+            L.moe_expert_ffn_down(ex.w, off, 4, 300, self.y, ws, n)
+
+    sides = [Side(), Side()]
+    graphs = []
+    for s in sides:
+        s.x.copy_(torch.randn((T, H), generator=torch.Generator().manual_seed(2)))
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            s.call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.call()
+        graphs.append(g)
+    for seed in (5, 6, 7):
+        for i, s in enumerate(sides):
+            s.x.copy_(torch.randn((T, H), generator=torch.Generator().manual_seed(10 * seed + i)))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        got = [s.y.clone() for s in sides]
+        for s, y in zip(sides, got):
+            s.y.fill_(4)
+            s.call()
+            torch.cuda.synchronize()
+            assert torch.equal(s.y.view(torch.int16), y.view(torch.int16))
+
+
+def test_two_streams_with_a_workspace_each():
+    """Calls that overlap on two streams give what they give alone."""
+    L = _lib()
+    ex = Experts(2048, 1024, 4, False, 18)
+    want, state = [], []
+    for i in range(2):
+        R = 300 + 41 * i
+        x, xs, _ = quantized((R, 2048), 1.0, 40 + i)
+        offsets = [0, 20, 160, 160 + i, R]
+        want.append(run_ffn(x, xs, ex, offsets, R))
+        n = L.moe_expert_ffn_workspace_size(ex.w, R)
+        state.append((x, xs, torch.tensor(offsets, dtype=torch.int32, device=DEV), R,
+                      torch.zeros((R, 2048), dtype=torch.bfloat16, device=DEV),
+                      torch.empty(n, dtype=torch.uint8, device=DEV), n, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, xs, off, R, y, ws, n, st in state:
+            L.moe_expert_ffn(ex.w, x, xs, off, 4, R, y, ws, n, st)
+    torch.cuda.synchronize()
+    for w, s in zip(want, state):
+        assert torch.equal(s[4].view(torch.int16), w.view(torch.int16))

@@ -201,3 +201,31 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for (_, want), (_, _, _, o, _) in zip(sides, state):
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("T,k,E,H,I,shared", [
+    (16, 8, 16, 512, 2176, True),    # more (expert, token) rows than are held at a time, two segments of K each
+    (16, 8, 9, 256, 4224, False),    # three segments, the last of one step and a half-filled one
+    (9, 2, 3, 256, 16384, True),     # the widest intermediate
+    (16, 4, 64, 768, 128, True)])
+def test_many_rows_and_segments(T, k, E, H, I, shared):
+    ex = Experts(H, I, E, shared, 31)
+    x = tokens(T, H, 33)
+    g = torch.Generator().manual_seed(T + E)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)])
+    w = torch.rand((T, k), generator=g)
+    _, _, out = few(ex, x, ids, w)
+    want, bound = reference(x, ids, w, ex)
+    check(f"few {T}x{k} of {E}, {H}x{I}", out, want, bound)
+    assert torch.equal(out, few(ex, x, ids, w)[2])
+
+
+def test_most_local_experts():
+    """512 local experts behind a base, picks at both ends of the range and next to it."""
+    ex = Experts(256, 128, 512, True, 32)
+    x = tokens(4, 256, 34)
+    ids = torch.tensor([[100, 611], [99, 612], [611, 610], [131, 132]])
+    w = torch.tensor([[.5, .5], [.4, .6], [.3, .7], [1., 2.]])
+    _, _, out = few(ex, x, ids, w, base=100, E=700)
+    want, bound = reference(x, ids, w, ex, base=100)
+    check("few 512", out, want, bound)
