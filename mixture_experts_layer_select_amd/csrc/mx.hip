@@ -32,6 +32,8 @@ __device__ __forceinline__ void load_eight<float>(const float* p, float* v) {
     }
 }
 
+// Eight values a thread, a block in four neighbouring lanes. Bound by HBM: 4096 x
+// 7168 fp32 take 27 us to quantise and 24 to read back (5.0 and 5.7 TB/s).
 template <typename TIn>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const TIn* __restrict__ x, long n_eight,
                                                           uint32_t* __restrict__ codes,
@@ -83,6 +85,12 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 // 16-byte piece per row and sit in registers for them. A load takes 8 rows of
 // 128 bytes: 16 rows of 64 bytes moved 14 TB/s from L2 where these move 23.
 // An item's first loads are issued before the previous item's epilogue.
+//
+// Measured at H = 7168, I = 2048, 32 experts, random codes (gate/up + down): 16
+// rows an expert 95 + 59 us (5.25 and 4.2 TB/s of weights), 128 rows 122 + 81, 256
+// rows 154 + 110, 512 rows 280 to 300 + 190 to 200 (3.4 and 2.5 PFLOP/s). From 256
+// rows on the loads to LDS bound it: without the products they take 0.96 of the
+// kernel's time on zero codes, the products with their LDS reads alone 0.69.
 //
 // Waves form a 2 x 4 grid: wave (wm, wn) owns the 32-token blocks 2j + wm of
 // the tile and 64 weight rows, as 2 x NX blocks of 32x32 accumulators, NX =
