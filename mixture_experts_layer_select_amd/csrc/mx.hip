@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 
 // ============================================================================ grouped GEMMs
 // Items are (m-tile of at most 256 rows, n-block of 256 weight rows); one
-// workgroup of 8 waves per CU walks them (item_at's order, a contiguous slice
+// workgroup of 8 waves per CU walks them (mx_item_at's order, a contiguous slice
 // per XCD). Both operands of each K step of 256 (128 bytes of a row) arrive in
 // LDS by direct global->LDS loads; the E8M0 scales of two steps come in one
 // 16-byte piece per row and sit in registers for them. A load takes 8 rows of
@@ -118,34 +118,51 @@ struct MxScales {  // two K steps
 
 // Tiles and rows of the groups, built by every workgroup once from the
 // device-resident offsets: first tile (tile_start) and first row (row0, clamped
-// to the buffer) of each group. A group's nt = ceil(m / 256) tiles split its m
-// rows evenly. Looked up from LDS alone, since every item's start waits for it.
+// to the buffer) of each group. A group's nt = ceil(m / height) tiles split its
+// m rows evenly. Looked up from LDS alone, since every item's start waits for it.
 constexpr int kMxMaxGroups = 513;  // E_local <= 512 and a shared group: checked by the C entry
 struct MxTiles {
     int tile_start[kMxMaxGroups + 1];
     int row0[kMxMaxGroups + 1];
+    int sums[3];
 };
 
-// all threads call (it holds barriers); returns the number of tiles
+// All threads call (it holds barriers); returns the number of tiles. The height
+// is 256 rows, or 128 or 64 where all items then still run at once: a call so
+// small takes as long as its tallest tile (nine groups of 17 rows and one of 203
+// at H = 1280, I = 384: gate/up 14.2 us with one tile of 203 rows, 10.0 with four).
 __device__ __forceinline__ int mx_build_tiles(MxTiles& tm, const int32_t* __restrict__ offsets, int n_groups,
-                                              int max_rows) {
+                                              int max_rows, int NB) {
     for (int g = threadIdx.x; g <= n_groups; g += kMxThreads) tm.row0[g] = clamp_row(offsets[g], max_rows);
     __syncthreads();
-    if (threadIdx.x < 64) {  // one wave: 64 groups at a time
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int height = kMxTM >> wave;  // waves 0 to 2 count tiles of 256, 128 and 64 rows
+    auto tiles_of = [&](int g, int h) {
+        return g < n_groups ? max(0, tm.row0[g + 1] - tm.row0[g] + h - 1) / h : 0;
+    };
+    if (wave < 3) {
+        int sum = 0;
+        for (int g = lane; g < n_groups; g += 64) sum += tiles_of(g, height);
+#pragma unroll
+        for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s);
+        if (lane == 0) tm.sums[wave] = sum;
+    }
+    __syncthreads();
+    const int h = tm.sums[2] <= (int)gridDim.x / NB ? 64 : tm.sums[1] <= (int)gridDim.x / NB ? 128 : kMxTM;
+    if (wave == 0) {  // 64 groups at a time
         int run = 0;
         for (int g0 = 0; g0 < n_groups; g0 += 64) {
-            const int g = g0 + (int)threadIdx.x;
-            const int nt = g < n_groups ? max(0, tm.row0[g + 1] - tm.row0[g] + kMxTM - 1) / kMxTM : 0;
+            const int g = g0 + lane, nt = tiles_of(g, h);
             int sum = nt;
 #pragma unroll
             for (int s = 1; s < 64; s <<= 1) {
                 const int o = __shfl_up(sum, s);
-                if ((int)threadIdx.x >= s) sum += o;
+                if (lane >= s) sum += o;
             }
             if (g < n_groups) tm.tile_start[g] = run + sum - nt;
             run += __shfl(sum, 63);
         }
-        if (threadIdx.x == 0) tm.tile_start[n_groups] = run;
+        if (lane == 0) tm.tile_start[n_groups] = run;
     }
     __syncthreads();
     return tm.tile_start[n_groups];
@@ -172,8 +189,8 @@ __device__ __forceinline__ MTile mx_item_at(const MxTiles& tm, int n_groups, int
     const int idx = local - pi * kMxPanel * NB;
     nb = idx / ph;
     const int i = pi * kMxPanel + idx - nb * ph;
-    const int a = (int)((long)i * m / nt), b = (int)((long)(i + 1) * m / nt);
-    return MTile{__builtin_amdgcn_readfirstlane(lo), r0 + a, b - a};
+    const int each = m / nt, more = m - each * nt;  // the first `more` tiles hold one row more
+    return MTile{__builtin_amdgcn_readfirstlane(lo), r0 + i * each + min(i, more), each + (i < more ? 1 : 0)};
 }
 
 // weight row (within the wave's 32) that MFMA row rho reads: lane (l31, hi)
@@ -218,7 +235,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     const int I = p.Nw / 2;  // SwiGLU: intermediate size
     // uniform, so that the item loop and the descriptors it carries stay scalar
     const int n_items =
-        __builtin_amdgcn_readfirstlane(mx_build_tiles(tm, p.offsets, p.n_groups, p.max_rows)) * p.NB;
+        __builtin_amdgcn_readfirstlane(mx_build_tiles(tm, p.offsets, p.n_groups, p.max_rows, p.NB)) * p.NB;
     const int xcd = blockIdx.x & 7;
     const int per_xcd = gridDim.x >> 3;
     const int i_lo = (int)((long)n_items * xcd / 8);
@@ -267,24 +284,34 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                           : buffer_rsrc(p.xs + (size_t)row0 * kb, clamp_bytes((size_t)rows * kb));
         return d;
     };
-    auto item_of = [&](int item) MX_INLINE {
+    // An item in two parts: find() looks up its tile and asks for its rows' slots, place() makes the offsets from
+    // them. The next item's find() stands ahead of the current one's steps, its place() behind them, so the slots
+    // arrive under the products.
+    const int w4 = wave & 3;
+    auto find = [&](int item) MX_INLINE {
         Item c;
         c.tile = mx_item_at(tm, p.n_groups, item, p.NB, c.nb);
-        auto src_row = [&](int r) MX_INLINE -> uint32_t {  // the tile's row r, clamped to it
+        auto slot = [&](int r) MX_INLINE -> uint32_t {  // of the tile's row r, clamped to it
             r = min(r, c.tile.rows - 1);
-            if (!kGather) return (uint32_t)r;
-            const int slot = p.src.row_slot[c.tile.row0 + r];
-            const int tk = slot < p.src.S ? slot / p.src.k : slot - p.src.S;
+            return kGather ? (uint32_t)p.src.row_slot[c.tile.row0 + r] : (uint32_t)r;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c.xoff[i] = slot(64 * i + pr);
+        c.soff = slot(64 * w4 + lane);
+        return c;
+    };
+    auto place = [&](Item& c) MX_INLINE {
+        auto src_row = [&](uint32_t v) MX_INLINE -> uint32_t {
+            if (!kGather) return v;
+            const int s = (int)v, tk = s < p.src.S ? s / p.src.k : s - p.src.S;
             return (uint32_t)max(0, min(tk, p.src.rows - 1));
         };
         c.woff = (uint32_t)((kSwiGLU ? c.nb * 128 : c.nb * 256) + pr) * rowb + ((lane & 7) ^ mx_swz_w(pr)) * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c.xoff[i] = src_row(64 * i + pr) * rowb + ((lane & 7) ^ mx_swz_x(pr)) * 16;
-        const int w4 = wave & 3;
+        for (int i = 0; i < 4; ++i) c.xoff[i] = src_row(c.xoff[i]) * rowb + ((lane & 7) ^ mx_swz_x(pr)) * 16;
         c.soff = wave < 4
                      ? (uint32_t)((kSwiGLU ? (w4 >> 1) * I + c.nb * 128 + 64 * (w4 & 1) : c.nb * 256 + 64 * w4) + lane) * kb
-                     : src_row(64 * w4 + lane) * kb;
-        return c;
+                     : src_row(c.soff) * kb;
     };
     auto issue = [&](const Item& c, const Desc& d, auto nx_c, int kc, uint8_t* W, uint8_t* X01, uint8_t* X23) MX_INLINE {
         constexpr int NX = decltype(nx_c)::value;
@@ -322,11 +349,12 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
 
     int item = i_lo + (int)(blockIdx.x >> 3);
     if (item >= i_hi) return;
-    Item cur = item_of(item);
+    Item cur = find(item);
+    place(cur);
     first_loads(cur);
     for (;;) {
         const bool more = item + per_xcd < i_hi;
-        const Item next = more ? item_of(item + per_xcd) : cur;
+        Item next = more ? find(item + per_xcd) : cur;
         const MTile tile{__builtin_amdgcn_readfirstlane(cur.tile.group), __builtin_amdgcn_readfirstlane(cur.tile.row0),
                          __builtin_amdgcn_readfirstlane(cur.tile.rows)};
         const int nb = __builtin_amdgcn_readfirstlane(cur.nb);
@@ -437,6 +465,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
             wait_vmcnt<0>();
             mx_barrier();  // no stage is read any more
             if (more) {
+                place(next);
                 first_loads(next);
             }
 

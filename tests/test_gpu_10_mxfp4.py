@@ -368,3 +368,19 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for w, s in zip(want, state):
         assert torch.equal(s[4].view(torch.int16), w.view(torch.int16))
+
+
+@pytest.mark.parametrize("rows", [[203, 17, 17, 0, 40], [256, 1, 129], [700, 64, 65, 500], [2000]])
+def test_rows_do_not_depend_on_the_tiles(rows):
+    """A row's bits are the same whatever the other groups are, and so whatever height its tile gets."""
+    H, I = 512, 384
+    ex = Experts(H, I, len(rows), False, 19)
+    offsets = [0] + np.cumsum(rows).tolist()
+    R = offsets[-1]
+    x, xs, xv = quantized((R, H), 1.0, 28)
+    y = run_ffn(x, xs, ex, offsets, R)
+    for e in range(len(rows)):
+        a, b = offsets[e], offsets[e + 1]
+        for n in {1, 60, rows[e] // 2, rows[e]} & set(range(1, rows[e] + 1)):
+            alone = run_ffn(x[a:a + n].contiguous(), xs[a:a + n].contiguous(), ex, [0] * (e + 1) + [n] * (len(rows) - e), n)
+            assert torch.equal(alone.view(torch.int16), y[a:a + n].view(torch.int16)), (e, n)
