@@ -51,23 +51,33 @@ struct FewArgs {
     float* topk_w;             // [T][k]
     int T, k, E, scoring, renorm, H, I, base, E_local, has_shared;
     const uint8_t *w13, *w13s, *w2, *w2s, *ws13, *ws13s, *ws2, *ws2s;
+    struct FewGroups* groups;  // the map, from the gate/up kernel to the down kernel
     float* a;                  // [T*k + T][I] fp32 intermediate, row = slot (T*k + t: shared)
     uint16_t* out;             // [T][H] bf16
     int cols;                  // output columns per workgroup of the down kernel
 };
 
 // The groups: the shared expert (if any), then the distinct local experts among
-// the picks, ascending.
+// the picks, ascending. The gate/up kernel's workgroups build it; the first one
+// leaves it in memory for the down kernel, which so knows its experts one load
+// after its start.
+struct FewGroups {
+    int n;
+    int expert[kFewGroups];              // -1: the shared one
+    uint32_t mask[kFewGroups];           // the tokens that picked it
+    short slot[kFewGroups * kFewT + 2];  // the first slot of a token that did, -1: none
+};
+static_assert(sizeof(FewGroups) % 4 == 0, "copied by dwords");
 struct FewMap {
     __attribute__((aligned(16))) uint32_t hit[kFewMaxE / 32];  // the local experts among the picks
     int id[kFewSlots + kFewK];           // local expert of a slot, -1: none
     float w[kFewSlots + kFewK];
-    int expert[kFewGroups];              // -1: the shared one
-    uint32_t mask[kFewGroups];           // the tokens that picked it
-    short slot[kFewGroups * kFewT];      // the first slot of a token that did, -1: none
+    FewGroups g;
 };
-// ... and what the down kernel needs besides
+// ... and what the down kernel makes of it
 struct FewSum {
+    int id[kFewSlots + kFewK];
+    float w[kFewSlots + kFewK];
     float weight[kFewGroups * kFewT];    // the sum of a token's weights (an id may stand twice in a row)
     int pre[kFewGroups + 1];             // picked (group, token) pairs before each group
     short pair_slot[kFewSlots + kFewT];  // the pairs in order: slot and group
@@ -78,22 +88,18 @@ __device__ __forceinline__ int few_local(const FewArgs& p, int id) {  // any val
     return id >= p.base && id - p.base < p.E_local ? id - p.base : -1;
 }
 
-// Before the barrier behind which m.id (-1 behind the T k slots) and m.w are seen
-template <bool kSum>
-__device__ __forceinline__ void init_few_map(FewMap& m, FewSum* s, const FewArgs& p) {
+// Before the barrier behind which m.id (-1 behind the T k slots) is seen
+__device__ __forceinline__ void init_few_map(FewMap& m, const FewArgs& p) {
     const int tid = threadIdx.x, S = p.T * p.k;
     if (tid < kFewMaxE / 32) m.hit[tid] = 0;
-    for (int i = tid; i < kFewGroups * kFewT; i += kFewThreads) {
-        m.slot[i] = (short)(p.has_shared && i < p.T ? S + i : -1);
-        if (kSum) s->weight[i] = p.has_shared && i < p.T ? 1.0f : 0.0f;
-    }
-    for (int i = tid; i < kFewGroups; i += kFewThreads) m.mask[i] = p.has_shared && i == 0 ? (1u << p.T) - 1 : 0;
+    for (int i = tid; i < kFewGroups * kFewT; i += kFewThreads)
+        m.g.slot[i] = (short)(p.has_shared && i < p.T ? S + i : -1);
+    for (int i = tid; i < kFewGroups; i += kFewThreads) m.g.mask[i] = p.has_shared && i == 0 ? (1u << p.T) - 1 : 0;
 }
 
 // Builds the map behind that barrier and returns the number of groups. All
 // threads call; ends with a barrier.
-template <bool kSum>
-__device__ __forceinline__ int build_few_map(FewMap& m, FewSum* s, const FewArgs& p) {
+__device__ __forceinline__ int build_few_map(FewMap& m, const FewArgs& p) {
     const int tid = threadIdx.x, sh = p.has_shared ? 1 : 0;
     const int e = tid < kFewSlots ? m.id[tid] : -1;
     if (e >= 0) atomicOr(&m.hit[e >> 5], 1u << (e & 31));
@@ -106,56 +112,66 @@ __device__ __forceinline__ int build_few_map(FewMap& m, FewSum* s, const FewArgs
         rank += __popc(below < 32 ? hit & ((1u << below) - 1) : hit);
         n += __popc(hit);
     }
-    if (tid == 0 && sh) m.expert[0] = -1;
+    if (tid == 0) {
+        m.g.n = n;
+        if (sh) m.g.expert[0] = -1;
+    }
     if (e >= 0) {
         const int t = tid / p.k, j0 = tid - t * p.k;
         bool first = true;  // of its token's picks
-        float w = 0.f;
 #pragma unroll
-        for (int j = kFewK - 1; j >= 0; --j) {
-            const bool same = j < p.k && m.id[tid - j0 + j] == e;
-            if (same && j < j0) first = false;
-            if (kSum && same) w += m.w[tid - j0 + j];
-        }
-        m.expert[rank] = e;
+        for (int j = 0; j < kFewK; ++j)
+            if (j < j0 && m.id[tid - j0 + j] == e) first = false;
+        m.g.expert[rank] = e;
         if (first) {
-            m.slot[rank * kFewT + t] = (short)tid;
-            if (kSum) s->weight[rank * kFewT + t] = w;
-            atomicOr(&m.mask[rank], 1u << t);
+            m.g.slot[rank * kFewT + t] = (short)tid;
+            atomicOr(&m.g.mask[rank], 1u << t);
         }
     }
     mx_barrier();
-    n = __builtin_amdgcn_readfirstlane(n);
-    if (kSum) {
-        if (tid < 64) {
-            int run = 0;
-            for (int g0 = 0; g0 < n; g0 += 64) {
-                const int g = g0 + tid;
-                const int c = g < n ? __popc(m.mask[g]) : 0;
-                int sum = c;
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Behind a barrier that shows g, s.id and s.w; ends with one
+__device__ __forceinline__ void sum_few_map(const FewGroups& g, FewSum& s, int n, const FewArgs& p) {
+    const int tid = threadIdx.x, sh = p.has_shared ? 1 : 0;
+    if (tid < 64) {
+        int run = 0;
+        for (int g0 = 0; g0 < n; g0 += 64) {
+            const int c = g0 + tid < n ? __popc(g.mask[g0 + tid]) : 0;
+            int sum = c;
 #pragma unroll
-                for (int d = 1; d < 64; d <<= 1) {
-                    const int o = __shfl_up(sum, d);
-                    if (tid >= d) sum += o;
-                }
-                if (g < n) s->pre[g] = run + sum - c;
-                run += __shfl(sum, 63);
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(sum, d);
+                if (tid >= d) sum += o;
             }
-            if (tid == 0) s->pre[n] = run;
+            if (g0 + tid < n) s.pre[g0 + tid] = run + sum - c;
+            run += __shfl(sum, 63);
         }
-        mx_barrier();
-        for (int i = tid; i < n * kFewT; i += kFewThreads) {
-            const int g = i / kFewT, t = i % kFewT;
-            const uint32_t mask = m.mask[g];
-            if (mask >> t & 1) {
-                const int at = s->pre[g] + __popc(mask & ((1u << t) - 1));
-                s->pair_slot[at] = m.slot[i];
-                s->pair_group[at] = (short)g;
-            }
-        }
-        mx_barrier();
+        if (tid == 0) s.pre[n] = run;
     }
-    return n;
+    for (int i = tid; i < n * kFewT; i += kFewThreads) {
+        const int gr = i / kFewT, t = i % kFewT;
+        float w = gr < sh ? 1.0f : 0.f;
+        if (gr >= sh && g.mask[gr] >> t & 1) {
+            const int id = s.id[g.slot[i]];
+#pragma unroll
+            for (int j = kFewK - 1; j >= 0; --j)
+                if (j < p.k && s.id[t * p.k + j] == id) w += s.w[t * p.k + j];
+        }
+        s.weight[i] = w;
+    }
+    mx_barrier();
+    for (int i = tid; i < n * kFewT; i += kFewThreads) {
+        const int gr = i / kFewT, t = i % kFewT;
+        const uint32_t mask = g.mask[gr];
+        if (mask >> t & 1) {
+            const int at = s.pre[gr] + __popc(mask & ((1u << t) - 1));
+            s.pair_slot[at] = g.slot[i];
+            s.pair_group[at] = (short)gr;
+        }
+    }
+    mx_barrier();
 }
 
 __device__ __forceinline__ f32x4 mfma16_fp4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
@@ -202,7 +218,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
     auto issue = [&](int it, int n, uint8_t (&st)[kFewWaves][kGuStage]) MX_INLINE {
         const bool on = it < n * per;  // items past the end load nothing, but count
         const int g = on ? it / per : 0, i0 = on ? it % per * 8 : 0;
-        const int e = on && g >= sh ? __builtin_amdgcn_readfirstlane(m.expert[g]) : 0;
+        const int e = on && g >= sh ? __builtin_amdgcn_readfirstlane(m.g.expert[g]) : 0;
         const size_t rows = 2 * (size_t)p.I;
         const uint8_t* W = (g < sh ? p.ws13 : p.w13 + e * rows * rowb) + (size_t)i0 * rowb;
         const uint8_t* Ws = (g < sh ? p.ws13s : p.w13s + e * rows * kb) + (size_t)i0 * kb;
@@ -256,7 +272,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
             }
         }
     }
-    init_few_map<false>(m, nullptr, p);
+    init_few_map(m, p);
     if (!p.logits && threadIdx.x < kFewSlots)
         m.id[threadIdx.x] = threadIdx.x < S ? few_local(p, p.ids[threadIdx.x]) : -1;
     mx_barrier();
@@ -278,7 +294,10 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
         m.id[threadIdx.x] = threadIdx.x < S ? few_local(p, id) : -1;
     }
     mx_barrier();
-    const int n = build_few_map<false>(m, nullptr, p);
+    const int n = build_few_map(m, p);
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < (int)(sizeof(FewGroups) / 4); i += kFewThreads)
+            reinterpret_cast<uint32_t*>(p.groups)[i] = reinterpret_cast<const uint32_t*>(&m.g)[i];
     if (!early) issue(it, n, s0);
     wait_vmcnt<0>();  // said once here, or the compiler says it in the loop, before the first stage's reads
     issue(it + G, n, s1);
@@ -289,7 +308,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
     auto finish = [&](int par) MX_INLINE {
         const int i = threadIdx.x & 7, t = threadIdx.x >> 3;
         const int g = prev / per, i0 = prev % per * 8;
-        const int slot = threadIdx.x < 8 * kFewT && prev >= 0 ? m.slot[g * kFewT + t] : -1;
+        const int slot = threadIdx.x < 8 * kFewT && prev >= 0 ? m.g.slot[g * kFewT + t] : -1;
         if (slot >= 0) {
             float gs = 0.f, us = 0.f;
 #pragma unroll
@@ -353,7 +372,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     __shared__ __attribute__((aligned(1024))) uint8_t s1[kFewWaves][kDnUnit];
     __shared__ __attribute__((aligned(1024))) uint8_t s2[kFewWaves][kDnUnit];
     __shared__ __attribute__((aligned(16))) uint8_t act[kActRows * kActPitch];  // quantised rows of the intermediate
-    __shared__ FewMap m;
+    __shared__ FewGroups m;
     __shared__ FewSum fs;
     static_assert(sizeof(float) * kFewWaves * kDnCols * (kFewT + 1) <= sizeof(act), "the last sums reuse act");
     const int lane = threadIdx.x & 63;
@@ -363,13 +382,25 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     const int nseg = (p.I + kSegK - 1) / kSegK;
     const int h0 = blockIdx.x * p.cols, cols = min(p.cols, p.H - h0);
     const int S = p.T * p.k, sh = p.has_shared ? 1 : 0;
-    init_few_map<true>(m, &fs, p);
-    if (threadIdx.x < kFewSlots) {
-        m.id[threadIdx.x] = threadIdx.x < S ? few_local(p, p.ids[threadIdx.x]) : -1;
-        m.w[threadIdx.x] = threadIdx.x < S ? p.topk_w[threadIdx.x] : 0.f;
+    {
+        constexpr int kDwords = sizeof(FewGroups) / 4, kEach = (kDwords + kFewThreads - 1) / kFewThreads;
+        uint32_t t[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            t[i] = reinterpret_cast<const uint32_t*>(p.groups)[min((int)threadIdx.x + i * kFewThreads, kDwords - 1)];
+        const int s = min((int)threadIdx.x, S - 1);
+        const int id = p.ids[s];
+        const float w = p.topk_w[s];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (threadIdx.x + i * kFewThreads < kDwords) reinterpret_cast<uint32_t*>(&m)[threadIdx.x + i * kFewThreads] = t[i];
+        if (threadIdx.x < S) {
+            fs.id[threadIdx.x] = id;
+            fs.w[threadIdx.x] = w;
+        }
     }
     mx_barrier();
-    const int n = build_few_map<true>(m, &fs, p);
+    const int n = __builtin_amdgcn_readfirstlane(m.n);
     const int nsg = n * nseg;  // sub-groups: a segment of a group
     auto group_of = [&](int sg) MX_INLINE { return nseg == 1 ? sg : sg / nseg; };
 
@@ -455,10 +486,11 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         mx_barrier();
     };
 
-    begin(0);  // ahead of the weights, which would be waited for with it
     issue(0, s0);
     issue(1, s1);
     issue(2, s2);
+    sum_few_map(m, fs, n, p);
+    begin(0);
     quantise();
 
     const uint32_t srow = few_opaque(kDnCols * 128 + li * 8);
@@ -532,6 +564,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
 }
 
 struct FewWs {
+    FewGroups* groups;
     float* logits;
     float* a;
     size_t bytes;
@@ -545,6 +578,7 @@ FewWs carve_few(const moe_expert_weights* w, int T, int E, int k, void* base) {
         return base ? (void*)((uint8_t*)base + o) : nullptr;
     };
     FewWs r{};
+    r.groups = (FewGroups*)take(sizeof(FewGroups));
     r.logits = (float*)take((size_t)T * E * 4);
     r.a = (float*)take(((size_t)T * k + T) * w->I * 4);
     r.bytes = off;
@@ -588,6 +622,7 @@ moe_status launch_layer_few(const void* x, const void* w_router, const float* bi
     p.ws13s = (const uint8_t*)w->ws13_scale;
     p.ws2 = (const uint8_t*)w->ws2;
     p.ws2s = (const uint8_t*)w->ws2_scale;
+    p.groups = s.groups;
     p.a = s.a;
     p.out = (uint16_t*)out;
     const int cu = device_info().cu_count;
