@@ -26,9 +26,9 @@
 // two units' loads in flight while one is multiplied, so no wave waits for
 // another's data. Weights read straight into the MFMA's registers (16 rows of
 // 64 bytes per load, waited for before each product) reached 2.7 and 2.0 TB/s.
-// At H = 7168, I = 2048 one token's nine experts take 29 + 19 us behind 4.7 of
-// logits (140 and 70 MB; 6 TB/s between a head of 5 to 8 us and the end), eight
-// tokens' 58 take 150 to 166 + 87 to 95 us (5.4 TB/s in all).
+// At H = 7168, I = 2048 one token's nine experts take 29 + 17 us behind 4.7 of
+// logits (140 and 70 MB; 6 TB/s once the weights run, 2 to 5 us after the start),
+// eight tokens' 58 take 150 to 166 + 87 to 95 us (5.4 TB/s in all).
 #include "mx_dev.h"
 #include "route_dev.h"
 
