@@ -7,12 +7,12 @@
 //
 //   logits: one wave per (token, expert), the same bits as moe_route's.
 //   gate/up: every workgroup picks the experts from the logits itself (one wave
-//     per token), which costs less than a kernel of its own. An item is 8
+//     per token), which costs less than a kernel of its own. An item is 8 to 32
 //     intermediate columns of one expert (8 gate and 8 up rows, one MFMA
-//     operand); the 8 waves split K and add their partial sums through LDS.
-//     Items are I/8 per hit expert, so with one workgroup per CU the load is
-//     even for any number of experts. The quantised tokens stay in registers
-//     for the whole kernel. Items of the shared expert come first: the load of
+//     operand, to a wave); 8 to 2 waves split K, by its length, and add their
+//     partial sums through LDS. Items are I/8 to I/32 per hit expert, so with
+//     one workgroup per CU the load is even for any number of experts. The
+//     quantised tokens stay in registers for the whole kernel. Items of the shared expert come first: the load of
 //     the first one does not wait for the routing.
 //   down + combine: a workgroup owns up to 32 columns of the output for every
 //     hit expert; the waves split K and add each expert's product, times its
@@ -42,7 +42,7 @@ constexpr int kFewGroups = kFewSlots + 1;
 constexpr int kFewMaxE = 512;  // local experts: checked by the C entry
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / 64;
-constexpr int kFewPairs = 4;   // K steps of 256 per wave of the gate/up kernel: H <= 8192
+constexpr int kFewPairs = 4;   // K steps of 256 per wave of the gate/up kernel, at most: H <= 8192
 
 struct FewArgs {
     const uint16_t* x;         // [T][H] bf16
@@ -197,6 +197,8 @@ constexpr int kGuCodes = 16 * 128 * kFewPairs;  // a wave's share of one item
 constexpr int kGuStage = kGuCodes + 16 * 8 * kFewPairs;  // ... and its scales
 constexpr int kGuLoads = 2 * kFewPairs + 2;     // its loads: codes, and two for the scales
 
+// ks: waves that share an item's K, 2, 4 or 8
+template <int ks>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
     // a stage is an object of its own, so that reads of one do not wait for loads into the other
     __shared__ __attribute__((aligned(1024))) uint8_t s0[kFewWaves][kGuStage];
@@ -207,17 +209,20 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lk = lane >> 4;
     const int rowb = p.H / 2, kb = p.H / kMxBlock;
-    const int np = p.H / 256, p0 = wave * np / kFewWaves, cnt = (wave + 1) * np / kFewWaves - p0;
+    // the wave's slice of K and its 8 columns of the item
+    constexpr int width = 8 * kFewWaves / ks;
+    const int ksi = wave & (ks - 1), cg = wave / ks;
+    const int np = p.H / 256, p0 = ksi * np / ks, cnt = (ksi + 1) * np / ks - p0;
     const int S = p.T * p.k, sh = p.has_shared ? 1 : 0;
-    const int per = p.I / 8, G = gridDim.x;
+    const int per = p.I / width, G = gridDim.x;
 
     // a load: the 8 gate or the 8 up rows of an item for one K step
-    const uint32_t wv = (uint32_t)((lane >> 3) * rowb + p0 * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
+    const uint32_t wv = (uint32_t)((8 * cg + (lane >> 3)) * rowb + p0 * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
     const uint32_t up = (uint32_t)p.I * rowb;
-    const uint32_t sv = (uint32_t)((lane >> 3) * kb + p0 * 8 + (lane & 7) * 4), sup = (uint32_t)p.I * kb;
+    const uint32_t sv = (uint32_t)((8 * cg + (lane >> 3)) * kb + p0 * 8 + (lane & 7) * 4), sup = (uint32_t)p.I * kb;
     auto issue = [&](int it, int n, uint8_t (&st)[kFewWaves][kGuStage]) MX_INLINE {
         const bool on = it < n * per;  // items past the end load nothing, but count
-        const int g = on ? it / per : 0, i0 = on ? it % per * 8 : 0;
+        const int g = on ? it / per : 0, i0 = on ? it % per * width : 0;
         const int e = on && g >= sh ? __builtin_amdgcn_readfirstlane(m.g.expert[g]) : 0;
         const size_t rows = 2 * (size_t)p.I;
         const uint8_t* W = (g < sh ? p.ws13 : p.w13 + e * rows * rowb) + (size_t)i0 * rowb;
@@ -306,15 +311,15 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs p) {
     // the intermediate of the item before from the waves' partial sums
     int prev = -1;
     auto finish = [&](int par) MX_INLINE {
-        const int i = threadIdx.x & 7, t = threadIdx.x >> 3;
-        const int g = prev / per, i0 = prev % per * 8;
-        const int slot = threadIdx.x < 8 * kFewT && prev >= 0 ? m.g.slot[g * kFewT + t] : -1;
+        const int g = prev / per, i0 = prev % per * width;
+        const int i = threadIdx.x & (width - 1), t = threadIdx.x / width;
+        const int slot = t < kFewT && prev >= 0 ? m.g.slot[g * kFewT + t] : -1;
         if (slot >= 0) {
             float gs = 0.f, us = 0.f;
 #pragma unroll
-            for (int w = 0; w < kFewWaves; ++w) {
-                gs += red[par][w][t][i];
-                us += red[par][w][t][8 + i];
+            for (int w = 0; w < ks; ++w) {
+                gs += red[par][(i >> 3) * ks + w][t][i & 7];
+                us += red[par][(i >> 3) * ks + w][t][8 + (i & 7)];
             }
             p.a[(size_t)slot * p.I + i0 + i] = silu_mul(gs, us);
         }
@@ -364,14 +369,15 @@ constexpr int kDnCols = 32;                        // output columns of a workgr
 constexpr int kDnUnit = kDnCols * 128 + kDnCols * 8;  // 256 of K for each: codes, then scales
 constexpr int kDnLoads = kDnCols / 8 + 1;
 constexpr int kSegK = 256 * kFewWaves;             // a segment of K: one unit per wave
-constexpr int kActPitch = kSegK / 2 + kSegK / kMxBlock + 16;
-constexpr int kActRows = 38;                       // >= kFewT: a group fits
+constexpr int kActBytes = 41952;                   // 37 rows of a whole segment: a group (kFewT) fits
 
+// kWhole: rows of act hold whole segments (I >= 2048); otherwise rows as narrow as I, so that more of them fit
+template <bool kWhole>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     __shared__ __attribute__((aligned(1024))) uint8_t s0[kFewWaves][kDnUnit];
     __shared__ __attribute__((aligned(1024))) uint8_t s1[kFewWaves][kDnUnit];
     __shared__ __attribute__((aligned(1024))) uint8_t s2[kFewWaves][kDnUnit];
-    __shared__ __attribute__((aligned(16))) uint8_t act[kActRows * kActPitch];  // quantised rows of the intermediate
+    __shared__ __attribute__((aligned(16))) uint8_t act[kActBytes];  // quantised rows of the intermediate
     __shared__ FewGroups m;
     __shared__ FewSum fs;
     static_assert(sizeof(float) * kFewWaves * kDnCols * (kFewT + 1) <= sizeof(act), "the last sums reuse act");
@@ -379,7 +385,10 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lk = lane >> 4;
     const int rowb = p.I / 2, kb = p.I / kMxBlock, nk = p.I / 128, np = (nk + 1) / 2;
-    const int nseg = (p.I + kSegK - 1) / kSegK;
+    const int nseg = kWhole ? (p.I + kSegK - 1) / kSegK : 1;
+    // a row of act: a segment's codes, its scales, and a pad; reads of a half that is not there end in the slack
+    const int segk = kWhole ? kSegK : p.I, pitch = segk / 2 + ((segk / kMxBlock + 31) & ~15);
+    const int act_rows = (kActBytes - 128) / pitch, eights = segk / 8;
     const int h0 = blockIdx.x * p.cols, cols = min(p.cols, p.H - h0);
     const int S = p.T * p.k, sh = p.has_shared ? 1 : 0;
     {
@@ -407,11 +416,12 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     // rows past cols are past the descriptors' end and read zeros
     const uint32_t wv = (uint32_t)((lane >> 3) * rowb + wave * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
     const uint32_t sv = (uint32_t)((lane >> 1) * kb + wave * 8 + (lane & 1) * 4);
-    auto issue = [&](int sg, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
+    auto expert_of = [&](int sg) MX_INLINE { return m.expert[group_of(min(sg, max(nsg - 1, 0)))]; };
+    auto issue = [&](int sg, int expert, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
         const int g = group_of(sg), seg = sg - g * nseg;
         const bool on = sg < nsg && kFewWaves * seg + wave < np;
         const bool shared = g < sh;
-        const int e = shared || !on ? 0 : __builtin_amdgcn_readfirstlane(m.expert[g]);
+        const int e = shared || !on ? 0 : __builtin_amdgcn_readfirstlane(expert);
         const uint8_t* W = (shared ? p.ws2 : p.w2 + (size_t)e * p.H * rowb) + (size_t)h0 * rowb;
         const uint8_t* Ws = (shared ? p.ws2s : p.w2s + (size_t)e * p.H * kb) + (size_t)h0 * kb;
         const __amdgpu_buffer_rsrc_t wd = buffer_rsrc(W, on ? (uint32_t)cols * rowb : 0),
@@ -431,14 +441,14 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     // The rows from sub-group sg on, as many whole sub-groups as fit, eight values per thread at a time. begin() loads
     // the first ones.
     int rows = 0;
-    constexpr int kBatch = 4, kEights = kSegK / 8;
+    constexpr int kBatch = 4;
     f32x4 v[kBatch][2];
+    int to[kBatch], scale_to[kBatch];  // where they go, -1: nowhere
     const __amdgpu_buffer_rsrc_t ad = buffer_rsrc(p.a, (uint32_t)((S + p.T) * p.I * 4));
-    const int e8 = threadIdx.x % kEights;
-    auto load_rows = [&](int r0) MX_INLINE {  // zeros past the last row and past I
+    auto load_rows = [&](int i0) MX_INLINE {  // zeros past the last row and past I
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int r = r0 + q * (kFewThreads / kEights);
+            const int i = i0 + q * kFewThreads, r = i / eights, e8 = i - r * eights;
             int pair = c_row + min(r, max(rows - 1, 0)), seg = 0;
             if (nseg > 1) {
                 const int g = fs.pair_group[pair / nseg], rem = pair - nseg * fs.pre[g], c = max(__popc(m.mask[g]), 1);
@@ -449,46 +459,47 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
             const uint32_t off = r < rows && k0 < p.I ? (uint32_t)(fs.pair_slot[pair] * p.I + k0) * 4 : 0xffffff00u;
             v[q][0] = __builtin_bit_cast(f32x4, buffer_load16(ad, off, 0));
             v[q][1] = __builtin_bit_cast(f32x4, buffer_load16(ad, off, 16));
+            to[q] = r < rows ? r * pitch + e8 * 4 : -1;
+            scale_to[q] = r < rows && (e8 & 3) == 0 ? r * pitch + segk / 2 + (e8 >> 2) : -1;
         }
     };
     auto begin = [&](int sg) MX_INLINE {
         c_row = __builtin_amdgcn_readfirstlane(row_of(sg));
-        // a sub-group has at least one row, so at most kActRows < 64 of them fit
-        const int to = min(sg + 1 + lane, nsg);
-        const uint64_t fit = __ballot(sg + 1 + lane <= nsg && row_of(to) - c_row <= kActRows);
+        const int to_sg = min(sg + 1 + lane, nsg);  // at most 64 of them
+        const uint64_t fit = __ballot(sg + 1 + lane <= nsg && row_of(to_sg) - c_row <= act_rows);
         c_end = sg + __popcll(fit);
         rows = __builtin_amdgcn_readfirstlane(row_of(c_end)) - c_row;
-        load_rows(threadIdx.x / kEights);
+        load_rows(threadIdx.x);
     };
     auto quantise = [&]() MX_INLINE {
         mx_barrier();  // the rows before have been read
 #pragma unroll 1
-        for (int r0 = threadIdx.x / kEights; r0 < rows; r0 += kBatch * (kFewThreads / kEights)) {
+        for (int i0 = threadIdx.x; i0 < rows * eights; i0 += kBatch * kFewThreads) {
             uint32_t code[kBatch], byte[kBatch];
+            int at[kBatch], scale_at[kBatch];
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
                 float f[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = v[q][i >> 2][i & 3];
                 code[q] = mx_quantise8(f, byte[q]);
+                at[q] = to[q];
+                scale_at[q] = scale_to[q];
             }
-            load_rows(r0 + kBatch * (kFewThreads / kEights));
+            load_rows(i0 + kBatch * kFewThreads);
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-                const int r = r0 + q * (kFewThreads / kEights);
-                if (r < rows) {
-                    *reinterpret_cast<uint32_t*>(&act[r * kActPitch + e8 * 4]) = code[q];
-                    if ((e8 & 3) == 0) act[r * kActPitch + kSegK / 2 + (e8 >> 2)] = (uint8_t)byte[q];
-                }
+                if (at[q] >= 0) *reinterpret_cast<uint32_t*>(act + at[q]) = code[q];
+                if (scale_at[q] >= 0) act[scale_at[q]] = (uint8_t)byte[q];
             }
         }
         wait_vmcnt<0>();  // said once here, or the compiler says it in the loop, before its stages' reads
         mx_barrier();
     };
 
-    issue(0, s0);
-    issue(1, s1);
-    issue(2, s2);
+    issue(0, expert_of(0), s0);
+    issue(1, expert_of(1), s1);
+    issue(2, expert_of(2), s2);
     sum_few_map(m, fs, n, p);
     begin(0);
     quantise();
@@ -502,6 +513,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         }
         wait_vmcnt<2 * kDnLoads>();  // this unit has landed; the next two may fly
         const int g = group_of(sg), seg = sg - g * nseg;
+        const int expert = expert_of(sg + 3);
         const int left = nk - 2 * (kFewWaves * seg + wave);  // halves of this wave's unit that are there
         const uint32_t mask = m.mask[g];
         const bool on = left > 0 && mask >> li & 1;
@@ -509,8 +521,9 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         const float w = fs.weight[g * kFewT + li];
         // a column that nobody picked multiplies row 0's values and is dropped
         const int row = on ? sg_row + __popc(mask & ((1u << li) - 1)) : 0;
-        const uint8_t* ar = act + row * kActPitch;
-        const uint64_t as = *reinterpret_cast<const uint64_t*>(ar + kSegK / 2 + 8 * wave) >> (8 * lk);
+        const uint8_t* ar = act + row * pitch + (left > 0 ? wave * 128 : 0);
+        const uint64_t as =
+            *reinterpret_cast<const uint64_t*>(act + row * pitch + segk / 2 + (left > 0 ? wave * 8 : 0)) >> (8 * lk);
         f32x4 acc[2] = {};
         uint64_t ws[2];
 #pragma unroll
@@ -520,7 +533,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         for (int u = 0; u < 2; ++u) {
             // past the end of K: scales of 2^-127 on both sides, and the codes are numbers whatever they are
             const uint32_t own = u < left ? 0xffu : 0u;
-            const u32x4 b = *reinterpret_cast<const u32x4*>(ar + (8 * wave + 4 * u + lk) * 16);
+            const u32x4 b = *reinterpret_cast<const u32x4*>(ar + (4 * u + lk) * 16);
             const uint32_t sb = (uint32_t)(as >> (32 * u)) & own;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -536,7 +549,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         asm volatile("" ::: "memory");
         wait_lds();  // this stage has been read
         asm volatile("" ::: "memory");
-        issue(sg + 3, st);
+        issue(sg + 3, expert, st);
     };
     for (int sg = 0; sg < nsg;) {
         body(sg, s0);
@@ -628,11 +641,16 @@ moe_status launch_layer_few(const void* x, const void* w_router, const float* bi
     const int cu = device_info().cu_count;
     // 8 columns are one load: as many workgroups as the CUs, or 32 columns each
     p.cols = std::min(kDnCols, (int)align_up((size_t)(w->H + cu - 1) / cu, 8));
-    const long items = ((long)std::min(T * k, w->E_local) + p.has_shared) * (w->I / 8);
-    hipLaunchKernelGGL(few_gate_up_kernel, dim3((int)std::min<long>(cu, items)), dim3(kFewThreads), 0, st, p);
+    // As few waves to an item's K as their stages allow, and so as many columns (at most 32: a thread for each and each
+    // token): an item's sums and barrier cost 1.5 us whatever it loads. 50 experts at H = 512, I = 2048 take 78 us with
+    // 8 columns an item and 26 with 32, 38 experts at H = 1024 64 and 25.
+    const int ks = w->H <= 2 * 256 * kFewPairs ? 2 : w->H <= 4 * 256 * kFewPairs ? 4 : 8;
+    const long items = ((long)std::min(T * k, w->E_local) + p.has_shared) * (w->I / (8 * kFewWaves / ks));
+    auto gate_up = ks == 2 ? few_gate_up_kernel<2> : ks == 4 ? few_gate_up_kernel<4> : few_gate_up_kernel<8>;
+    hipLaunchKernelGGL(gate_up, dim3((int)std::min<long>(cu, items)), dim3(kFewThreads), 0, st, p);
     const moe_status r = check_launch("few_gate_up_kernel");
     if (r) return r;
-    hipLaunchKernelGGL(few_down_kernel, dim3((w->H + p.cols - 1) / p.cols), dim3(kFewThreads), 0, st, p);
+    hipLaunchKernelGGL(w->I >= kSegK ? few_down_kernel<true> : few_down_kernel<false>, dim3((w->H + p.cols - 1) / p.cols), dim3(kFewThreads), 0, st, p);
     return check_launch("few_down_kernel");
 }
 
