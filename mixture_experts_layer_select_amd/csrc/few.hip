@@ -12,11 +12,13 @@
 //     operand, to a wave); 8 to 2 waves split K, by its length, and add their
 //     partial sums through LDS. Items are I/8 to I/32 per hit expert, so with
 //     one workgroup per CU the load is even for any number of experts. The
-//     quantised tokens stay in registers for the whole kernel. Items of the shared expert come first: the load of
-//     the first one does not wait for the routing.
+//     quantised tokens stay in registers for the whole kernel. Items of the
+//     shared expert come first: the load of the first one does not wait for the
+//     routing.
 //   down + combine: a workgroup owns up to 32 columns of the output for every
-//     hit expert; the waves split K and add each expert's product, times its
-//     routing weight, in fp32 registers until the end. One rounding, no
+//     hit expert; the waves split K (and the experts, where K is short) and add
+//     each expert's product, times its routing weight, in fp32 registers until
+//     the end. One rounding, no
 //     atomics, and a token's sum depends neither on the schedule nor on the
 //     other tokens. The intermediate is quantised into LDS, as many
 //     (expert, token) rows at a time as fit.
@@ -402,7 +404,8 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         const float w = p.topk_w[s];
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            if (threadIdx.x + i * kFewThreads < kDwords) reinterpret_cast<uint32_t*>(&m)[threadIdx.x + i * kFewThreads] = t[i];
+            if (threadIdx.x + i * kFewThreads < kDwords)
+                reinterpret_cast<uint32_t*>(&m)[threadIdx.x + i * kFewThreads] = t[i];
         if (threadIdx.x < S) {
             fs.id[threadIdx.x] = id;
             fs.w[threadIdx.x] = w;
@@ -413,13 +416,38 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
     const int nsg = n * nseg;  // sub-groups: a segment of a group
     auto group_of = [&](int sg) MX_INLINE { return nseg == 1 ? sg : sg / nseg; };
 
+    // A wave takes the K step ksi of its groups. Where I has fewer than eight, the waves left over take other groups:
+    // by the expert's number, so that a token's sum does not depend on the other tokens' experts. (50 experts at H =
+    // 2048, I = 128: 31 us with one wave at work, 14 with eight.)
+    const int ks = kWhole || np > 4 ? 8 : np > 2 ? 4 : np, ksi = wave & (ks - 1), cls = wave / ks;
+    uint64_t mine[3] = {};
+    int counter = 0;
+    if (!kWhole && ks < 8) {
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+            const int g = 64 * b + lane, e = g < n ? m.expert[g] : -2;
+            mine[b] = __ballot(e != -2 && (e < 0 ? 0 : e & (kFewWaves / ks - 1)) == cls);
+        }
+    }
+    auto next_sg = [&]() MX_INLINE {  // ascending; nsg and more: none left
+        if (kWhole || ks == 8) return counter++;
+        const int b = mine[0] ? 0 : mine[1] ? 1 : 2;
+        const uint64_t set = mine[0] ? mine[0] : mine[1] ? mine[1] : mine[2];
+        const int sg = set ? 64 * b + (int)__builtin_ctzll(set) : nsg;
+        const uint64_t rest = set & (set - 1);
+        mine[2] = b == 2 ? rest : mine[2];
+        mine[1] = b == 1 ? rest : mine[1];
+        mine[0] = b == 0 ? rest : mine[0];
+        return __builtin_amdgcn_readfirstlane(sg);
+    };
+
     // rows past cols are past the descriptors' end and read zeros
-    const uint32_t wv = (uint32_t)((lane >> 3) * rowb + wave * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
-    const uint32_t sv = (uint32_t)((lane >> 1) * kb + wave * 8 + (lane & 1) * 4);
+    const uint32_t wv = (uint32_t)((lane >> 3) * rowb + ksi * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
+    const uint32_t sv = (uint32_t)((lane >> 1) * kb + ksi * 8 + (lane & 1) * 4);
     auto expert_of = [&](int sg) MX_INLINE { return m.expert[group_of(min(sg, max(nsg - 1, 0)))]; };
     auto issue = [&](int sg, int expert, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
         const int g = group_of(sg), seg = sg - g * nseg;
-        const bool on = sg < nsg && kFewWaves * seg + wave < np;
+        const bool on = sg < nsg && kFewWaves * seg + ksi < np;
         const bool shared = g < sh;
         const int e = shared || !on ? 0 : __builtin_amdgcn_readfirstlane(expert);
         const uint8_t* W = (shared ? p.ws2 : p.w2 + (size_t)e * p.H * rowb) + (size_t)h0 * rowb;
@@ -497,33 +525,34 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         mx_barrier();
     };
 
-    issue(0, expert_of(0), s0);
-    issue(1, expert_of(1), s1);
-    issue(2, expert_of(2), s2);
+    int sg0 = next_sg(), sg1 = next_sg(), sg2 = next_sg();  // what the stages hold
+    issue(sg0, expert_of(sg0), s0);
+    issue(sg1, expert_of(sg1), s1);
+    issue(sg2, expert_of(sg2), s2);
     sum_few_map(m, fs, n, p);
     begin(0);
     quantise();
 
     const uint32_t srow = few_opaque(kDnCols * 128 + li * 8);
     f32x4 total[2] = {};
-    auto body = [&](int sg, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
-        if (sg == c_end) {
-            begin(sg);
+    auto body = [&](int& sg, uint8_t (&st)[kFewWaves][kDnUnit]) MX_INLINE {
+        while (sg >= c_end) {
+            begin(c_end);
             quantise();
         }
         wait_vmcnt<2 * kDnLoads>();  // this unit has landed; the next two may fly
         const int g = group_of(sg), seg = sg - g * nseg;
-        const int expert = expert_of(sg + 3);
-        const int left = nk - 2 * (kFewWaves * seg + wave);  // halves of this wave's unit that are there
+        const int after = next_sg(), expert = expert_of(after);
+        const int left = nk - 2 * (kFewWaves * seg + ksi);  // halves of this wave's unit that are there
         const uint32_t mask = m.mask[g];
         const bool on = left > 0 && mask >> li & 1;
         const int sg_row = row_of(sg) - c_row;
         const float w = fs.weight[g * kFewT + li];
         // a column that nobody picked multiplies row 0's values and is dropped
         const int row = on ? sg_row + __popc(mask & ((1u << li) - 1)) : 0;
-        const uint8_t* ar = act + row * pitch + (left > 0 ? wave * 128 : 0);
+        const uint8_t* ar = act + row * pitch + (left > 0 ? ksi * 128 : 0);
         const uint64_t as =
-            *reinterpret_cast<const uint64_t*>(act + row * pitch + segk / 2 + (left > 0 ? wave * 8 : 0)) >> (8 * lk);
+            *reinterpret_cast<const uint64_t*>(act + row * pitch + segk / 2 + (left > 0 ? ksi * 8 : 0)) >> (8 * lk);
         f32x4 acc[2] = {};
         uint64_t ws[2];
 #pragma unroll
@@ -549,15 +578,20 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         asm volatile("" ::: "memory");
         wait_lds();  // this stage has been read
         asm volatile("" ::: "memory");
-        issue(sg + 3, expert, st);
+        issue(after, expert, st);
+        sg = after;
     };
-    for (int sg = 0; sg < nsg;) {
-        body(sg, s0);
-        if (++sg >= nsg) break;
-        body(sg, s1);
-        if (++sg >= nsg) break;
-        body(sg, s2);
-        ++sg;
+    for (;;) {
+        if (sg0 >= nsg) break;
+        body(sg0, s0);
+        if (sg1 >= nsg) break;
+        body(sg1, s1);
+        if (sg2 >= nsg) break;
+        body(sg2, s2);
+    }
+    while (c_end < nsg) {  // the other waves' rows: all of them meet at the barriers
+        begin(c_end);
+        quantise();
     }
     wait_vmcnt<0>();
     mx_barrier();  // act is free
@@ -650,7 +684,8 @@ moe_status launch_layer_few(const void* x, const void* w_router, const float* bi
     hipLaunchKernelGGL(gate_up, dim3((int)std::min<long>(cu, items)), dim3(kFewThreads), 0, st, p);
     const moe_status r = check_launch("few_gate_up_kernel");
     if (r) return r;
-    hipLaunchKernelGGL(w->I >= kSegK ? few_down_kernel<true> : few_down_kernel<false>, dim3((w->H + p.cols - 1) / p.cols), dim3(kFewThreads), 0, st, p);
+    auto down = w->I >= kSegK ? few_down_kernel<true> : few_down_kernel<false>;
+    hipLaunchKernelGGL(down, dim3((w->H + p.cols - 1) / p.cols), dim3(kFewThreads), 0, st, p);
     return check_launch("few_down_kernel");
 }
 
