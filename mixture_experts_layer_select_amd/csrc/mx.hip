@@ -518,7 +518,7 @@ size_t mx_scale_offset(const moe_expert_weights* w, int max_rows) {
 
 template <bool kSwiGLU, bool kGather>
 moe_status launch_gemm(const MxGemm& p, hipStream_t st) {
-    const long tiles = (long)(p.max_rows + kMxTM - 1) / kMxTM + std::min(p.n_groups, p.max_rows);
+    const long tiles = ((long)p.max_rows + 63) / 64 + std::min(p.n_groups, p.max_rows);  // of 64 rows, at most
     const int grid = (int)std::min((tiles * p.NB + 7) / 8 * 8, (long)device_info().cu_count / 8 * 8);
     hipLaunchKernelGGL((mx_gemm_kernel<kSwiGLU, kGather>), dim3(grid), dim3(kMxThreads), 0, st, p);
     return check_launch("mx_gemm_kernel");
