@@ -342,6 +342,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 issue(c, d, nx_c, 0, o0, o0 + 32 * kKB, o1);
             } else {
                 issue(c, d, nx_c, 0, o0, o0 + 32 * kKB, nullptr);
+                asm volatile("" ::: "memory");  // in this order: the waits count the loads
                 issue(c, d, nx_c, 1, o2, o1, nullptr);
             }
         });
@@ -450,6 +451,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                     wait_vmcnt<L>();
                     mx_barrier();
                     issue_scales(cur, d, j + 1);
+                    asm volatile("" ::: "memory");  // in this order: the waits count the loads
                     load(j + 2, next_s);
                     if (j < nk) work(j, C1{}, cur_s);
                 };
