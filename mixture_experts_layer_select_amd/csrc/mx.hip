@@ -478,9 +478,11 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 if constexpr (kSwiGLU) {
                     float v[16];
                     uint32_t mx = 0;
+                    // With the divide, as moe_layer_few has it: a reciprocal instruction gives 0 where exp(-g) is above
+                    // 2^126, and its last bit moved codes. 1 us of 158 at 128 decode tokens, 2 of 226 at 4096.
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        v[r] = mx_silu_mul(acc[0][j][r], acc[1][j][r]);
+                        v[r] = silu_mul(acc[0][j][r], acc[1][j][r]);
                         mx = max(mx, abs_bits(v[r]));
                     }
                     mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));

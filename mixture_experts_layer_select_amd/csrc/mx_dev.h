@@ -69,11 +69,6 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
-// silu(g) * u with the reciprocal instruction (1 ulp) in place of a divide
-__device__ __forceinline__ float mx_silu_mul(float g, float u) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
 // D += A B with both operands E2M1 (format 4): lane (l31, hi) holds row l31's
 // codes k = 32 hi + [0, 32) of A, and the same of B's column l31, each with
 // that block's scale byte; it receives D[8 (r / 4) + 4 hi + r % 4][l31].
