@@ -478,7 +478,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs p) {
         for (int q = 0; q < kBatch; ++q) {
             const int i = i0 + q * kFewThreads, r = i / eights, e8 = i - r * eights;
             int pair = c_row + min(r, max(rows - 1, 0)), seg = 0;
-            if (nseg > 1) {
+            if (nseg > 1 && rows > 0) {  // without rows (no local pick, no shared expert) there are no pairs to look up
                 const int g = fs.pair_group[pair / nseg], rem = pair - nseg * fs.pre[g], c = max(__popc(m.mask[g]), 1);
                 seg = rem / c;
                 pair = fs.pre[g] + rem - seg * c;
