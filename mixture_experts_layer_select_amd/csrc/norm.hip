@@ -14,6 +14,8 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxH = 16384;
+// rows of one launch, at most: a grid of 2^32 work items and more (2^26 rows of one wave) runs short without an error
+constexpr int kNormRows = 1 << 21;
 
 // sum over the workgroup, the same in every thread
 template <int kThreads>
@@ -69,10 +71,10 @@ __device__ __forceinline__ void put8(T* p, int h, int H, const float* v) {
 
 template <typename T, bool kVec, int kThreads, int kChunks>
 __global__ __launch_bounds__(kThreads) void pre_norm_kernel(const T* x, const T* __restrict__ delta, float scale,
-                                                            const float* __restrict__ gain, float eps, int H,
+                                                            const float* __restrict__ gain, float eps, int t0, int H,
                                                             T* h_out, T* n_out) {
     __shared__ float red[kThreads / 64];
-    const size_t row = (size_t)blockIdx.x * H;
+    const size_t row = (size_t)(t0 + (int)blockIdx.x) * H;
     float v[kChunks][8];
     float ss = 0.f;
 #pragma unroll
@@ -116,6 +118,7 @@ __global__ __launch_bounds__(kThreads) void pre_norm_kernel(const T* x, const T*
 }
 
 struct CombineNorm {
+    int t0;  // first token of the launch
     const void* y;
     const int32_t* slot_to_row;
     const float* topk_w;
@@ -134,7 +137,7 @@ struct CombineNorm {
 template <typename TY, typename TO, bool kVec, int kThreads, int kChunks>
 __global__ __launch_bounds__(kThreads) void combine_norm_kernel(CombineNorm p) {
     __shared__ float red[kThreads / 64];
-    const int t = blockIdx.x, H = p.H;
+    const int t = p.t0 + (int)blockIdx.x, H = p.H;
     const TY* y = (const TY*)p.y;
     float acc[kChunks][8] = {};
     auto add = [&](int row, float w) {
@@ -204,29 +207,35 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 template <typename T, bool kVec>
 void pre_norm_sized(const void* x, const void* delta, float scale, const float* gain, float eps, int T_, int H,
                     void* h_out, void* n_out, hipStream_t st) {
-    const dim3 grid(T_);
+    for (int t0 = 0; t0 < T_;) {
+        const dim3 grid(std::min(T_ - t0, kNormRows));
 #define PRE(THREADS, CHUNKS)                                                                                 \
     hipLaunchKernelGGL((pre_norm_kernel<T, kVec, THREADS, CHUNKS>), grid, dim3(THREADS), 0, st, (const T*)x, \
-                       (const T*)delta, scale, gain, eps, H, (T*)h_out, (T*)n_out)
-    if (H <= 512) PRE(64, 1);
-    else if (H <= 2048) PRE(256, 1);
-    else if (H <= 4096) PRE(512, 1);
-    else if (H <= 8192) PRE(512, 2);
-    else PRE(1024, 2);
+                       (const T*)delta, scale, gain, eps, t0, H, (T*)h_out, (T*)n_out)
+        if (H <= 512) PRE(64, 1);
+        else if (H <= 2048) PRE(256, 1);
+        else if (H <= 4096) PRE(512, 1);
+        else if (H <= 8192) PRE(512, 2);
+        else PRE(1024, 2);
 #undef PRE
+        t0 += (int)grid.x;
+    }
 }
 
 template <typename TY, typename TO, bool kVec>
-void combine_norm_sized(const CombineNorm& p, hipStream_t st) {
-    const dim3 grid(p.T);
+void combine_norm_sized(CombineNorm p, hipStream_t st) {
+    while (p.t0 < p.T) {
+        const dim3 grid(std::min(p.T - p.t0, kNormRows));
 #define POST(THREADS, CHUNKS) \
     hipLaunchKernelGGL((combine_norm_kernel<TY, TO, kVec, THREADS, CHUNKS>), grid, dim3(THREADS), 0, st, p)
-    if (p.H <= 512) POST(64, 1);
-    else if (p.H <= 2048) POST(256, 1);
-    else if (p.H <= 4096) POST(512, 1);
-    else if (p.H <= 8192) POST(1024, 1);
-    else POST(1024, 2);
+        if (p.H <= 512) POST(64, 1);
+        else if (p.H <= 2048) POST(256, 1);
+        else if (p.H <= 4096) POST(512, 1);
+        else if (p.H <= 8192) POST(1024, 1);
+        else POST(1024, 2);
 #undef POST
+        p.t0 += (int)grid.x;
+    }
 }
 
 template <typename TY, typename TO>
@@ -260,7 +269,7 @@ moe_status launch_combine_norm(const void* y_perm, moe_dtype y_dt, const int32_t
                                const float* topk_w, int T, int k, int H, const int32_t* offsets,
                                int shared_group, const float* gain, float eps, const void* gate, int gate_rows,
                                float alpha, const void* residual, void* out, moe_dtype out_dt, hipStream_t st) {
-    const CombineNorm p{y_perm, slot_to_row, topk_w, T, k, H, offsets, shared_group, gain, eps, gate, gate_rows,
+    const CombineNorm p{0, y_perm, slot_to_row, topk_w, T, k, H, offsets, shared_group, gain, eps, gate, gate_rows,
                         alpha, residual, out};
     if (y_dt == MOE_BF16 && out_dt == MOE_BF16) combine_norm_typed<uint16_t, uint16_t>(p, st);
     else if (y_dt == MOE_BF16) combine_norm_typed<uint16_t, float>(p, st);

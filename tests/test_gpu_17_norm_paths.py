@@ -1,0 +1,56 @@
+"""The norms where the launch shape or the addresses differ from test_gpu_11_norm's: more rows than one grid of
+work items holds, and rows at addresses that no vector access may take."""
+import pytest
+import torch
+
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+MANY = (1 << 26) + 5  # times 64 threads: more than 2^32 work items
+H = 8
+
+
+def _lib():
+    import mixture_experts_layer_select_amd as L
+    return L
+
+
+def bits(a):
+    return a.view(torch.int16)
+
+
+def test_pre_norm_of_more_rows_than_one_grid():
+    """The whole equals its two halves, each of which is one grid."""
+    L = _lib()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((MANY, H), generator=g, device=DEV, dtype=torch.bfloat16)
+    n, want = torch.zeros_like(x), torch.zeros_like(x)
+    L.moe_pre_norm(x, None, 0.0, None, 1e-6, L.BF16, MANY, H, None, n)
+    half = 1 << 25
+    for a, b in ((0, half), (half, MANY)):
+        L.moe_pre_norm(x[a:b], None, 0.0, None, 1e-6, L.BF16, b - a, H, None, want[a:b])
+    assert bool((want[-1] != 0).all()) and torch.equal(bits(n), bits(want))
+
+
+def test_combine_norm_of_more_tokens_than_one_grid():
+    """One pick a token and a shared row, a gate and a residual for each; the halves take their part of every input."""
+    L = _lib()
+    g = torch.Generator(device=DEV).manual_seed(2)
+    draw = lambda: torch.randn((MANY, H), generator=g, device=DEV, dtype=torch.bfloat16)
+    y, res = torch.cat([draw(), draw()]), draw()
+    gate = res.flip(0).contiguous()
+    rows = torch.arange(MANY - 1, -1, -1, dtype=torch.int32, device=DEV)
+    w = torch.rand((MANY, 1), generator=g, device=DEV)
+    gain = torch.rand(H, generator=g, device=DEV) + 0.5
+
+    def call(a, b, out):
+        off = torch.tensor([0, MANY + a, 2 * MANY], dtype=torch.int32, device=DEV)  # the shared rows of tokens a on
+        L.moe_combine_norm(y, L.BF16, rows[a:b], w[a:b], b - a, 1, H, off, 1, gain, 1e-6, gate[a:b], b - a, 0.5,
+                           res[a:b], out[a:b], L.BF16)
+    out, want = torch.zeros_like(res), torch.zeros_like(res)
+    call(0, MANY, out)
+    half = 1 << 25
+    call(0, half, want)
+    call(half, MANY, want)
+    assert bool((want[-1] != 0).any()) and torch.equal(bits(out), bits(want))
