@@ -69,8 +69,10 @@ __device__ __forceinline__ void put8(T* p, int h, int H, const float* v) {
     }
 }
 
+// h_out may be x or delta: neither they nor the outputs are __restrict__. A thread has loaded all its columns of a row
+// before it stores the first.
 template <typename T, bool kVec, int kThreads, int kChunks>
-__global__ __launch_bounds__(kThreads) void pre_norm_kernel(const T* x, const T* __restrict__ delta, float scale,
+__global__ __launch_bounds__(kThreads) void pre_norm_kernel(const T* x, const T* delta, float scale,
                                                             const float* __restrict__ gain, float eps, int t0, int H,
                                                             T* h_out, T* n_out) {
     __shared__ float red[kThreads / 64];

@@ -54,3 +54,20 @@ def test_combine_norm_of_more_tokens_than_one_grid():
     call(0, half, want)
     call(half, MANY, want)
     assert bool((want[-1] != 0).any()) and torch.equal(bits(out), bits(want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,width", [(5, 64), (3, 7168), (2, 8200), (4, 1001)])
+def test_pre_norm_in_place_of_either_input(T, width, dtype):
+    """h_out over x and over delta, at one and two chunks a thread, with and without vector accesses."""
+    L = _lib()
+    g = torch.Generator().manual_seed(T + width)
+    x, d = (torch.randn((T, width), generator=g).to(dtype).to(DEV) for _ in range(2))
+    gain = (torch.rand(width, generator=g) + 0.5).to(DEV)
+    dt = L.BF16 if dtype == torch.bfloat16 else L.F32
+    h, n = torch.empty_like(x), torch.empty_like(x)
+    L.moe_pre_norm(x, d, 0.75, gain, 1e-6, dt, T, width, h, n)
+    for which in (0, 1):
+        pair, n2 = (x.clone(), d.clone()), torch.empty_like(x)
+        L.moe_pre_norm(*pair, 0.75, gain, 1e-6, dt, T, width, pair[which], n2)
+        assert torch.equal(pair[which], h) and torch.equal(n2, n) and torch.equal(pair[1 - which], (x, d)[1 - which])
