@@ -289,8 +289,17 @@ class MoELayer:
         h + alpha * gate * norm(combine) (moe_combine_norm; no post norm when
         post_gain is None). gain, post_gain [H] fp32; gate [1, H] or [T, H] in
         the layer's activation dtype. b.h holds h, b.n the normed rows, b.out
-        the block's output."""
+        the block's output.
+
+        Where this GPU holds a part of the router's experts, the combine is this
+        part's sum: b.out is then h + alpha * gate * that sum, and h (and the
+        shared expert, if the layer has it) is in every GPU's output. The norm
+        of the whole sum cannot be had from norms of its parts, so post_gain is
+        refused there."""
         self.check_inputs(x)
+        if post_gain is not None and self.router["w"].shape[0] != self.E_local:
+            raise ValueError(f"post_gain: the layer holds {self.E_local} of {self.router['w'].shape[0]} experts, and "
+                             "the norm of a partial sum is not a part of the sum's norm")
         act, dev = x.dtype, self.w13.device
         for t, name, dt in ((delta, "delta", act), (gain, "gain", torch.float32),
                             (post_gain, "post_gain", torch.float32), (gate, "gate", act)):

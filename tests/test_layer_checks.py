@@ -1,0 +1,32 @@
+"""MoELayer's own checks of arguments, without a GPU: each refuses before anything is enqueued."""
+import pytest
+import torch
+
+H, I, E, K = 256, 128, 4, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+
+    import mixture_experts_layer_select_amd as pkg
+    if not os.path.exists(pkg._lib.LIB_PATH):
+        pkg.build()
+    return pkg
+
+
+def layer(L, E_local=E, n_router=E, base=0, k=K):
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    router = None
+    if n_router:
+        router = dict(w=torch.zeros((n_router, H), dtype=torch.bfloat16), bias=None, scoring=L.SIGMOID)
+    return L.MoELayer("mxfp4", H, I, k, u8(E_local, 2 * I, H // 2), u8(E_local, H, I // 2),
+                      u8(E_local, 2 * I, H // 32), u8(E_local, H, I // 32), router=router, expert_base=base)
+
+
+@pytest.mark.parametrize("base", [0, 4])
+def test_post_norm_of_an_expert_share_is_refused(L, base):
+    """A share's combine is a partial sum: its norm is no part of the block's."""
+    x = torch.zeros((3, H), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="post_gain: the layer holds 4 of 8 experts"):
+        layer(L, n_router=8, base=base).forward_block(x, post_gain=torch.ones(H))
