@@ -53,6 +53,10 @@ class MoELayer:
     quantize_mxfp4 makes them).
     router: dict(w=[E, H], bias=[E] or None, scoring, renormalize) or None
     when the routing is handed in (expert-parallel share).
+
+    Calls for the same number of tokens share their buffers and workspaces, the
+    outputs among them: calls of one layer must not overlap on two streams, and
+    a result is read or copied before the next call.
     """
 
     def __init__(self, fmt: str, H: int, I: int, k: int, w13, w2, w13_scale=None, w2_scale=None,
@@ -236,14 +240,16 @@ class MoELayer:
                           ws.numel(), stream)
         return b
 
-    # batches of mxfp4 experts up to this size go through moe_layer_few
+    # forward_few takes batches of mxfp4 experts up to this size; forward and
+    # forward_block run the separate steps at every size
     FEW_MAX_T = 16
 
-    def uses_few(self, T: int) -> bool:
-        """Whether forward_few takes T tokens (moe_layer_few's limits)."""
-        E = self.E_local if self.router is None else self.router["w"].shape[0]
-        return (self.fmt == "mxfp4" and T <= self.FEW_MAX_T and self.k <= 8 and self.H <= 8192
-                and (self.router is None or E <= 256))
+    def uses_few(self, T: int, routed: bool = False) -> bool:
+        """Whether forward_few takes T tokens (moe_layer_few's limits), routed
+        by this layer or, with routed=True, by the caller."""
+        return (self.fmt == "mxfp4" and T <= self.FEW_MAX_T and self.k <= 8 and self.E_local <= 512
+                and self.H % 256 == 0 and self.H <= 8192 and self.I % 128 == 0 and self.I <= 16384
+                and (routed or (self.router is not None and self.router["w"].shape[0] <= 256)))
 
     def few_workspace(self, T: int) -> torch.Tensor:
         """forward_few's workspace for T tokens."""
@@ -259,7 +265,9 @@ class MoELayer:
     def forward_few(self, x: torch.Tensor, topk_ids=None, topk_w=None, stream=None) -> LayerBuffers:
         """The layer for at most 16 tokens with mxfp4 experts (moe_layer_few):
         forward's ids and weights, and its output without the expert outputs'
-        rounding to bf16."""
+        rounding to bf16. The fp32 sums are taken in another order, so an
+        element of the intermediate that lies next to a rounding threshold may
+        get the neighbouring 4-bit code or block scale."""
         self.check_inputs(x, topk_ids, topk_w)
         T = x.shape[0]
         b = self.buffers(T, x.device)

@@ -30,3 +30,19 @@ def test_post_norm_of_an_expert_share_is_refused(L, base):
     x = torch.zeros((3, H), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="post_gain: the layer holds 4 of 8 experts"):
         layer(L, n_router=8, base=base).forward_block(x, post_gain=torch.ones(H))
+
+
+def test_uses_few_holds_the_limits_of_the_call(L):
+    """Each limit of moe_layer_few from both sides; the router's size counts only where the layer routes."""
+    assert all(layer(L).uses_few(T) for T in (0, 1, 16)) and not layer(L).uses_few(17)
+    assert layer(L, n_router=256).uses_few(1) and not layer(L, n_router=257).uses_few(1)
+    assert layer(L, n_router=257).uses_few(1, routed=True)
+    bare = layer(L, n_router=0)
+    assert bare.uses_few(16, routed=True) and not bare.uses_few(16)
+    assert layer(L, k=8, n_router=8).uses_few(1) and not layer(L, k=9, n_router=9).uses_few(1)
+    for key, good, bad in (("E_local", 512, 513), ("H", 8192, 8448), ("H", 512, 384), ("I", 16384, 16512), ("I", 384, 192)):
+        m = layer(L)
+        setattr(m, key, good)
+        assert m.uses_few(1, routed=True), (key, good)
+        setattr(m, key, bad)
+        assert not m.uses_few(1, routed=True), (key, bad)
