@@ -275,7 +275,8 @@ moe_status moe_layer_fused(const void* x, const void* w_router, const float* bia
  *   zeros has byte 127; one with a NaN or an infinity has byte 255 (NaN) and
  *   codes 0.
  * moe_dequantize_mxfp4: out [rows, cols] (MOE_BF16 or MOE_F32) = E2M1(code) *
- *   2^(byte - 127), exact in either type; NaN where the byte is 255.
+ *   2^(byte - 127), exact in either type up to its range (from byte 253 on the
+ *   largest codes are infinities); NaN where the byte is 255.
  * Limits: cols % 32 == 0; x and out 16-byte, codes 4-byte aligned. */
 moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_dt, int64_t rows, int cols, void* codes,
                               uint8_t* scales, void* stream);
@@ -288,8 +289,10 @@ moe_status moe_dequantize_mxfp4(const void* codes, const uint8_t* scales, int64_
  * hold one), and the routing-weighted sum. Each distinct expert's weights are
  * read once for all tokens. The intermediate A is quantised from fp32 as in
  * moe_expert_ffn; the weighted sum is taken in fp32 over unrounded expert outputs
- * and rounded once, so out differs from moe_expert_ffn + moe_combine by those
- * roundings to bf16.
+ * and rounded once. So out differs from moe_expert_ffn + moe_combine by those
+ * roundings to bf16 and by the order of the fp32 sums: an element of A next to a
+ * rounding threshold may get the neighbouring code, a block of A whose largest
+ * is next to a power of two the neighbouring scale.
  *   x [T,H] bf16, w_router [E,H] bf16 or NULL, bias [E] fp32 or NULL, w: dt =
  *   MOE_MXFP4; topk_ids [T,k] int32 and topk_w [T,k] fp32: written by the call, or
  *   read by it when w_router is NULL (E is then the number of experts that ids
