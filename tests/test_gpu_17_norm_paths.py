@@ -71,3 +71,34 @@ def test_pre_norm_in_place_of_either_input(T, width, dtype):
         pair, n2 = (x.clone(), d.clone()), torch.empty_like(x)
         L.moe_pre_norm(*pair, 0.75, gain, 1e-6, dt, T, width, pair[which], n2)
         assert torch.equal(pair[which], h) and torch.equal(n2, n) and torch.equal(pair[1 - which], (x, d)[1 - which])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,width,which", [(3, 512, "y"), (3, 512, "gain"), (4, 1024, "gate"), (2, 7168, "residual"),
+                                           (5, 2056, "out"), (2, 8200, "all"), (7, 64, "all")])
+def test_combine_norm_at_any_alignment(T, width, which, dtype):
+    """Each buffer, and all of them, one element past a vector boundary: the threads' columns and the order of every
+    sum stay what they are, so the bits are those of the aligned call."""
+    L = _lib()
+    k, dt = 3, L.BF16 if dtype == torch.bfloat16 else L.F32
+    g = torch.Generator().manual_seed(T + width)
+    draw = lambda *s, t=dtype: torch.randn(s, generator=g).to(t).to(DEV)
+
+    def odd(t, name):
+        if which not in (name, "all"):
+            return t
+        room = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)
+        room[1:1 + t.numel()] = t.flatten()
+        return room[1:1 + t.numel()].view(t.shape)
+    y, gate, res, gain = draw(T * k + T, width), draw(T, width), draw(T, width), draw(width, t=torch.float32)
+    rows = torch.randperm(T * k, generator=g).to(torch.int32)
+    rows[1] = -1
+    rows, w = rows.to(DEV), draw(T, k, t=torch.float32)
+    off = torch.tensor([0, T * k, T * k + T], dtype=torch.int32, device=DEV)
+
+    def call(y, gain, gate, res, out):
+        L.moe_combine_norm(y, dt, rows, w, T, k, width, off, 1, gain, 1e-6, gate, T, 0.5, res, out, dt)
+        return out
+    want = call(y, gain, gate, res, torch.zeros_like(res))
+    got = call(odd(y, "y"), odd(gain, "gain"), odd(gate, "gate"), odd(res, "residual"), odd(torch.zeros_like(res), "out"))
+    assert torch.equal(got, want) and bool((want != 0).any(1).all())
