@@ -138,6 +138,34 @@ def expect(t, name: str, dtypes, device=None):
         raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
+def _here(*tensors, host=False):
+    """Raw pointers, as _ptr gives them. The calls launch on the current
+    device: tensors of another one are refused, and those of the host unless
+    `host` (pinned memory is the caller's to know)."""
+    dev, out = None, []
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            at = t.get_device()
+            if at >= 0 or not host:
+                if dev is None:
+                    dev = torch.cuda.current_device()
+                if at != dev:
+                    raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+            out.append(t.data_ptr() if t.is_contiguous() else _ptr(t))
+        else:
+            out.append(t)
+    return out
+
+
+def _weights(w):
+    """The struct for a call on the current device: weights of another one are
+    refused (a struct that holds addresses only is the caller's to know)."""
+    at = getattr(w, "_device", -1)
+    if at >= 0 and at != torch.cuda.current_device():
+        raise ValueError(f"weights on cuda:{at}, the current device is cuda:{torch.cuda.current_device()}")
+    return C.byref(w)
+
+
 def _stream(stream=None):
     if stream is None:  # the handle itself: a Stream object made per call costs more than the launch it is for
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -195,6 +223,10 @@ def make_weights(dt, E_local, H, I, w13, w2, w13_scale=None, w2_scale=None, ws13
     # the struct holds raw device pointers: keep the tensors alive with it, or
     # their memory could be handed to other tensors while the struct is in use
     w._tensors = (w13, w2, w13_scale, w2_scale, ws13, ws2, ws13_scale, ws2_scale)
+    devices = {t.get_device() for t in w._tensors if isinstance(t, torch.Tensor)} - {-1}
+    if len(devices) > 1:
+        raise ValueError(f"weights and scales on several devices: {sorted(devices)}")
+    w._device = devices.pop() if devices else -1
     return w
 
 
@@ -204,16 +236,16 @@ def moe_expert_ffn_workspace_size(w: moe_expert_weights, max_rows: int) -> int:
 
 def moe_expert_ffn(w: moe_expert_weights, x_perm, x_perm_scale, expert_offsets, n_groups, max_rows,
                    y_perm, workspace, ws_bytes, stream=None):
-    _check("moe_expert_ffn", lib().moe_expert_ffn(
-        C.byref(w), _ptr(x_perm), _ptr(x_perm_scale), _ptr(expert_offsets), n_groups, max_rows,
-        _ptr(y_perm), _ptr(workspace), ws_bytes, _stream(stream)))
+    x, scale, offsets, y, ws = _here(x_perm, x_perm_scale, expert_offsets, y_perm, workspace, host=True)
+    _check("moe_expert_ffn", lib().moe_expert_ffn(_weights(w), x, scale, offsets, n_groups, max_rows, y, ws, ws_bytes,
+                                                  _stream(stream)))
 
 
 def moe_expert_ffn_gate_up(w: moe_expert_weights, x_perm, x_perm_scale, expert_offsets, n_groups,
                            max_rows, workspace, ws_bytes, stream=None):
-    _check("moe_expert_ffn_gate_up", lib().moe_expert_ffn_gate_up(
-        C.byref(w), _ptr(x_perm), _ptr(x_perm_scale), _ptr(expert_offsets), n_groups, max_rows,
-        _ptr(workspace), ws_bytes, _stream(stream)))
+    x, scale, offsets, ws = _here(x_perm, x_perm_scale, expert_offsets, workspace, host=True)
+    _check("moe_expert_ffn_gate_up", lib().moe_expert_ffn_gate_up(_weights(w), x, scale, offsets, n_groups, max_rows, ws,
+                                                                  ws_bytes, _stream(stream)))
 
 
 # size of the static device scratch behind moe_expert_ffn_noalloc
@@ -222,9 +254,9 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 
 def moe_expert_ffn_noalloc(w: moe_expert_weights, x_perm, x_perm_scale, expert_offsets, n_groups,
                            max_rows, y_perm, stream=None):
-    _check("moe_expert_ffn_noalloc", lib().moe_expert_ffn_noalloc(
-        C.byref(w), _ptr(x_perm), _ptr(x_perm_scale), _ptr(expert_offsets), n_groups, max_rows,
-        _ptr(y_perm), _stream(stream)))
+    x, scale, offsets, y = _here(x_perm, x_perm_scale, expert_offsets, y_perm, host=True)
+    _check("moe_expert_ffn_noalloc", lib().moe_expert_ffn_noalloc(_weights(w), x, scale, offsets, n_groups, max_rows, y,
+                                                                  _stream(stream)))
 
 
 def moe_quantize_tokens(x, x_dt, T, H, codes, scales, stream=None):
@@ -234,9 +266,9 @@ def moe_quantize_tokens(x, x_dt, T, H, codes, scales, stream=None):
 
 def moe_expert_ffn_gate_up_tokens(w: moe_expert_weights, x_tokens, x_tokens_scale, T, k, row_to_slot,
                                   expert_offsets, n_groups, max_rows, workspace, ws_bytes, stream=None):
+    x, scale, slots, offsets, ws = _here(x_tokens, x_tokens_scale, row_to_slot, expert_offsets, workspace, host=True)
     _check("moe_expert_ffn_gate_up_tokens", lib().moe_expert_ffn_gate_up_tokens(
-        C.byref(w), _ptr(x_tokens), _ptr(x_tokens_scale), T, k, _ptr(row_to_slot),
-        _ptr(expert_offsets), n_groups, max_rows, _ptr(workspace), ws_bytes, _stream(stream)))
+        _weights(w), x, scale, T, k, slots, offsets, n_groups, max_rows, ws, ws_bytes, _stream(stream)))
 
 
 def moe_layer_fused_workspace_size(w: moe_expert_weights, T, E, k) -> int:
@@ -252,9 +284,9 @@ def moe_layer_fused(x, w_router, bias, T, E, k, scoring, renormalize, w: moe_exp
 
 def moe_expert_ffn_down(w: moe_expert_weights, expert_offsets, n_groups, max_rows, y_perm, workspace,
                         ws_bytes, stream=None):
-    _check("moe_expert_ffn_down", lib().moe_expert_ffn_down(
-        C.byref(w), _ptr(expert_offsets), n_groups, max_rows, _ptr(y_perm), _ptr(workspace),
-        ws_bytes, _stream(stream)))
+    offsets, y, ws = _here(expert_offsets, y_perm, workspace, host=True)
+    _check("moe_expert_ffn_down", lib().moe_expert_ffn_down(_weights(w), offsets, n_groups, max_rows, y, ws, ws_bytes,
+                                                            _stream(stream)))
 
 
 def moe_combine(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, out, out_dt,
@@ -262,22 +294,6 @@ def moe_combine(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shar
     _check("moe_combine", lib().moe_combine(
         _ptr(y_perm), y_dt, _ptr(slot_to_row), _ptr(topk_w), T, k, H, _ptr(expert_offsets),
         shared_group, _ptr(out), out_dt, _stream(stream)))
-
-
-def _here(*tensors):
-    """Raw pointers, as _ptr gives them. The calls launch on the current
-    device: tensors of another one are refused."""
-    dev, out = None, []
-    for t in tensors:
-        if isinstance(t, torch.Tensor):
-            if dev is None:
-                dev = torch.cuda.current_device()
-            if t.get_device() != dev:
-                raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
-            out.append(t.data_ptr() if t.is_contiguous() else _ptr(t))
-        else:
-            out.append(t)
-    return out
 
 
 def moe_quantize_mxfp4(x, x_dt, rows, cols, codes, scales, stream=None):
@@ -298,7 +314,7 @@ def moe_layer_few(x, w_router, bias, T, E, k, scoring, renormalize, w: moe_exper
                   topk_w, out, workspace, ws_bytes, stream=None):
     x, w_router, bias, topk_ids, topk_w, out, workspace = _here(x, w_router, bias, topk_ids, topk_w, out, workspace)
     _check("moe_layer_few", lib().moe_layer_few(
-        x, w_router, bias, T, E, k, scoring, int(bool(renormalize)), C.byref(w), expert_base, topk_ids, topk_w, out,
+        x, w_router, bias, T, E, k, scoring, int(bool(renormalize)), _weights(w), expert_base, topk_ids, topk_w, out,
         workspace, ws_bytes, _stream(stream)))
 
 

@@ -1,0 +1,49 @@
+"""Calls that take MXFP4 weights launch on the current device and refuse tensors and weights of another one before
+anything is enqueued. The other device is played by the answer of torch.cuda.current_device(), so one GPU is enough."""
+import pytest
+import torch
+
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+H, I, E, T = 256, 128, 2, 3
+
+
+@pytest.fixture
+def calls():
+    import mixture_experts_layer_select_amd as L
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device=DEV)
+    shapes = ((E, 2 * I, H // 2), (E, H, I // 2), (E, 2 * I, H // 32), (E, H, I // 32))
+    w = L.make_weights(L.MXFP4, E, H, I, *[u8(*s) for s in shapes])
+    x, xs, off = u8(T, H // 2), u8(T, H // 32), torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    y, slots = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV), torch.zeros(T, dtype=torch.int32, device=DEV)
+    n = L.moe_expert_ffn_workspace_size(w, T)
+    ws = u8(n)
+    few = u8(L.moe_layer_few_workspace_size(w, T, E, 1))
+    ids, tw = torch.zeros((T, 1), dtype=torch.int32, device=DEV), torch.zeros((T, 1), device=DEV)
+    return dict(
+        ffn=lambda w=w, x=x: L.moe_expert_ffn(w, x, xs, off, E, T, y, ws, n),
+        gate_up=lambda w=w, x=x: L.moe_expert_ffn_gate_up(w, x, xs, off, E, T, ws, n),
+        tokens=lambda w=w, x=x: L.moe_expert_ffn_gate_up_tokens(w, x, xs, T, 1, slots, off, E, T, ws, n),
+        down=lambda w=w, x=y: L.moe_expert_ffn_down(w, off, E, T, x, ws, n),
+        noalloc=lambda w=w, x=x: L.moe_expert_ffn_noalloc(w, x, xs, off, E, T, y),
+        few=lambda w=w, x=y: L.moe_layer_few(x, None, None, T, E, 1, L.SIGMOID, True, w, 0, ids, tw, y, few, few.numel()))
+
+
+@pytest.mark.parametrize("name", ["ffn", "gate_up", "tokens", "down", "noalloc", "few"])
+def test_another_device_is_refused(calls, name, monkeypatch):
+    call = calls[name]
+    call()  # on its own device the same call goes through
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="tensor on cuda:0, the current device is cuda:1"):
+        call()
+
+
+def test_weights_of_another_device_are_refused(monkeypatch):
+    import mixture_experts_layer_select_amd as L
+    w = L.make_weights(L.MXFP4, 1, H, I, *[torch.zeros(1, 1, dtype=torch.uint8, device=DEV)] * 4)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="weights on cuda:0, the current device is cuda:1"):
+        L.moe_expert_ffn(w, None, None, None, 1, 0, None, None, 0, 0)

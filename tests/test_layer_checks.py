@@ -46,3 +46,20 @@ def test_uses_few_holds_the_limits_of_the_call(L):
         assert m.uses_few(1, routed=True), (key, good)
         setattr(m, key, bad)
         assert not m.uses_few(1, routed=True), (key, bad)
+
+
+class On(torch.Tensor):
+    """A host tensor that says it lies on GPU `at`."""
+
+    def get_device(self):
+        return self.at
+
+
+def test_weights_on_two_devices_are_refused(L):
+    def on(at):
+        t = torch.zeros(1, dtype=torch.uint8).as_subclass(On)
+        t.at = at
+        return t
+    with pytest.raises(ValueError, match=r"several devices: \[0, 1\]"):
+        L.make_weights(L.MXFP4, 1, H, I, on(0), on(0), on(0), on(1))
+    L.make_weights(L.MXFP4, 1, H, I, on(1), on(1), on(1), on(1))
