@@ -166,9 +166,16 @@ def _weights(w):
     return C.byref(w)
 
 
+# torch's handle of the current stream without a Stream object, which costs more per call than the launch it is for;
+# a torch that has no such function gives the handle through the object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    if stream is None:  # the handle itself: a Stream object made per call costs more than the launch it is for
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -47,3 +47,15 @@ def test_weights_of_another_device_are_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="weights on cuda:0, the current device is cuda:1"):
         L.moe_expert_ffn(w, None, None, None, 1, 0, None, None, 0, 0)
+
+
+def test_current_stream_by_either_way(monkeypatch):
+    """Calls without a stream go to torch's current one, with torch's raw handle and without it."""
+    from mixture_experts_layer_select_amd import _lib
+    side = torch.cuda.Stream()
+    for raw in (_lib._raw_stream, None):
+        monkeypatch.setattr(_lib, "_raw_stream", raw)
+        assert _lib._stream() == torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(side):
+            assert _lib._stream() == side.cuda_stream != torch.cuda.default_stream().cuda_stream
+        assert _lib._stream(side) == side.cuda_stream
