@@ -63,3 +63,9 @@ def test_weights_on_two_devices_are_refused(L):
     with pytest.raises(ValueError, match=r"several devices: \[0, 1\]"):
         L.make_weights(L.MXFP4, 1, H, I, on(0), on(0), on(0), on(1))
     L.make_weights(L.MXFP4, 1, H, I, on(1), on(1), on(1), on(1))
+
+
+@pytest.mark.parametrize("shape", [(), (4, 0), (0,), (4, 48), (31,)])
+def test_quantize_mxfp4_refuses_rows_that_are_no_blocks(L, shape):
+    with pytest.raises(ValueError, match="not a multiple of 32"):
+        L.quantize_mxfp4(torch.zeros(shape))
