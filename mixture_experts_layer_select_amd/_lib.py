@@ -179,6 +179,11 @@ def _stream(stream=None):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def stream_of(stream) -> torch.cuda.Stream:
+    """torch's object of a stream that a call was given (an object or a handle)."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+
+
 def dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return F32

@@ -9,6 +9,7 @@ arithmetic happens in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import Optional
 
@@ -332,12 +333,15 @@ class MoELayer:
 
 def quantize_mxfp4(x: torch.Tensor, stream=None):
     """(codes [..., K/2], scale bytes [..., K/32]) of a bf16 or fp32 tensor
-    [..., K] (moe_quantize_mxfp4), as MoELayer takes expert weights."""
+    [..., K] (moe_quantize_mxfp4), as MoELayer takes expert weights. With a
+    stream they are allocated on it, so that memory freed behind the call is
+    not handed to other streams' work while that stream may still use it."""
     L.expect(x, "x", (torch.float32, torch.bfloat16))
     K = x.shape[-1] if x.dim() else 0
     if K == 0 or K % 32:
         raise ValueError(f"x: last dimension of shape {tuple(x.shape)} is not a multiple of 32 (32 or more)")
-    codes = torch.empty(x.shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(x.shape[:-1] + (K // 32,), dtype=torch.uint8, device=x.device)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(L.stream_of(stream)):
+        codes = torch.empty(x.shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(x.shape[:-1] + (K // 32,), dtype=torch.uint8, device=x.device)
     L.moe_quantize_mxfp4(x, L.dtype_code(x), x.numel() // K, K, codes, scales, stream)
     return codes, scales

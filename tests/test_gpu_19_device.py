@@ -59,3 +59,23 @@ def test_current_stream_by_either_way(monkeypatch):
         with torch.cuda.stream(side):
             assert _lib._stream() == side.cuda_stream != torch.cuda.default_stream().cuda_stream
         assert _lib._stream(side) == side.cuda_stream
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_quantize_mxfp4_allocates_on_its_stream(handle):
+    """Freed codes go back to the stream that wrote them: the next tensor there takes their memory, one of the current
+    stream does not, so nothing is written over while the other stream works."""
+    import mixture_experts_layer_select_amd as L
+    side = torch.cuda.Stream()
+    x = torch.randn((4096, 16384), device=DEV)
+    torch.cuda.synchronize()
+    want = L.quantize_mxfp4(x)
+    codes, scales = L.quantize_mxfp4(x, side.cuda_stream if handle else side)
+    side.synchronize()
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
+    at, n = codes.data_ptr(), codes.numel()
+    del codes
+    here = torch.empty(n, dtype=torch.uint8, device=DEV)
+    with torch.cuda.stream(side):
+        there = torch.empty(n, dtype=torch.uint8, device=DEV)
+    assert here.data_ptr() != at and there.data_ptr() == at
