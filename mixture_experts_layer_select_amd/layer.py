@@ -72,11 +72,27 @@ class MoELayer:
         self.shared = shared
         self.router = router
         sh = shared or {}
+        if fmt == "mxfp4":
+            self._check_mxfp4(sh)
         self.weights = L.make_weights(self.dt, self.E_local, H, I, w13, w2, w13_scale, w2_scale,
                                       sh.get("w13"), sh.get("w2"), sh.get("w13_scale"),
                                       sh.get("w2_scale"))
         self.n_groups = self.E_local + (1 if shared is not None else 0)
         self._bufs = {}
+
+    def _check_mxfp4(self, sh: dict):
+        """Codes and scale bytes of the sizes that the kernels read; the
+        shared expert's with or without a leading dimension of 1."""
+        E, H, I = self.E_local, self.H, self.I
+        sizes = dict(w13=(2 * I, H // 2), w2=(H, I // 2), w13_scale=(2 * I, H // 32), w2_scale=(H, I // 32))
+        for name, size in sizes.items():
+            given = [(name, getattr(self, name), ((E, *size),))]
+            if self.shared is not None:
+                given.append((f"shared {name}", sh.get(name), (size, (1, *size))))
+            for label, t, shapes in given:
+                if t is None or t.element_size() != 1 or tuple(t.shape) not in shapes:
+                    have = "missing" if t is None else f"{t.dtype} of shape {tuple(t.shape)}"
+                    raise ValueError(f"{label}: {have}, expected bytes of shape {shapes[0]}")
 
     # fp8 layers with a shared expert quantise each token once and let gate/up
     # read its token's row (moe_quantize_tokens + moe_expert_ffn_gate_up_tokens)

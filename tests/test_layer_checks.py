@@ -69,3 +69,27 @@ def test_weights_on_two_devices_are_refused(L):
 def test_quantize_mxfp4_refuses_rows_that_are_no_blocks(L, shape):
     with pytest.raises(ValueError, match="not a multiple of 32"):
         L.quantize_mxfp4(torch.zeros(shape))
+
+
+def test_mxfp4_weights_of_other_sizes_are_refused(L):
+    """The kernels read what H and I say: a tensor that is smaller, wider or missing is refused when the layer is made."""
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    good = dict(w13=u8(E, 2 * I, H // 2), w2=u8(E, H, I // 2), w13_scale=u8(E, 2 * I, H // 32), w2_scale=u8(E, H, I // 32))
+    shared = {n: t[0] for n, t in good.items()}
+
+    def make(shared=None, **kw):
+        w = {**good, **kw}
+        return L.MoELayer("mxfp4", H, I, K, w["w13"], w["w2"], w["w13_scale"], w["w2_scale"], shared=shared)
+    make()
+    make(shared)
+    make({n: t[None] for n, t in shared.items()})
+    for name, t in good.items():
+        bad = [t[:, :-1], t[..., :-1], t.to(torch.int16), torch.cat([t, t], -1), None]
+        for b in bad[:-1] if name == "w13" else bad:
+            with pytest.raises(ValueError, match=f"^{name}: "):
+                make(**{name: b})
+        for b in (t, t[0, 1:], t[0].to(torch.float32), None):
+            with pytest.raises(ValueError, match=f"^shared {name}: "):
+                make({**shared, name: b})
+    with pytest.raises(ValueError, match="^w2: "):
+        make(w2=good["w2"][:3])  # fewer experts than w13
