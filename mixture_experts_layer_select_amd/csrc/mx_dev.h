@@ -16,7 +16,6 @@ namespace moe {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMxBlock = 32;
 constexpr uint32_t kMxNan = 255;

@@ -2,7 +2,7 @@
 // norm before it, and the routing-weighted combine, post norm, gate, residual
 // scale and residual behind it, each in one pass over its rows.
 //
-// One workgroup per token keeps the token's row in registers (at most 8 chunks
+// One workgroup per token keeps the token's row in registers (one or two chunks
 // of 8 columns a thread), so each input is read once: the sum of squares is
 // taken while the row is held. Bound by HBM for many tokens, by memory latency
 // for a few. Sums are fp32 in a fixed order. At H = 7168 in bf16: 16383 rows of
