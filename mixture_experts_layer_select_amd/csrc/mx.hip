@@ -315,9 +315,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     };
     auto issue = [&](const Item& c, const Desc& d, auto nx_c, int kc, uint8_t* W, uint8_t* X01, uint8_t* X23) MX_INLINE {
         constexpr int NX = decltype(nx_c)::value;
-        // Steps past the end, which the rings' counts include, bring the last one again, unused. Loading nothing there
-        // (empty buffers) gave 158.1 against 158.8 us at 128 decode tokens, 226.2 against 225.7 at 4096 and 21.0 against
-        // 20.1 for a call of 203 tokens at H = 1280; in the tall tiles' loop the test cost 6%.
+        // Steps past the end, which the rings' counts include, bring the last one again, unused. (Loading nothing there,
+        // from empty buffers, took 158.1 against 158.8 us at 128 decode tokens and 226.2 against 225.7 at 4096 while a
+        // short tile still went six steps at a time; in the tall tiles' loop that test cost 6%.)
         const uint32_t ko = (uint32_t)min(kc, nk - 1) * kMxStepB;
 #pragma unroll
         for (int i = 0; i < 4; ++i) lds_buf16(d.w, c.woff, wdist(i) + ko, W + (8 * i + wave) * 1024);
@@ -458,8 +458,10 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                 for (int j = 0; j < nk; j += 6) {
                     even(j, S0, S2);
                     odd(j + 1, S1, S0);
+                    if (j + 2 >= nk) break;  // at most three steps past the end: 158.7 -> 151.3 us at 128 decode tokens
                     even(j + 2, S2, S1);
                     odd(j + 3, S0, S2);
+                    if (j + 4 >= nk) break;
                     even(j + 4, S1, S0);
                     odd(j + 5, S2, S1);
                 }
@@ -479,7 +481,8 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
                     float v[16];
                     uint32_t mx = 0;
                     // With the divide, as moe_layer_few has it: a reciprocal instruction gives 0 where exp(-g) is above
-                    // 2^126, and its last bit moved codes. 1 us of 158 at 128 decode tokens, 2 of 226 at 4096.
+                    // 2^126, and its last bit moved codes (9 rows of 165 000 against the plain form, 3 with the divide; none
+                    // with expf, for 2% at 16384 tokens). It costs 1 us at 128 decode tokens, 2 at 4096, 10 at 16384.
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         v[r] = silu_mul(acc[0][j][r], acc[1][j][r]);
