@@ -87,10 +87,11 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 // An item's first loads are issued before the previous item's epilogue.
 //
 // Measured at H = 7168, I = 2048, 32 experts, random codes (gate/up + down): 16
-// rows an expert 95 + 59 us (5.25 and 4.2 TB/s of weights), 128 rows 122 + 81, 256
-// rows 154 + 110, 512 rows 280 to 300 + 190 to 200 (3.4 and 2.5 PFLOP/s). From 256
-// rows on the loads to LDS bound it: without the products they take 0.96 of the
-// kernel's time on zero codes, the products with their LDS reads alone 0.69.
+// rows an expert 96 + 57 us (5.2 and 4.4 TB/s of weights), 128 rows 125 + 76, 256
+// rows 159 + 109, 512 rows 290 to 304 + 190 to 198 (3.2 and 2.5 PFLOP/s). From 256
+// rows on the loads with one step in flight bound it: without the products they take
+// 0.96 of the kernel's time on zero codes (0.86 with two steps in flight, for which
+// LDS has no room), the products with their LDS reads alone 0.69.
 //
 // Waves form a 2 x 4 grid: wave (wm, wn) owns the 32-token blocks 2j + wm of
 // the tile and 64 weight rows, as 2 x NX blocks of 32x32 accumulators, NX =
