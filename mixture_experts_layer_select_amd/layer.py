@@ -215,10 +215,13 @@ class MoELayer:
 
     def check_inputs(self, x: torch.Tensor, topk_ids=None, topk_w=None):
         """x must be [T, H] in the layer's activation dtype on the weights'
-        device; given routing must be int32 ids and fp32 weights [T, k]."""
+        device, which is the current one; given routing must be int32 ids and
+        fp32 weights [T, k]."""
         act = torch.float32 if self.fmt == "f32" else torch.bfloat16
         dev = self.w13.device
         L.expect(x, "x", (act,), dev)
+        if x.is_cuda and x.get_device() != torch.cuda.current_device():
+            raise ValueError(f"x: on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
         if x.dim() != 2 or x.shape[1] != self.H:
             raise ValueError(f"x: shape {tuple(x.shape)}, expected [T, {self.H}]")
         if (topk_ids is None) != (topk_w is None):

@@ -79,3 +79,22 @@ def test_quantize_mxfp4_allocates_on_its_stream(handle):
     with torch.cuda.stream(side):
         there = torch.empty(n, dtype=torch.uint8, device=DEV)
     assert here.data_ptr() != at and there.data_ptr() == at
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("name", ["forward", "forward_few", "forward_block", "forward_fused"])
+def test_layer_of_another_device_is_refused(fmt, name, monkeypatch):
+    """Before its first step: not even buffers are made."""
+    import mixture_experts_layer_select_amd as L
+    w13, w2 = torch.zeros((E, 2 * I, H), device=DEV), torch.zeros((E, H, I), device=DEV)
+    if fmt == "mxfp4":
+        (w13, s13), (w2, s2) = L.quantize_mxfp4(w13), L.quantize_mxfp4(w2)
+    else:
+        w13, w2, s13, s2 = w13.to(torch.bfloat16), w2.to(torch.bfloat16), None, None
+    router = dict(w=torch.zeros((E, H), dtype=torch.bfloat16, device=DEV), bias=None, scoring=L.SIGMOID)
+    layer = L.MoELayer(fmt, H, I, 1, w13, w2, s13, s2, router=router)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="x: on cuda:0, the current device is cuda:1"):
+        getattr(layer, name)(x)
+    assert not layer._bufs
