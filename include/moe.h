@@ -340,6 +340,91 @@ moe_status moe_combine_norm(const void* y_perm, moe_dtype y_dt, const int32_t* s
                             const float* gain, float eps, const void* gate, int gate_rows, float alpha,
                             const void* residual, void* out, moe_dtype out_dt, void* stream);
 
+/* ---------------------------------------------------------------- training
+ * A training step of the layer: moe_route, moe_permute and moe_combine forward, the
+ * experts as moe_grouped_gemm -> moe_swiglu -> moe_grouped_gemm, and backward
+ * moe_combine_grad, moe_grouped_gemm_dx / _dw around moe_swiglu_grad, moe_combine
+ * with weights of one (the gradient of the permutation's copies), moe_route_grad,
+ * and the gate's own products as grouped products of one group. All of it can be
+ * captured in a HIP graph; nothing here has a workspace or uses atomics, so calls
+ * may overlap and results do not vary from run to run.
+ *
+ * Matrix products grouped by expert. Group g holds rows [offsets[g], offsets[g+1])
+ * of its row operands, as moe_permute writes them (offsets [n_groups+1] on the
+ * device, not descending; rows at or past max_rows are left out):
+ *   moe_grouped_gemm:     y[r,n]    = sum_k x[r,k] w[g][n][k]
+ *   moe_grouped_gemm_dx:  dx[r,k]   = sum_n dy[r,n] w[g][n][k]
+ *   moe_grouped_gemm_dw:  dw[g][n][k] = sum_{r of g} dy[r,n] x[r,k]  (a group without rows: zeros)
+ * accumulated in fp32 and rounded once. With accumulate the product is added in
+ * fp32 to what the output holds, before that rounding.
+ *   x [max_rows, K], y [max_rows, N], and their gradients likewise; w, dw
+ *   [n_groups][N][K]. w_last (dw_last), where not NULL, is the last group's [N][K],
+ *   and w (dw) then holds the others (NULL for n_groups 1): the shared expert of
+ *   moe_permute's group E_local. Inputs all in dt (MOE_BF16 or MOE_F32), the output in its
+ *   own type: MOE_F32, or MOE_BF16 from bf16. Rows past offsets[n_groups] are neither
+ *   read nor written. The output must not overlap the inputs.
+ * Limits: N and K multiples of 8 (bf16) or 4 (fp32), at most 65536; matrices 16-byte
+ * aligned; n_groups <= 1025. */
+moe_status moe_grouped_gemm(const void* x, const void* w, const void* w_last, moe_dtype dt,
+                            const int32_t* expert_offsets, int n_groups, int max_rows, int N, int K, void* y,
+                            moe_dtype y_dt, int accumulate, void* stream);
+moe_status moe_grouped_gemm_dx(const void* dy, const void* w, const void* w_last, moe_dtype dt,
+                               const int32_t* expert_offsets, int n_groups, int max_rows, int N, int K, void* dx,
+                               moe_dtype dx_dt, int accumulate, void* stream);
+moe_status moe_grouped_gemm_dw(const void* dy, const void* x, moe_dtype dt, const int32_t* expert_offsets,
+                               int n_groups, int max_rows, int N, int K, void* dw, void* dw_last, moe_dtype dw_dt,
+                               int accumulate, void* stream);
+
+/* Dropout whose mask is never stored: drop(v)_i = 0 where 16 random bits of element
+ * i are below t = floor(65536 p + 1/2), and v_i * 65536 / (65536 - t) elsewhere; a dropped
+ * value is 0 whatever it was (NaN among them). The bits are half i mod 8 (low halves
+ * first) of the four words of Philox4x32-10 with the key seed and the 128-bit counter
+ * (i / 8, offset). rng: seed and offset in device memory (two 64-bit words, 8-byte
+ * aligned), read when the call runs, so that a captured call draws anew for a new
+ * offset; the gradient's call needs the forward's. rng may be NULL where t is 0.
+ *
+ * moe_dropout: out_i = residual_i + drop(x)_i (residual NULL: 0), n elements in dt
+ *   (MOE_BF16 or MOE_F32), in fp32, rounded once. out may be x or residual. Its gradient
+ *   with respect to x is the same call on the gradient of out, without a residual.
+ * moe_swiglu: a[r,i] = drop(silu(G) U)[r,i], silu(v) = v / (1 + exp(-v)), element r*I + i
+ *   for the dropout.
+ * moe_swiglu_grad: from da: dG, dU (and a again, where a is not NULL, for the down
+ *   projection's weight gradient: the forward pass need not keep it).
+ *   gu, dgu [max_rows, 2I]: a row's G, then its U, as moe_grouped_gemm writes them with
+ *   w13; da, a [max_rows, I]; all in dt. Rows from *n_rows on (device, NULL: max_rows; the
+ *   offsets' last element for the used rows) are neither read nor written. dgu may
+ *   be gu, a may be da.
+ * Limits: 0 <= p, t <= 65535; I <= 2^24. */
+moe_status moe_dropout(const void* x, const void* residual, moe_dtype dt, int64_t n, float p, const int64_t* rng,
+                       void* out, void* stream);
+moe_status moe_swiglu(const void* gu, moe_dtype dt, const int32_t* n_rows, int max_rows, int I, float dropout_p,
+                      const int64_t* rng, void* a, void* stream);
+moe_status moe_swiglu_grad(const void* gu, const void* da, moe_dtype dt, const int32_t* n_rows, int max_rows, int I,
+                           float dropout_p, const int64_t* rng, void* dgu, void* a, void* stream);
+
+/* Gradient of moe_combine:
+ *   dy_perm[slot_to_row[t*k+j]] = topk_w[t,j] * dout[t]  and
+ *   dtopk_w[t,j] = sum_h dout[t,h] * y_perm[slot_to_row[t*k+j], h]  (0 for a pick that is not local),
+ *   dy_perm[expert_offsets[shared_group] + t] = dout[t]  (if shared_group >= 0).
+ *   dout [T,H], y_perm and dy_perm [.., H] in dt (MOE_BF16 or MOE_F32), dtopk_w [T,k]
+ *   fp32, or NULL (y_perm may then be NULL). dy_perm may be y_perm. A row belongs to at
+ *   most one slot, as in moe_permute's maps; rows of no slot are left as they are.
+ * Limits: k <= 256, H <= 2^24. */
+moe_status moe_combine_grad(const void* dout, const void* y_perm, moe_dtype dt, const int32_t* slot_to_row,
+                            const float* topk_w, int T, int k, int H, const int32_t* expert_offsets, int shared_group,
+                            void* dy_perm, float* dtopk_w, void* stream);
+
+/* Gradient of moe_route's weights with respect to its logits, the picks held fixed:
+ *   dlogits[t,e] = sum_j dtopk_w[t,j] * d topk_w[t,j] / d logits[t,e]
+ * for the scoring and renormalisation that the picks' weights were made with. logits
+ * [T,E] fp32 as moe_route writes them, topk_ids [T,k] int32, dtopk_w [T,k] fp32;
+ * dlogits [T,E] in dlogits_dt (MOE_BF16 or MOE_F32), every element written. A pick
+ * whose id is outside [0, E) has no weight and no gradient; an id that stands twice gets
+ * both. With the products dx = dlogits w_router and dw_router = dlogits^T x it is the gate's
+ * gradient. Limits: 1 <= k <= E <= 256. */
+moe_status moe_route_grad(const float* logits, const int32_t* topk_ids, const float* dtopk_w, int T, int E, int k,
+                          moe_scoring scoring, int renormalize, void* dlogits, moe_dtype dlogits_dt, void* stream);
+
 /* Host-only balanced partition of E experts into G sets of E/G with balanced
  * activation totals ([Moreh-EP] Inter-GPU load balancing: a balanced number
  * partitioning variant). LPT under the set-size limit (experts by count

@@ -27,6 +27,8 @@ EXPORTS = [
     "moe_expert_ffn_gate_up_tokens", "moe_layer_fused_workspace_size", "moe_layer_fused", "moe_combine",
     "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_layer_few_workspace_size", "moe_layer_few",
     "moe_pre_norm", "moe_combine_norm",
+    "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_swiglu", "moe_swiglu_grad", "moe_dropout",
+    "moe_combine_grad", "moe_route_grad",
     "moe_balanced_partition", "moe_gather_rows",
     "moe_count_accumulate", "moe_coactivation", "moe_affinity_partition",
     "moe_status_string", "moe_last_error_message",
@@ -88,6 +90,14 @@ def lib() -> C.CDLL:
         L.moe_layer_few.argtypes = [p, p, p, i, i, i, i, i, C.POINTER(moe_expert_weights), i, p, p, p, p, sz, p]
         L.moe_pre_norm.argtypes = [p, p, f, p, f, i, i, i, p, p, p]
         L.moe_combine_norm.argtypes = [p, i, p, p, i, i, i, p, i, p, f, p, i, f, p, p, i, p]
+        L.moe_grouped_gemm.argtypes = [p, p, p, i, p, i, i, i, i, p, i, i, p]
+        L.moe_grouped_gemm_dx.argtypes = [p, p, p, i, p, i, i, i, i, p, i, i, p]
+        L.moe_grouped_gemm_dw.argtypes = [p, p, i, p, i, i, i, i, p, p, i, i, p]
+        L.moe_swiglu.argtypes = [p, i, p, i, i, f, p, p, p]
+        L.moe_swiglu_grad.argtypes = [p, p, i, p, i, i, f, p, p, p, p]
+        L.moe_dropout.argtypes = [p, p, i, C.c_int64, f, p, p, p]
+        L.moe_combine_grad.argtypes = [p, p, i, p, p, i, i, i, p, i, p, p, p]
+        L.moe_route_grad.argtypes = [p, p, p, i, i, i, i, i, p, i, p]
         L.moe_balanced_partition.argtypes = [p, i, i, p, p, p]
         L.moe_gather_rows.argtypes = [p, i, p, p, i, sz, p]
         L.moe_count_accumulate.argtypes = [p, i, p, p]
@@ -99,7 +109,9 @@ def lib() -> C.CDLL:
         for f in ("moe_route", "moe_route_select", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_gate_up",
                   "moe_expert_ffn_down", "moe_expert_ffn_noalloc", "moe_quantize_tokens", "moe_expert_ffn_gate_up_tokens",
                   "moe_layer_fused", "moe_combine", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
-                  "moe_layer_few", "moe_pre_norm", "moe_combine_norm",
+                  "moe_layer_few", "moe_pre_norm", "moe_combine_norm", "moe_grouped_gemm", "moe_grouped_gemm_dx",
+                  "moe_grouped_gemm_dw", "moe_swiglu", "moe_swiglu_grad", "moe_dropout", "moe_combine_grad",
+                  "moe_route_grad",
                   "moe_balanced_partition", "moe_gather_rows", "moe_count_accumulate",
                   "moe_coactivation", "moe_affinity_partition"):
             getattr(L, f).restype = C.c_int
@@ -343,6 +355,56 @@ def moe_combine_norm(y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets,
     _check("moe_combine_norm", lib().moe_combine_norm(
         y_perm, y_dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, gain, eps, gate, gate_rows, alpha,
         residual, out, out_dt, _stream(stream)))
+
+
+def moe_grouped_gemm(x, w, w_last, dt, expert_offsets, n_groups, max_rows, N, K, y, y_dt, accumulate, stream=None):
+    x, w, w_last, offsets, y = _here(x, w, w_last, expert_offsets, y)
+    _check("moe_grouped_gemm", lib().moe_grouped_gemm(x, w, w_last, dt, offsets, n_groups, max_rows, N, K, y, y_dt,
+                                                      int(bool(accumulate)), _stream(stream)))
+
+
+def moe_grouped_gemm_dx(dy, w, w_last, dt, expert_offsets, n_groups, max_rows, N, K, dx, dx_dt, accumulate,
+                        stream=None):
+    dy, w, w_last, offsets, dx = _here(dy, w, w_last, expert_offsets, dx)
+    _check("moe_grouped_gemm_dx", lib().moe_grouped_gemm_dx(dy, w, w_last, dt, offsets, n_groups, max_rows, N, K, dx,
+                                                            dx_dt, int(bool(accumulate)), _stream(stream)))
+
+
+def moe_grouped_gemm_dw(dy, x, dt, expert_offsets, n_groups, max_rows, N, K, dw, dw_last, dw_dt, accumulate,
+                        stream=None):
+    dy, x, offsets, dw, dw_last = _here(dy, x, expert_offsets, dw, dw_last)
+    _check("moe_grouped_gemm_dw", lib().moe_grouped_gemm_dw(dy, x, dt, offsets, n_groups, max_rows, N, K, dw, dw_last,
+                                                            dw_dt, int(bool(accumulate)), _stream(stream)))
+
+
+def moe_swiglu(gu, dt, n_rows, max_rows, I, dropout_p, rng, a, stream=None):
+    gu, n_rows, rng, a = _here(gu, n_rows, rng, a)
+    _check("moe_swiglu", lib().moe_swiglu(gu, dt, n_rows, max_rows, I, dropout_p, rng, a, _stream(stream)))
+
+
+def moe_swiglu_grad(gu, da, dt, n_rows, max_rows, I, dropout_p, rng, dgu, a, stream=None):
+    gu, da, n_rows, rng, dgu, a = _here(gu, da, n_rows, rng, dgu, a)
+    _check("moe_swiglu_grad", lib().moe_swiglu_grad(gu, da, dt, n_rows, max_rows, I, dropout_p, rng, dgu, a,
+                                                    _stream(stream)))
+
+
+def moe_dropout(x, residual, dt, n, p, rng, out, stream=None):
+    x, residual, rng, out = _here(x, residual, rng, out)
+    _check("moe_dropout", lib().moe_dropout(x, residual, dt, n, p, rng, out, _stream(stream)))
+
+
+def moe_combine_grad(dout, y_perm, dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, dy_perm, dtopk_w,
+                     stream=None):
+    dout, y_perm, slot_to_row, topk_w, expert_offsets, dy_perm, dtopk_w = _here(
+        dout, y_perm, slot_to_row, topk_w, expert_offsets, dy_perm, dtopk_w)
+    _check("moe_combine_grad", lib().moe_combine_grad(dout, y_perm, dt, slot_to_row, topk_w, T, k, H, expert_offsets,
+                                                      shared_group, dy_perm, dtopk_w, _stream(stream)))
+
+
+def moe_route_grad(logits, topk_ids, dtopk_w, T, E, k, scoring, renormalize, dlogits, dlogits_dt, stream=None):
+    logits, topk_ids, dtopk_w, dlogits = _here(logits, topk_ids, dtopk_w, dlogits)
+    _check("moe_route_grad", lib().moe_route_grad(logits, topk_ids, dtopk_w, T, E, k, scoring, int(bool(renormalize)),
+                                                  dlogits, dlogits_dt, _stream(stream)))
 
 
 def moe_balanced_partition(counts, E, G, new_to_old, old_to_new, group_loads):

@@ -24,7 +24,7 @@ FLAGS = [
 ]
 
 SOURCES = ["api.cpp", "partition.cpp", "route.hip", "permute.hip", "ffn.hip", "combine.hip", "rebalance.hip",
-           "fused.hip", "mx.hip", "norm.hip", "few.hip"]
+           "fused.hip", "mx.hip", "norm.hip", "few.hip", "gemm.hip", "train.hip"]
 
 
 def _compile(src: str, verbose: bool, extra=(), build_dir=BUILD) -> str:

@@ -496,6 +496,152 @@ moe_status moe_combine(const void* y_perm, moe_dtype y_dt, const int32_t* slot_t
                           out, out_dt, (hipStream_t)stream);
 }
 
+// ---------------------------------------------------------------- training
+static moe_status check_grouped(const char* fn, moe_dtype dt, moe_dtype out_dt, int n_groups, int max_rows, int N,
+                                int K) {
+    REQUIRE(n_groups >= 1 && max_rows >= 0 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG,
+            "%s: need n_groups, N, K >= 1 and max_rows >= 0 (n_groups=%d max_rows=%d N=%d K=%d)", fn, n_groups,
+            max_rows, N, K);
+    REQUIRE(dt == MOE_BF16 || dt == MOE_F32, MOE_ERR_UNSUPPORTED, "%s: dt must be MOE_BF16 or MOE_F32", fn);
+    REQUIRE(out_dt == MOE_F32 || (out_dt == MOE_BF16 && dt == MOE_BF16), MOE_ERR_UNSUPPORTED,
+            "%s: the output must be MOE_F32, or MOE_BF16 from MOE_BF16", fn);
+    REQUIRE(n_groups <= 1025, MOE_ERR_UNSUPPORTED, "%s: n_groups=%d > 1025", fn, n_groups);
+    const int unit = dt == MOE_BF16 ? 8 : 4;
+    REQUIRE(N % unit == 0 && K % unit == 0 && N <= 65536 && K <= 65536, MOE_ERR_UNSUPPORTED,
+            "%s: N and K must be multiples of %d (whole 16-byte pieces) up to 65536 (N=%d K=%d)", fn, unit, N, K);
+    return MOE_OK;
+}
+
+// tiles of 64 rows times column blocks are counted in 32 bits
+static moe_status check_items(const char* fn, int n_groups, int max_rows, int cols) {
+    REQUIRE(((long)max_rows / 64 + n_groups + 1) * ((cols + 63) / 64) < (1L << 31), MOE_ERR_UNSUPPORTED,
+            "%s: max_rows=%d with %d columns has too many tiles", fn, max_rows, cols);
+    return MOE_OK;
+}
+
+moe_status moe_grouped_gemm(const void* x, const void* w, const void* w_last, moe_dtype dt,
+                            const int32_t* expert_offsets, int n_groups, int max_rows, int N, int K, void* y,
+                            moe_dtype y_dt, int accumulate, void* stream) {
+    g_msg[0] = 0;
+    moe_status s = check_grouped("moe_grouped_gemm", dt, y_dt, n_groups, max_rows, N, K);
+    if (s || max_rows == 0) return s;
+    if ((s = check_items("moe_grouped_gemm", n_groups, max_rows, N))) return s;
+    REQUIRE(x && (w || (w_last && n_groups == 1)) && expert_offsets && y, MOE_ERR_INVALID_ARG,
+            "moe_grouped_gemm: null pointer");
+    REQUIRE(aligned(x, 16) && aligned(w, 16) && aligned(w_last, 16) && aligned(y, 16), MOE_ERR_INVALID_ARG,
+            "moe_grouped_gemm: matrices must be 16-byte aligned");
+    return launch_grouped_gemm(x, w, w_last, dt, expert_offsets, n_groups, max_rows, N, K, y, y_dt, accumulate ? 1 : 0,
+                               (hipStream_t)stream);
+}
+
+moe_status moe_grouped_gemm_dx(const void* dy, const void* w, const void* w_last, moe_dtype dt,
+                               const int32_t* expert_offsets, int n_groups, int max_rows, int N, int K, void* dx,
+                               moe_dtype dx_dt, int accumulate, void* stream) {
+    g_msg[0] = 0;
+    moe_status s = check_grouped("moe_grouped_gemm_dx", dt, dx_dt, n_groups, max_rows, N, K);
+    if (s || max_rows == 0) return s;
+    if ((s = check_items("moe_grouped_gemm_dx", n_groups, max_rows, K))) return s;
+    REQUIRE(dy && (w || (w_last && n_groups == 1)) && expert_offsets && dx, MOE_ERR_INVALID_ARG,
+            "moe_grouped_gemm_dx: null pointer");
+    REQUIRE(aligned(dy, 16) && aligned(w, 16) && aligned(w_last, 16) && aligned(dx, 16), MOE_ERR_INVALID_ARG,
+            "moe_grouped_gemm_dx: matrices must be 16-byte aligned");
+    return launch_grouped_gemm_dx(dy, w, w_last, dt, expert_offsets, n_groups, max_rows, N, K, dx, dx_dt,
+                                  accumulate ? 1 : 0, (hipStream_t)stream);
+}
+
+moe_status moe_grouped_gemm_dw(const void* dy, const void* x, moe_dtype dt, const int32_t* expert_offsets,
+                               int n_groups, int max_rows, int N, int K, void* dw, void* dw_last, moe_dtype dw_dt,
+                               int accumulate, void* stream) {
+    g_msg[0] = 0;
+    moe_status s = check_grouped("moe_grouped_gemm_dw", dt, dw_dt, n_groups, max_rows, N, K);
+    if (s) return s;
+    REQUIRE((long)n_groups * ((N + 63) / 64) * ((K + 63) / 64) < (1L << 31), MOE_ERR_UNSUPPORTED,
+            "moe_grouped_gemm_dw: %d groups of %d x %d have too many tiles", n_groups, N, K);
+    REQUIRE((max_rows == 0 || (dy && x)) && (dw || (dw_last && n_groups == 1)) && expert_offsets, MOE_ERR_INVALID_ARG,
+            "moe_grouped_gemm_dw: null pointer");
+    REQUIRE(aligned(dy, 16) && aligned(x, 16) && aligned(dw, 16) && aligned(dw_last, 16), MOE_ERR_INVALID_ARG,
+            "moe_grouped_gemm_dw: matrices must be 16-byte aligned");
+    return launch_grouped_gemm_dw(dy, x, dt, expert_offsets, n_groups, max_rows, N, K, dw, dw_last, dw_dt,
+                                  accumulate ? 1 : 0, (hipStream_t)stream);
+}
+
+static moe_status check_dropout(const char* fn, moe_dtype dt, float p, const int64_t* rng) {
+    REQUIRE(dt == MOE_BF16 || dt == MOE_F32, MOE_ERR_UNSUPPORTED, "%s: dt must be MOE_BF16 or MOE_F32", fn);
+    REQUIRE(p >= 0.0f && p < 1.0f && dropout_threshold(p) < 65536u, MOE_ERR_INVALID_ARG,
+            "%s: p=%g, must be at least 0 and, in units of 2^-16, below 1", fn, (double)p);
+    REQUIRE(dropout_threshold(p) == 0 || rng, MOE_ERR_INVALID_ARG, "%s: p=%g without rng", fn, (double)p);
+    REQUIRE(aligned(rng, 8), MOE_ERR_INVALID_ARG, "%s: rng must be 8-byte aligned", fn);
+    return MOE_OK;
+}
+
+static moe_status check_units(const char* fn, moe_dtype dt, int max_rows, int I, float p, const int64_t* rng) {
+    REQUIRE(max_rows >= 0 && I >= 1, MOE_ERR_INVALID_ARG, "%s: need max_rows >= 0, I >= 1 (max_rows=%d I=%d)", fn,
+            max_rows, I);
+    REQUIRE(I <= 1 << 24, MOE_ERR_UNSUPPORTED, "%s: I=%d > 2^24", fn, I);
+    return check_dropout(fn, dt, p, rng);
+}
+
+moe_status moe_swiglu(const void* gu, moe_dtype dt, const int32_t* n_rows, int max_rows, int I, float dropout_p,
+                      const int64_t* rng, void* a, void* stream) {
+    g_msg[0] = 0;
+    const moe_status s = check_units("moe_swiglu", dt, max_rows, I, dropout_p, rng);
+    if (s || max_rows == 0) return s;
+    REQUIRE(gu && a, MOE_ERR_INVALID_ARG, "moe_swiglu: null pointer");
+    return launch_swiglu(gu, nullptr, dt, n_rows, max_rows, I, dropout_p, rng, nullptr, a, (hipStream_t)stream);
+}
+
+moe_status moe_swiglu_grad(const void* gu, const void* da, moe_dtype dt, const int32_t* n_rows, int max_rows, int I,
+                           float dropout_p, const int64_t* rng, void* dgu, void* a, void* stream) {
+    g_msg[0] = 0;
+    const moe_status s = check_units("moe_swiglu_grad", dt, max_rows, I, dropout_p, rng);
+    if (s || max_rows == 0) return s;
+    REQUIRE(gu && da && dgu, MOE_ERR_INVALID_ARG, "moe_swiglu_grad: null pointer");
+    return launch_swiglu(gu, da, dt, n_rows, max_rows, I, dropout_p, rng, dgu, a, (hipStream_t)stream);
+}
+
+moe_status moe_dropout(const void* x, const void* residual, moe_dtype dt, int64_t n, float p, const int64_t* rng,
+                       void* out, void* stream) {
+    g_msg[0] = 0;
+    REQUIRE(n >= 0, MOE_ERR_INVALID_ARG, "moe_dropout: n < 0");
+    const moe_status s = check_dropout("moe_dropout", dt, p, rng);
+    if (s || n == 0) return s;
+    REQUIRE(x && out, MOE_ERR_INVALID_ARG, "moe_dropout: null pointer");
+    return launch_dropout(x, residual, dt, n, p, rng, out, (hipStream_t)stream);
+}
+
+moe_status moe_combine_grad(const void* dout, const void* y_perm, moe_dtype dt, const int32_t* slot_to_row,
+                            const float* topk_w, int T, int k, int H, const int32_t* expert_offsets, int shared_group,
+                            void* dy_perm, float* dtopk_w, void* stream) {
+    g_msg[0] = 0;
+    REQUIRE(T >= 0 && k >= 1 && H >= 1, MOE_ERR_INVALID_ARG, "moe_combine_grad: need T >= 0, k >= 1, H >= 1");
+    REQUIRE(k <= 256, MOE_ERR_UNSUPPORTED, "moe_combine_grad: k=%d > 256", k);
+    REQUIRE(H <= 1 << 24, MOE_ERR_UNSUPPORTED, "moe_combine_grad: H=%d > 2^24", H);
+    REQUIRE(dt == MOE_BF16 || dt == MOE_F32, MOE_ERR_UNSUPPORTED, "moe_combine_grad: dt must be MOE_BF16 or MOE_F32");
+    if (T == 0) return MOE_OK;
+    REQUIRE(dout && slot_to_row && topk_w && dy_perm && (y_perm || !dtopk_w), MOE_ERR_INVALID_ARG,
+            "moe_combine_grad: null pointer");
+    REQUIRE(shared_group < 0 || expert_offsets, MOE_ERR_INVALID_ARG,
+            "moe_combine_grad: shared_group without expert_offsets");
+    return launch_combine_grad(dout, y_perm, dt, slot_to_row, topk_w, T, k, H, expert_offsets, shared_group, dy_perm,
+                               dtopk_w, (hipStream_t)stream);
+}
+
+moe_status moe_route_grad(const float* logits, const int32_t* topk_ids, const float* dtopk_w, int T, int E, int k,
+                          moe_scoring scoring, int renormalize, void* dlogits, moe_dtype dlogits_dt, void* stream) {
+    g_msg[0] = 0;
+    REQUIRE(T >= 0 && E >= 1 && k >= 1 && k <= E, MOE_ERR_INVALID_ARG,
+            "moe_route_grad: need T >= 0, 1 <= k <= E (T=%d E=%d k=%d)", T, E, k);
+    REQUIRE(E <= 256, MOE_ERR_UNSUPPORTED, "moe_route_grad: E=%d > 256", E);
+    REQUIRE(scoring == MOE_SOFTMAX || scoring == MOE_SIGMOID, MOE_ERR_INVALID_ARG,
+            "moe_route_grad: unknown scoring %d", (int)scoring);
+    REQUIRE(dlogits_dt == MOE_BF16 || dlogits_dt == MOE_F32, MOE_ERR_UNSUPPORTED,
+            "moe_route_grad: dlogits_dt must be MOE_BF16 or MOE_F32");
+    if (T == 0) return MOE_OK;
+    REQUIRE(logits && topk_ids && dtopk_w && dlogits, MOE_ERR_INVALID_ARG, "moe_route_grad: null pointer");
+    return launch_route_grad(logits, topk_ids, dtopk_w, T, E, k, scoring, renormalize ? 1 : 0, dlogits, dlogits_dt,
+                             (hipStream_t)stream);
+}
+
 moe_status moe_balanced_partition(const int64_t* counts, int E, int G, int32_t* new_to_old,
                                   int32_t* old_to_new, int64_t* group_loads) {
     g_msg[0] = 0;

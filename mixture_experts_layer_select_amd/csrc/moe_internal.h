@@ -146,6 +146,29 @@ moe_status launch_combine(const void* y_perm, moe_dtype y_dt, const int32_t* slo
                           const float* topk_w, int T, int k, int H, const int32_t* offsets,
                           int shared_group, void* out, moe_dtype out_dt, hipStream_t st);
 
+// grouped products of training (gemm.hip); w_last, dw_last: the last group's, or null
+moe_status launch_grouped_gemm(const void* x, const void* w, const void* w_last, moe_dtype dt, const int32_t* offsets,
+                               int n_groups, int max_rows, int N, int K, void* y, moe_dtype y_dt, int accumulate,
+                               hipStream_t st);
+moe_status launch_grouped_gemm_dx(const void* dy, const void* w, const void* w_last, moe_dtype dt,
+                                  const int32_t* offsets, int n_groups, int max_rows, int N, int K, void* dx,
+                                  moe_dtype dx_dt, int accumulate, hipStream_t st);
+moe_status launch_grouped_gemm_dw(const void* dy, const void* x, moe_dtype dt, const int32_t* offsets, int n_groups,
+                                  int max_rows, int N, int K, void* dw, void* dw_last, moe_dtype dw_dt, int accumulate,
+                                  hipStream_t st);
+
+// the rest of training (train.hip). p of dropout in units of 2^-16: above 65535 nothing would stay
+inline uint32_t dropout_threshold(float p) { return (uint32_t)((double)p * 65536.0 + 0.5); }
+moe_status launch_swiglu(const void* gu, const void* da, moe_dtype dt, const int32_t* n_rows, int max_rows, int I,
+                         float p, const void* rng, void* dgu, void* a, hipStream_t st);  // da null: forward
+moe_status launch_dropout(const void* x, const void* residual, moe_dtype dt, long n, float p, const void* rng,
+                          void* out, hipStream_t st);
+moe_status launch_combine_grad(const void* dout, const void* y, moe_dtype dt, const int32_t* slot_to_row,
+                               const float* topk_w, int T, int k, int H, const int32_t* offsets, int shared_group,
+                               void* dy, float* dw, hipStream_t st);
+moe_status launch_route_grad(const float* logits, const int32_t* ids, const float* dtopk_w, int T, int E, int k,
+                             int scoring, int renorm, void* dlogits, moe_dtype out_dt, hipStream_t st);
+
 moe_status launch_gather_rows(const void* src, void* dst, const int32_t* index, int n_src_rows,
                               int n_rows, size_t row_bytes, hipStream_t st);
 

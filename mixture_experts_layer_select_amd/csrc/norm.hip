@@ -30,45 +30,6 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return t;
 }
 
-// A row's bytes at the element's own alignment: the hardware takes vector
-// accesses there too, only slower where they cross a line. 16000 rows of 7171
-// bf16 columns take 200 us so, and 626 element by element.
-template <typename T>
-struct __attribute__((packed, aligned(sizeof(T)))) Eight {
-    T e[8];
-};
-
-// eight columns from h (kVec: one aligned vector or two; otherwise at the
-// element's alignment, and element by element where H ends, zeros past it)
-template <bool kVec, typename T>
-__device__ __forceinline__ void get8(const T* p, int h, int H, float* v) {
-    if constexpr (kVec) {
-        load8(p + h, v);
-    } else if (h + 8 <= H) {
-        alignas(16) Eight<T> t = *reinterpret_cast<const Eight<T>*>(p + h);
-        load8(t.e, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = load1(p + min(h + i, H - 1));  // no branches: the loads overlap
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = h + i < H ? v[i] : 0.f;
-    }
-}
-template <bool kVec, typename T>
-__device__ __forceinline__ void put8(T* p, int h, int H, const float* v) {
-    if constexpr (kVec) {
-        store8(p + h, v);
-    } else if (h + 8 <= H) {
-        alignas(16) Eight<T> t;
-        store8(t.e, v);
-        *reinterpret_cast<Eight<T>*>(p + h) = t;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (h + i < H) store1(p + h + i, v[i]);
-    }
-}
-
 // h_out may be x or delta: neither they nor the outputs are __restrict__. A thread has loaded all its columns of a row
 // before it stores the first.
 template <typename T, bool kVec, int kThreads, int kChunks>

@@ -1,0 +1,400 @@
+// What training the layer needs beside the grouped products: the gated units
+// and their gradient, dropout from a counter, and the gradients of the combine
+// and of the gate. One pass over the data each, sums in fp32 in a fixed order.
+#include "combine_dev.h"
+
+namespace moe {
+namespace {
+
+// ============================================================================ dropout
+// The random numbers come from Philox4x32-10 (J. Salmon et al., "Parallel
+// random numbers: as easy as 1, 2, 3", 2011): a block of four words is a
+// function of a 64-bit key and a 128-bit counter. Key: the seed; counter: the
+// block's number and the offset. Element i uses 16 bits, half i % 8 of block
+// i / 8, so eight neighbours (16 bytes of bf16) cost one block: ten rounds of
+// two 32 x 32 -> 64 bit products. With 32 bits an element the products alone would take
+// longer than HBM needs for a bf16 element; p is therefore held in units of 2^-16.
+struct Dropout {
+    const uint64_t* rng;  // device: seed, offset
+    uint32_t threshold;   // an element goes where its 16 bits are below; 0: no dropout, rng unread
+    float scale;          // 65536 / (65536 - threshold)
+};
+
+__device__ __forceinline__ u32x4 philox(uint64_t seed, uint64_t offset, uint64_t block) {
+    uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u32x4{c0, c1, c2, c3};
+}
+
+// bit j: element i + j stays. kWhole: i is a multiple of eight.
+template <bool kWhole>
+__device__ __forceinline__ uint32_t keep8(const Dropout& d, uint64_t seed, uint64_t offset, uint64_t i) {
+    auto bits = [&](uint64_t block) {
+        const u32x4 w = philox(seed, offset, block);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m |= ((w[j] & 0xffffu) >= d.threshold ? 1u : 0u) << (2 * j);
+            m |= ((w[j] >> 16) >= d.threshold ? 1u : 0u) << (2 * j + 1);
+        }
+        return m;
+    };
+    if constexpr (kWhole) return bits(i >> 3);
+    const int s = (int)(i & 7);
+    const uint32_t lo = bits(i >> 3);
+    return s ? (lo | bits((i >> 3) + 1) << 8) >> s : lo;
+}
+
+// out = residual + drop(x), flat. The outputs may be the inputs: a thread reads its eight elements before it writes
+// them.
+template <typename T, bool kVec>
+__global__ __launch_bounds__(256) void dropout_kernel(const T* x, const T* residual, long n, Dropout d, T* out) {
+    uint64_t seed = 0, offset = 0;
+    if (d.threshold) {
+        seed = d.rng[0];
+        offset = d.rng[1];
+    }
+    for (long i = ((long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (long)gridDim.x * 256 * 8) {
+        const int m = (int)min(8L, n - i);
+        float v[8], r[8] = {};
+        if (kVec && m == 8) {
+            get8<true>(x + i, 0, 8, v);
+            if (residual) get8<true>(residual + i, 0, 8, r);
+        } else {
+            get8<false>(x + i, 0, m, v);
+            if (residual) get8<false>(residual + i, 0, m, r);
+        }
+        const uint32_t keep = d.threshold ? keep8<true>(d, seed, offset, (uint64_t)i) : 0xffu;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = r[j] + (keep >> j & 1 ? v[j] * d.scale : 0.f);
+        if (kVec && m == 8) put8<true>(out + i, 0, 8, v);
+        else put8<false>(out + i, 0, m, v);
+    }
+}
+
+// ============================================================================ gated units
+// gu holds a row's gate columns G and, behind them, its up columns U:
+//   a = drop(silu(G) U),  silu(G) = G s,  s = 1 / (1 + exp(-G))
+//   da' = drop(da),  dU = da' silu(G),  dG = da' U s (1 + G (1 - s))
+// A thread takes eight columns of a row. fp32 has expf, whose last bits it holds. a and the gradients may be written
+// over the inputs: a thread reads all its elements before it writes.
+__device__ __forceinline__ float exp_for(float v, float) { return expf(v); }
+__device__ __forceinline__ float exp_for(float v, uint16_t) { return __expf(v); }
+
+template <typename T, bool kVec, bool kGrad>
+__global__ __launch_bounds__(256) void swiglu_kernel(const T* gu, const T* da, const int32_t* n_rows, int max_rows,
+                                                     int I, Dropout d, T* dgu, T* a) {
+    const int rows = n_rows ? max(0, min(*n_rows, max_rows)) : max_rows;
+    const int chunks = (I + 7) / 8;
+    const long n = (long)rows * chunks;
+    uint64_t seed = 0, offset = 0;
+    if (d.threshold) {
+        seed = d.rng[0];
+        offset = d.rng[1];
+    }
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
+        const long row = i / chunks;
+        const int c = (int)(i - row * chunks) * 8;
+        const size_t at = (size_t)row * I;
+        float g[8], u[8], t[8];
+        get8<kVec>(gu + 2 * at, c, I, g);
+        get8<kVec>(gu + 2 * at + I, c, I, u);
+        if (kGrad) get8<kVec>(da + at, c, I, t);
+        const uint32_t keep = d.threshold ? keep8<kVec>(d, seed, offset, (uint64_t)at + c) : 0xffu;
+        float av[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool on = keep >> j & 1;
+            const float s = 1.0f / (1.0f + exp_for(-g[j], T{}));
+            const float silu = g[j] * s;
+            av[j] = on ? silu * u[j] * d.scale : 0.f;
+            if (kGrad) {
+                const float w = on ? t[j] * d.scale : 0.f;
+                const float dg = w * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
+                u[j] = on ? w * silu : 0.f;
+                g[j] = on ? dg : 0.f;
+            }
+        }
+        if (kGrad) {
+            put8<kVec>(dgu + 2 * at, c, I, g);
+            put8<kVec>(dgu + 2 * at + I, c, I, u);
+        }
+        if (!kGrad || a) put8<kVec>(a + at, c, I, av);
+    }
+}
+
+// ============================================================================ gradient of the combine
+// out[t] = sum_j w[t,j] y[row(t,j)] + y[shared row t]:
+//   dy[row(t,j)] = w[t,j] dout[t],  dy[shared row t] = dout[t],  dw[t,j] = <dout[t], y[row(t,j)]>
+// A workgroup takes a token's picks [j0, j1) of blockIdx.y; the last one takes the shared row too. dy may be
+// y: a row belongs to one pick, and a thread reads its columns before it writes them.
+struct CombineGrad {
+    const void *dout, *y;
+    const int32_t* slot_to_row;
+    const float* topk_w;
+    int t0, T, k, H;
+    const int32_t* offsets;
+    int shared_group, per;  // picks of a workgroup
+    void* dy;
+    float* dw;  // null: y unread
+};
+
+template <typename T, bool kVec>
+__global__ __launch_bounds__(256) void combine_grad_kernel(CombineGrad p) {
+    __shared__ float red[4];
+    const int t = p.t0 + (int)blockIdx.x, H = p.H;
+    const T* d = (const T*)p.dout + (size_t)t * H;
+    const int j1 = min(p.k, ((int)blockIdx.y + 1) * p.per);
+    for (int j = blockIdx.y * p.per; j < j1; ++j) {
+        const size_t slot = (size_t)t * p.k + j;
+        const int row = p.slot_to_row[slot];
+        float sum = 0.f;
+        if (row >= 0) {
+            const float w = p.topk_w[slot];
+            const T* y = (const T*)p.y + (size_t)row * H;
+            T* dy = (T*)p.dy + (size_t)row * H;
+            for (int h = threadIdx.x * 8; h < H; h += 256 * 8) {
+                float v[8], o[8];
+                get8<kVec>(d, h, H, v);
+                if (p.dw) {
+                    get8<kVec>(y, h, H, o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v[i], o[i], sum);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= w;
+                put8<kVec>(dy, h, H, v);
+            }
+        }
+        if (p.dw) {
+#pragma unroll
+            for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s);
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+            __syncthreads();
+            if (threadIdx.x == 0) p.dw[slot] = red[0] + red[1] + red[2] + red[3];
+        }
+    }
+    if (p.shared_group >= 0 && blockIdx.y + 1 == gridDim.y) {
+        T* dy = (T*)p.dy + (size_t)(p.offsets[p.shared_group] + t) * H;
+        for (int h = threadIdx.x * 8; h < H; h += 256 * 8) {
+            float v[8];
+            get8<kVec>(d, h, H, v);
+            put8<kVec>(dy, h, H, v);
+        }
+    }
+}
+
+// ============================================================================ gradient of the gate
+// One wave per token. With D = sum_i w_i dw_i over the picks:
+//   sigmoid, renormalised: w_j = s_j / sum s   dl_j = w_j (1 - s_j) (dw_j - D)
+//   sigmoid:               w_j = s_j           dl_j = s_j (1 - s_j) dw_j
+//   softmax, renormalised: over the picks      dl_j = w_j (dw_j - D)
+//   softmax:               over all E          dl_e = [e picked] w_e dw_e - p_e D
+// Lane l owns experts 4l .. 4l + 3 of the output row and every 64th pick. An
+// expert picked twice gets both picks' sums.
+constexpr int kGateMaxE = 256;
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
+    return v;
+}
+
+template <typename TO, bool kSigmoid, bool kRenorm>
+__global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict__ logits,
+                                                         const int32_t* __restrict__ ids,
+                                                         const float* __restrict__ dtopk_w, int T, int E, int k,
+                                                         TO* __restrict__ dlogits) {
+    const int lane = threadIdx.x & 63;
+    const long t = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    constexpr int kMax = kGateMaxE / 64;  // picks of a lane
+    int id[kMax];
+    float l[kMax], dw[kMax], w[kMax];
+#pragma unroll
+    for (int i = 0; i < kMax; ++i) {
+        const int j = lane + 64 * i;
+        id[i] = j < k ? ids[t * k + j] : -1;
+        dw[i] = j < k ? dtopk_w[t * k + j] : 0.f;
+        if ((unsigned)id[i] >= (unsigned)E) id[i] = -1;  // no expert: no part in any sum
+        l[i] = id[i] >= 0 ? logits[t * E + id[i]] : 0.f;
+        if (id[i] < 0) dw[i] = 0.f;
+    }
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, d[kMax];
+    if constexpr (kSigmoid) {
+        float sum = 0.f, dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMax; ++i) {
+            w[i] = id[i] >= 0 ? 1.0f / (1.0f + expf(-l[i])) : 0.f;
+            sum += w[i];
+            dot = __builtin_fmaf(w[i], dw[i], dot);
+        }
+        if constexpr (kRenorm) {
+            sum = wave_sum(sum);
+            dot = wave_sum(dot) / sum;
+        }
+#pragma unroll
+        for (int i = 0; i < kMax; ++i)
+            d[i] = kRenorm ? w[i] / sum * (1.0f - w[i]) * (dw[i] - dot) : w[i] * (1.0f - w[i]) * dw[i];
+    } else {
+        float all[4], top = -__builtin_inff(), sum = 0.f, dot = 0.f;
+        if constexpr (kRenorm) {
+#pragma unroll
+            for (int i = 0; i < kMax; ++i) top = fmaxf(top, id[i] >= 0 ? l[i] : -__builtin_inff());
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                all[i] = 4 * lane + i < E ? logits[t * E + 4 * lane + i] : -__builtin_inff();
+                top = fmaxf(top, all[i]);
+            }
+        }
+        top = wave_max(top);
+#pragma unroll
+        for (int i = 0; i < kMax; ++i) {
+            w[i] = id[i] >= 0 ? expf(l[i] - top) : 0.f;
+            if (kRenorm) sum += w[i];
+            dot = __builtin_fmaf(w[i], dw[i], dot);
+        }
+        if constexpr (!kRenorm) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                all[i] = 4 * lane + i < E ? expf(all[i] - top) : 0.f;
+                sum += all[i];
+            }
+        }
+        sum = wave_sum(sum);
+        dot = wave_sum(dot) / sum;
+#pragma unroll
+        for (int i = 0; i < kMax; ++i) d[i] = kRenorm ? w[i] / sum * (dw[i] - dot) : w[i] / sum * dw[i];
+        if constexpr (!kRenorm) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = -all[i] / sum * dot;
+        }
+    }
+    for (int j = 0; j < k; ++j) {  // each pick to its expert's lane
+        int e = 0;
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMax; ++i)
+            if (j >> 6 == i) {
+                e = __shfl(id[i], j & 63);
+                v = __shfl(d[i], j & 63);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (e == 4 * lane + i) acc[i] += v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (4 * lane + i < E) store1(dlogits + t * E + 4 * lane + i, acc[i]);
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+Dropout dropout_of(float p, const void* rng) {
+    const uint32_t t = dropout_threshold(p);
+    return Dropout{(const uint64_t*)rng, t, 65536.0f / (float)(65536u - t)};
+}
+
+int blocks_for(long threads) {
+    return (int)std::max(1L, std::min((threads + 255) / 256, (long)device_info().cu_count * 16));
+}
+
+}  // namespace
+
+moe_status launch_dropout(const void* x, const void* residual, moe_dtype dt, long n, float p, const void* rng,
+                          void* out, hipStream_t st) {
+    const bool vec = aligned16(x) && aligned16(residual) && aligned16(out);
+    const Dropout d = dropout_of(p, rng);
+#define DROP(T, VEC)                                                                                             \
+    hipLaunchKernelGGL((dropout_kernel<T, VEC>), dim3(blocks_for((n + 7) / 8)), dim3(256), 0, st, (const T*)x, \
+                       (const T*)residual, n, d, (T*)out)
+    if (dt == MOE_BF16 && vec) DROP(uint16_t, true);
+    else if (dt == MOE_BF16) DROP(uint16_t, false);
+    else if (vec) DROP(float, true);
+    else DROP(float, false);
+#undef DROP
+    return check_launch("dropout_kernel");
+}
+
+moe_status launch_swiglu(const void* gu, const void* da, moe_dtype dt, const int32_t* n_rows, int max_rows, int I,
+                         float p, const void* rng, void* dgu, void* a, hipStream_t st) {
+    const bool vec = I % 8 == 0 && aligned16(gu) && aligned16(da) && aligned16(dgu) && aligned16(a);
+    const Dropout d = dropout_of(p, rng);
+    const dim3 grid(blocks_for((long)max_rows * ((I + 7) / 8)));
+#define UNITS(T, VEC, GRAD)                                                                                       \
+    hipLaunchKernelGGL((swiglu_kernel<T, VEC, GRAD>), grid, dim3(256), 0, st, (const T*)gu, (const T*)da, n_rows, \
+                       max_rows, I, d, (T*)dgu, (T*)a)
+#define UNITS_OF(T)                 \
+    if (vec && da) UNITS(T, true, true);  \
+    else if (vec) UNITS(T, true, false);  \
+    else if (da) UNITS(T, false, true);   \
+    else UNITS(T, false, false)
+    if (dt == MOE_BF16) {
+        UNITS_OF(uint16_t);
+    } else {
+        UNITS_OF(float);
+    }
+#undef UNITS_OF
+#undef UNITS
+    return check_launch("swiglu_kernel");
+}
+
+moe_status launch_combine_grad(const void* dout, const void* y, moe_dtype dt, const int32_t* slot_to_row,
+                               const float* topk_w, int T, int k, int H, const int32_t* offsets, int shared_group,
+                               void* dy, float* dw, hipStream_t st) {
+    const bool vec = H % 8 == 0 && aligned16(dout) && aligned16(y) && aligned16(dy);
+    constexpr int kMaxTokens = 1 << 21;
+    for (int t0 = 0; t0 < T; t0 += kMaxTokens) {
+        const int n = std::min(T - t0, kMaxTokens);
+        const int per = std::max(1, (int)std::min((long)k, (long)n * k / 1024));
+        const CombineGrad p{dout, y, slot_to_row, topk_w, t0, T, k, H, offsets, shared_group, per, dy, dw};
+        const dim3 grid(n, (k + per - 1) / per);
+#define CGRAD(T, VEC) hipLaunchKernelGGL((combine_grad_kernel<T, VEC>), grid, dim3(256), 0, st, p)
+        if (dt == MOE_BF16 && vec) CGRAD(uint16_t, true);
+        else if (dt == MOE_BF16) CGRAD(uint16_t, false);
+        else if (vec) CGRAD(float, true);
+        else CGRAD(float, false);
+#undef CGRAD
+    }
+    return check_launch("combine_grad_kernel");
+}
+
+moe_status launch_route_grad(const float* logits, const int32_t* ids, const float* dtopk_w, int T, int E, int k,
+                             int scoring, int renorm, void* dlogits, moe_dtype out_dt, hipStream_t st) {
+    const dim3 grid((T + 3) / 4);
+#define GATE(TO, SIG, REN)                                                                                           \
+    hipLaunchKernelGGL((route_grad_kernel<TO, SIG, REN>), grid, dim3(256), 0, st, logits, ids, dtopk_w, T, E, k, \
+                       (TO*)dlogits)
+#define GATE_OF(TO)                                         \
+    if (scoring == MOE_SIGMOID && renorm) GATE(TO, true, true);  \
+    else if (scoring == MOE_SIGMOID) GATE(TO, true, false);      \
+    else if (renorm) GATE(TO, false, true);                      \
+    else GATE(TO, false, false)
+    if (out_dt == MOE_BF16) {
+        GATE_OF(uint16_t);
+    } else {
+        GATE_OF(float);
+    }
+#undef GATE_OF
+#undef GATE
+    return check_launch("route_grad_kernel");
+}
+
+}  // namespace moe
