@@ -10,7 +10,8 @@
 // Q the one along its rows (x, dy, dy). An operand is stored with the
 // contraction along its rows ("K-contiguous": both of forward, Q of input) or
 // down its columns ("K-strided": P of input, both of weights).
-#include "ffn_dev.h"
+#include "mx_dev.h"
+#include "tile_dev.h"
 
 namespace moe {
 namespace {
@@ -208,11 +209,541 @@ moe_status launch_tiles(const GemmArgs& a, hipStream_t st) {
     return check_launch("gemm_tile_kernel");
 }
 
+// ============================================================================ bf16, an LDS ring
+constexpr int kBig = 256;  // rows and columns of a tile
+constexpr int kBigThreads = 512;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 lds_read_tr(const uint8_t* l) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(l));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(l + 2048));
+    const uint2 u = __builtin_bit_cast(uint2, x), v = __builtin_bit_cast(uint2, y);
+    return u32x4{u.x, u.y, v.x, v.y};
+}
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+}
+// Column (within 32) that MFMA row rho computes: a lane then holds 8 (bf16) or 4 (fp32) neighbouring columns a 16-byte
+// store, and its neighbour at lane + 32 the next ones.
+template <typename TO>
+__device__ __forceinline__ int col_of(int rho) {
+    return sizeof(TO) == 4 ? rho : 16 * (rho >> 4) + 8 * ((rho >> 2) & 1) + 4 * ((rho >> 3) & 1) + (rho & 3);
+}
+// chunk swizzles: of rows of 128 bytes read in col_of's order and in order, of rows of 512 read transposed
+template <typename TO>
+__device__ __forceinline__ int swz_p(int q) {
+    return sizeof(TO) == 4 ? (q & 7) ^ ((q >> 3) & 1) : ((q & 3) | ((q >> 3) & 1) << 2) ^ ((q >> 2) & 1);
+}
+__device__ __forceinline__ int swz_q(int q) { return (q & 7) ^ ((q >> 3) & 1); }
+__device__ __forceinline__ int swz_k(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
+
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t old, float lo, float hi) {
+    return cvt_bf16x2(lo + bf16_lo(old), hi + bf16_hi(old));
+}
+// sixteen values of a lane, to columns c0 + [0, 32) of an output row
+__device__ __forceinline__ void put16(uint16_t* o, int c0, int cols, int hi, const f32x16& v, bool add) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int c = c0 + 16 * t + 8 * hi;
+        if (c >= cols) continue;
+        u32x4* p = reinterpret_cast<u32x4*>(o + c);
+        u32x4 w;
+        if (add) {
+            const u32x4 old = *p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = add_bf16x2(old[i], v[8 * t + 2 * i], v[8 * t + 2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = cvt_bf16x2(v[8 * t + 2 * i], v[8 * t + 2 * i + 1]);
+        }
+        *p = w;
+    }
+}
+__device__ __forceinline__ void put16(float* o, int c0, int cols, int hi, const f32x16& v, bool add) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int c = c0 + 8 * t + 4 * hi;
+        if (c >= cols) continue;
+        f32x4* p = reinterpret_cast<f32x4*>(o + c);
+        f32x4 w = {v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]};
+        if (add) w += *p;
+        *p = w;
+    }
+}
+
+// ---------------------------------------------------------------- rows: forward and input
+// Which tiles a call is cut into: every workgroup finds the same plan from the
+// device-resident offsets. A group's m rows split evenly into ceil(m / height)
+// tiles, its columns into blocks of `width`.
+struct RowsPlan {
+    RowTiles<kMaxGroups> t;
+    int width;
+};
+
+// All threads call; returns the number of tiles. kUnit: widths are multiples of it.
+template <int kUnit>
+__device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restrict__ offsets, int n_groups,
+                                         int max_rows, int cols, int nk) {
+    plan.width = kBig;
+    const int NB = (cols + kBig - 1) / kBig;
+    return build_row_tiles<kBigThreads, kBig>(plan.t, offsets, n_groups, max_rows, NB);
+}
+
+template <int kForm, typename TO>
+__global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
+    constexpr bool kPc = kForm == kForward;
+    constexpr int kStepK = 64;
+    __shared__ __attribute__((aligned(1024))) uint8_t p0[32 * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t p1[32 * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t q0[32 * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t q1[32 * 1024];
+    __shared__ RowsPlan plan;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int l31 = lane & 31, hi = lane >> 5;
+    const int cols = kForm == kForward ? a.N : a.K;  // of the output
+    const int n_k = kForm == kForward ? a.K : a.N;   // the contraction, and a row of Q
+    const int nk = (n_k + kStepK - 1) / kStepK;
+    const size_t w_size = (size_t)a.N * a.K;
+    const bool apart = a.p_last != nullptr;
+    const int n_tiles = __builtin_amdgcn_readfirstlane(
+        plan_rows<kPc ? 16 : 64>(plan, a.offsets, a.n_groups, a.max_rows, cols, nk));
+    const int width = __builtin_amdgcn_readfirstlane(plan.width);
+    const int NB = (cols + width - 1) / width;
+    const int n_items = n_tiles * NB;
+    const int xcd = blockIdx.x & 7;
+    const int per_xcd = gridDim.x >> 3;
+    const int i_lo = (int)((long)n_items * xcd / 8);
+    const int i_hi = (int)((long)n_items * (xcd + 1) / 8);
+
+    // this lane's fragment offsets in a stage: K-contiguous, of k16 step h; K-strided, of block s
+    const int li = lane & 15;
+    int offp[4], offq[4];
+    if constexpr (kPc) {
+        const int r = col_of<TO>(l31);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) offp[h] = (64 * wn + r) * 128 + ((2 * h + hi) ^ swz_p<TO>(r)) * 16;
+    } else {
+        const int q = 4 * ((lane >> 4) & 1) + (li & 3), r = 8 * hi + (li >> 2);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            offp[s] = r * 512 + (((2 * wn + s) ^ swz_k(r)) << 6) + col_of<TO>(4 * q) * 2;
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) offq[h] = (32 * wm + l31) * 128 + ((2 * h + hi) ^ swz_q(l31)) * 16;
+    // This lane's part of the loads: piece i of a wave is 1 KB of an operand's stage, LDS rows 64 i + 8 wave + [0, 8) of
+    // 128 bytes, or 16 i + 2 wave + [0, 2) of 512. Its 16-byte chunk of the row, by the swizzle:
+    const int rc = 8 * wave + (lane >> 3), rs = 2 * wave + (lane >> 5);
+    const int cp = kPc ? (lane & 7) ^ swz_p<TO>(rc) : (lane & 31) ^ (swz_k(rs) << 2), cq = (lane & 7) ^ swz_q(rc);
+    uint32_t vp[4], vq[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        vp[i] = ((uint32_t)(kPc ? 64 * i + rc : 16 * i + rs) * a.K + 8 * cp) * 2;
+        vq[i] = ((uint32_t)(64 * i + rc) * n_k + 8 * cq) * 2;
+    }
+
+    // An item by numbers alone; the addresses are made anew from them, as scalars, where they are used (carried
+    // through the item loop they would be kept in vector registers, and every load would loop over its lanes).
+    struct Item {
+        int group, row0, rows, nb;
+    };
+    struct Tile {
+        const uint16_t *p, *q;  // of the first column (forward: its row of w), of the first row
+        TO* out;
+        int rows, cols, c0;
+    };
+    auto find = [&](int item) MX_INLINE {
+        Item c;
+        const MTile t = row_item_at(plan.t, a.n_groups, item, NB, c.nb);
+        c.group = t.group;
+        c.row0 = t.row0;
+        c.rows = t.rows;
+        return c;
+    };
+    auto tile_of = [&](const Item& c) MX_INLINE {
+        const int group = __builtin_amdgcn_readfirstlane(c.group), row0 = __builtin_amdgcn_readfirstlane(c.row0);
+        Tile t;
+        t.rows = __builtin_amdgcn_readfirstlane(c.rows);
+        t.c0 = __builtin_amdgcn_readfirstlane(c.nb) * width;
+        t.cols = min(width, cols - t.c0);
+        t.p = (apart && group == a.n_groups - 1 ? (const uint16_t*)a.p_last : (const uint16_t*)a.p + group * w_size) +
+              (kPc ? (size_t)t.c0 * a.K : t.c0);
+        t.q = (const uint16_t*)a.q + (size_t)row0 * n_k;
+        t.out = (TO*)a.out + (size_t)row0 * cols;
+        return t;
+    };
+    // Piece n of step kc into a stage: P's four, then Q's. What lies outside an operand is not fetched and arrives as
+    // zeros: rows past a descriptor's end, and chunks past the contraction or the columns by an offset past every
+    // descriptor (a tile's are under 2^26 bytes).
+    constexpr uint32_t kPast = 0x40000000u;
+    auto piece = [&](const Tile& c, int kc, uint8_t* P, uint8_t* Q, auto n_c) MX_INLINE {
+        constexpr int n = decltype(n_c)::value, i = n & 3;
+        const uint32_t so = (uint32_t)min(kc, nk - 1) * (kStepK * 2);  // never past the first row's end
+        const int left = n_k - kc * kStepK;                            // of the contraction
+        if constexpr (n >= 4) {
+            lds_buf16(buffer_rsrc(c.q, (uint32_t)c.rows * n_k * 2), vq[i] + (8 * cq < left ? 0u : kPast), so,
+                      Q + (8 * i + wave) * 1024);
+        } else if constexpr (kPc) {
+            lds_buf16(buffer_rsrc(c.p, (uint32_t)c.cols * a.K * 2), vp[i] + (8 * cp < left ? 0u : kPast), so,
+                      P + (8 * i + wave) * 1024);
+        } else {
+            const int rows = max(0, min(kStepK, left));
+            lds_buf16(buffer_rsrc(c.p + (size_t)kc * kStepK * a.K, rows ? (uint32_t)(rows * a.K - c.c0) * 2 : 0u),
+                      vp[i] + (8 * cp < c.cols ? 0u : kPast), 0, P + (8 * i + wave) * 1024);
+        }
+    };
+    auto load_p = [&](const Tile& c, int kc, uint8_t* P) MX_INLINE {
+        piece(c, kc, P, nullptr, std::integral_constant<int, 0>{});
+        piece(c, kc, P, nullptr, std::integral_constant<int, 1>{});
+        piece(c, kc, P, nullptr, std::integral_constant<int, 2>{});
+        piece(c, kc, P, nullptr, std::integral_constant<int, 3>{});
+        asm volatile("" ::: "memory");  // in this order: the waits count the loads
+    };
+    auto load_q = [&](const Tile& c, int kc, uint8_t* Q) MX_INLINE {  // the tile's rows, 64 at a time
+        piece(c, kc, nullptr, Q, std::integral_constant<int, 4>{});
+        if (c.rows > 64) piece(c, kc, nullptr, Q, std::integral_constant<int, 5>{});
+        if (c.rows > 128) piece(c, kc, nullptr, Q, std::integral_constant<int, 6>{});
+        if (c.rows > 192) piece(c, kc, nullptr, Q, std::integral_constant<int, 7>{});
+        asm volatile("" ::: "memory");
+    };
+    using C0 = std::integral_constant<int, 0>;
+    using C1 = std::integral_constant<int, 1>;
+    using C2 = std::integral_constant<int, 2>;
+    using C3 = std::integral_constant<int, 3>;
+    using C4 = std::integral_constant<int, 4>;
+    auto first_loads = [&](const Tile& c) MX_INLINE {
+        load_p(c, 0, p0);
+        load_q(c, 0, q0);
+        load_p(c, 1, p1);
+    };
+    auto with_nx = [&](int rows, auto f) MX_INLINE {
+        if (rows <= 64) f(C1{});
+        else if (rows <= 128) f(C2{});
+        else if (rows <= 192) f(C3{});
+        else f(C4{});
+    };
+
+    int item = i_lo + (int)(blockIdx.x >> 3);
+    if (item >= i_hi) return;
+    Item at = find(item);
+    first_loads(tile_of(at));
+    for (;;) {
+        const bool more = item + per_xcd < i_hi;
+        const Tile cur = tile_of(at);
+        auto done = [&]() MX_INLINE {
+            wait_vmcnt<0>();
+            mx_barrier();  // no stage is read or written any more
+            if (more) {
+                at = find(item + per_xcd);
+                first_loads(tile_of(at));
+            }
+        };
+        auto run = [&](auto nx_c) MX_INLINE {
+            constexpr int NX = decltype(nx_c)::value;
+            f32x16 acc[2][NX] = {};
+            u32x4 fp[2][2], fq[2][NX];
+            auto read = [&](auto h_c, const uint8_t* P, const uint8_t* Q) MX_INLINE {
+                constexpr int h = decltype(h_c)::value, b = h & 1;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if constexpr (kPc) fp[b][s] = *reinterpret_cast<const u32x4*>(P + s * 4096 + offp[h]);
+                    else fp[b][s] = lds_read_tr(P + offp[s] + h * 8192);
+                }
+#pragma unroll
+                for (int j = 0; j < NX; ++j) fq[b][j] = *reinterpret_cast<const u32x4*>(Q + j * 8192 + offq[h]);
+                __builtin_amdgcn_sched_barrier(0);  // these reads ahead of the products, and no others
+            };
+            // The products of k16 step h. The loads of a later step stand among those of h = 3 (P) and 0 (Q).
+            auto multiply = [&](auto h_c, int kc, uint8_t* P, uint8_t* Q) MX_INLINE {
+                constexpr int h = decltype(h_c)::value, b = h & 1;
+                auto col = [&](auto j_c) MX_INLINE {
+                    constexpr int j = decltype(j_c)::value;
+                    if constexpr (j < NX) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) acc[s][j] = mfma32(fp[b][s], fq[b][j], acc[s][j]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if constexpr (h == 3 || (h == 0 && j < NX)) {
+                        piece(cur, kc, P, Q, std::integral_constant<int, (h == 3 ? 0 : 4) + j>{});
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                };
+                col(C0{});
+                col(C1{});
+                col(C2{});
+                col(C3{});
+            };
+            // a step from stage (P, Q), whose first fragments are in registers; (Pn, Qn) gets the rest of the next one
+            auto step = [&](int kc, uint8_t* P, uint8_t* Q, uint8_t* Pn, uint8_t* Qn) MX_INLINE {
+                read(C1{}, P, Q);
+                multiply(C0{}, kc + 1, Pn, Qn);
+                read(C2{}, P, Q);
+                multiply(C1{}, 0, nullptr, nullptr);
+                read(C3{}, P, Q);
+                multiply(C2{}, 0, nullptr, nullptr);
+                wait_vmcnt<0>();  // the next step has landed
+                mx_barrier();     // and no wave reads this stage any more
+                read(C0{}, Pn, Qn);
+                multiply(C3{}, kc + 2, P, Q);
+            };
+            wait_vmcnt<4>();
+            mx_barrier();
+            read(C0{}, p0, q0);
+            for (int kc = 0;;) {
+                step(kc, p0, q0, p1, q1);
+                if (kc + 1 >= nk) break;
+                step(kc + 1, p1, q1, p0, q0);
+                kc += 2;
+                if (kc >= nk) break;
+            }
+            done();
+#pragma unroll
+            for (int j = 0; j < NX; ++j) {
+                const int m = 64 * j + 32 * wm + l31;
+                if (m >= cur.rows) continue;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    put16(cur.out + (size_t)m * cols + cur.c0, 64 * wn + 32 * s, cur.cols, hi, acc[s][j],
+                          a.accumulate != 0);
+            }
+        };
+        if (64 * wn < cur.cols) {
+            with_nx(cur.rows, run);
+        } else {  // a wave without columns: its part of the loads
+            wait_vmcnt<4>();
+            mx_barrier();
+            auto step = [&](int kc, uint8_t* P, uint8_t* Q, uint8_t* Pn, uint8_t* Qn) MX_INLINE {
+                load_q(cur, kc + 1, Qn);
+                wait_vmcnt<0>();
+                mx_barrier();
+                load_p(cur, kc + 2, P);
+            };
+            for (int kc = 0; kc < nk; kc += 2) {
+                step(kc, p0, q0, p1, q1);
+                if (kc + 1 < nk) step(kc + 1, p1, q1, p0, q0);
+            }
+            done();
+        }
+        if (!more) break;
+        item += per_xcd;
+    }
+}
+
+template <int kForm, typename TO>
+moe_status launch_rows(const GemmArgs& a, hipStream_t st) {
+    const long cols = kForm == kForward ? a.N : a.K;
+    const long tiles = ((long)a.max_rows + 63) / 64 + std::min(a.n_groups, a.max_rows);  // of 64 rows, at most
+    const long blocks = (cols + 63) / 64;
+    const int grid = (int)std::min((tiles * blocks + 7) / 8 * 8, (long)device_info().cu_count / 8 * 8);
+    hipLaunchKernelGGL((gemm_rows_kernel<kForm, TO>), dim3(grid), dim3(kBigThreads), 0, st, a);
+    return check_launch("gemm_rows_kernel");
+}
+
+// ---------------------------------------------------------------- weights
+template <typename TO>
+__global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a) {
+    constexpr int kStepK = 32;  // rows of a step
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[32 * 1024];  // P: 16 KB, Q behind it
+    __shared__ __attribute__((aligned(1024))) uint8_t s1[32 * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t s2[32 * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t s3[32 * 1024];
+    __shared__ int row0[kMaxGroups + 1];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int l31 = lane & 31, hi = lane >> 5;
+    const int NB = (a.K + kBig - 1) / kBig, MB = (a.N + kBig - 1) / kBig;
+    const size_t w_size = (size_t)a.N * a.K;
+    for (int g = threadIdx.x; g <= a.n_groups; g += kBigThreads) row0[g] = clamp_row(a.offsets[g], a.max_rows);
+    __syncthreads();
+    const int n_items = a.n_groups * MB * NB;
+    const int xcd = blockIdx.x & 7;
+    const int per_xcd = gridDim.x >> 3;
+    const int i_lo = (int)((long)n_items * xcd / 8);
+    const int i_hi = (int)((long)n_items * (xcd + 1) / 8);
+
+    // fragments of a stage's block s (P) or j (Q); k16 step h lies 8 KB on
+    int offp[2], offq[4];
+    {
+        const int q = 4 * ((lane >> 4) & 1) + (lane & 3), r = 8 * hi + ((lane & 15) >> 2);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) offp[s] = r * 512 + (((2 * wn + s) ^ swz_k(r)) << 6) + col_of<TO>(4 * q) * 2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) offq[j] = 16384 + r * 512 + (((2 * j + wm) ^ swz_k(r)) << 6) + 8 * q;
+    }
+    // piece i of a wave is 1 KB of an operand's stage, LDS rows 16 i + 2 wave + [0, 2)
+    const int rs = 2 * wave + (lane >> 5), cs = (lane & 31) ^ (swz_k(rs) << 2);
+    const uint32_t vp = ((uint32_t)rs * a.K + 8 * cs) * 2, vq = ((uint32_t)rs * a.N + 8 * cs) * 2;
+
+    struct Item {
+        int group, mb, nb;
+    };
+    struct Tile {
+        const uint16_t *p, *q;
+        TO* out;
+        int n_k, c0, o0, rows;  // the group's rows; first column of x and of dy, columns of dy
+    };
+    auto find = [&](int item) MX_INLINE {
+        Item c;
+        c.group = item / (MB * NB);
+        const int in = item - c.group * (MB * NB);
+        c.mb = in / NB;
+        c.nb = in - c.mb * NB;
+        return c;
+    };
+    auto tile_of = [&](const Item& c) MX_INLINE {
+        const int group = __builtin_amdgcn_readfirstlane(c.group);
+        const int r0 = __builtin_amdgcn_readfirstlane(row0[group]), r1 = __builtin_amdgcn_readfirstlane(row0[group + 1]);
+        Tile t;
+        t.n_k = max(0, r1 - r0);
+        t.c0 = __builtin_amdgcn_readfirstlane(c.nb) * kBig;
+        t.o0 = __builtin_amdgcn_readfirstlane(c.mb) * kBig;
+        t.rows = min(kBig, a.N - t.o0);
+        t.p = (const uint16_t*)a.p + (size_t)r0 * a.K;
+        t.q = (const uint16_t*)a.q + (size_t)r0 * a.N;
+        t.out = (a.out_last && group == a.n_groups - 1 ? (TO*)a.out_last : (TO*)a.out + group * w_size) +
+                (size_t)t.o0 * a.K;
+        return t;
+    };
+    // Pieces 2n and 2n + 1 of step kc: P's for n = 0, Q's for n = 1. Rows past the group are not fetched and arrive as
+    // zeros; columns past the matrix bring the next row's, for outputs that are not kept.
+    auto two = [&](const Tile& c, int kc, uint8_t* S, auto n_c) MX_INLINE {
+        constexpr bool kQ = decltype(n_c)::value == 1;
+        const int ld = kQ ? a.N : a.K, o = kQ ? c.o0 : c.c0;
+        const int left = max(0, min(kStepK, c.n_k - kc * kStepK));
+        const __amdgpu_buffer_rsrc_t d = buffer_rsrc((kQ ? c.q : c.p) + (size_t)kc * kStepK * ld + o,
+                                                     left ? (uint32_t)(left * ld - o) * 2 : 0u);
+        uint8_t* l = S + (kQ ? 16384 : 0) + wave * 1024;
+        const uint32_t v = kQ ? vq : vp;
+        lds_buf16(d, v, 0, l);
+        __builtin_amdgcn_sched_barrier(0);
+        return [=]() MX_INLINE { lds_buf16(d, v + 32u * ld, 0, l + 8192); };
+    };
+    using C0 = std::integral_constant<int, 0>;
+    using C1 = std::integral_constant<int, 1>;
+    using C2 = std::integral_constant<int, 2>;
+    using C3 = std::integral_constant<int, 3>;
+    using C4 = std::integral_constant<int, 4>;
+    auto whole = [&](const Tile& c, int kc, uint8_t* S) MX_INLINE {
+        two(c, kc, S, C0{})();
+        two(c, kc, S, C1{})();
+        asm volatile("" ::: "memory");  // in this order: the waits count the loads
+    };
+    auto first_loads = [&](const Tile& c) MX_INLINE {
+        whole(c, 0, s0);
+        whole(c, 1, s1);
+        whole(c, 2, s2);
+        two(c, 3, s3, C0{})();
+        asm volatile("" ::: "memory");
+    };
+    auto with_nx = [&](int rows, auto f) MX_INLINE {
+        if (rows <= 64) f(C1{});
+        else if (rows <= 128) f(C2{});
+        else if (rows <= 192) f(C3{});
+        else f(C4{});
+    };
+
+    int item = i_lo + (int)(blockIdx.x >> 3);
+    if (item >= i_hi) return;
+    Item at = find(item);
+    first_loads(tile_of(at));
+    for (;;) {
+        const bool more = item + per_xcd < i_hi;
+        const Tile cur = tile_of(at);
+        if (more) at = find(item + per_xcd);
+        auto run = [&](auto nx_c) MX_INLINE {
+            constexpr int NX = decltype(nx_c)::value;
+            const int nk = (cur.n_k + kStepK - 1) / kStepK;
+            f32x16 acc[2][NX] = {};
+            u32x4 fp[2][2], fq[2][NX];
+            auto read = [&](auto h_c, const uint8_t* S) MX_INLINE {
+                constexpr int h = decltype(h_c)::value;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) fp[h][s] = lds_read_tr(S + offp[s] + h * 8192);
+#pragma unroll
+                for (int j = 0; j < NX; ++j) fq[h][j] = lds_read_tr(S + offq[j] + h * 8192);
+                __builtin_amdgcn_sched_barrier(0);  // these reads ahead of the products, and no others
+            };
+            // the products of k16 step h, half of a later step's loads among them
+            auto multiply = [&](auto h_c, int kc, uint8_t* S) MX_INLINE {
+                constexpr int h = decltype(h_c)::value;
+                auto col = [&](auto j_c) MX_INLINE {
+                    constexpr int j = decltype(j_c)::value;
+                    if constexpr (j < NX) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) acc[s][j] = mfma32(fp[h][s], fq[h][j], acc[s][j]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                };
+                col(C0{});
+                auto second = two(cur, kc, S, std::integral_constant<int, 1 - h>{});
+                col(C1{});
+                col(C2{});
+                second();
+                __builtin_amdgcn_sched_barrier(0);
+                col(C3{});
+            };
+            // A step from stage S, whose first fragments are in registers; Sn holds the next one, Sp is the one before,
+            // of which P is loaded.
+            auto step = [&](int kc, uint8_t* S, uint8_t* Sn, uint8_t* Sp) MX_INLINE {
+                read(C1{}, S);
+                multiply(C0{}, kc + 3, Sp);
+                wait_vmcnt<8>();  // the next step has landed, two fly
+                mx_barrier();     // and no wave reads this stage any more
+                read(C0{}, Sn);
+                multiply(C1{}, kc + 4, S);
+            };
+            wait_vmcnt<10>();
+            mx_barrier();
+            read(C0{}, s0);
+            for (int kc = 0;;) {
+                step(kc, s0, s1, s3);
+                if (kc + 1 >= nk) break;
+                step(kc + 1, s1, s2, s0);
+                if (kc + 2 >= nk) break;
+                step(kc + 2, s2, s3, s1);
+                if (kc + 3 >= nk) break;
+                step(kc + 3, s3, s0, s2);
+                kc += 4;
+                if (kc >= nk) break;
+            }
+            wait_vmcnt<0>();
+            mx_barrier();  // no stage is read or written any more
+            if (more) first_loads(tile_of(at));
+            if (nk > 0 || !a.accumulate) {
+#pragma unroll
+                for (int j = 0; j < NX; ++j) {
+                    const int m = 64 * j + 32 * wm + l31;
+                    if (m >= cur.rows) continue;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        put16(cur.out + (size_t)m * a.K, cur.c0 + 64 * wn + 32 * s, a.K, hi, acc[s][j],
+                              a.accumulate != 0);
+                }
+            }
+        };
+        with_nx(cur.rows, run);
+        if (!more) break;
+        item += per_xcd;
+    }
+}
+
+template <typename TO>
+moe_status launch_weights(const GemmArgs& a, hipStream_t st) {
+    const long items = (long)a.n_groups * ((a.N + kBig - 1) / kBig) * ((a.K + kBig - 1) / kBig);
+    const int grid = (int)std::min((items + 7) / 8 * 8, (long)device_info().cu_count / 8 * 8);
+    hipLaunchKernelGGL(gemm_weights_kernel<TO>, dim3(grid), dim3(kBigThreads), 0, st, a);
+    return check_launch("gemm_weights_kernel");
+}
+
 template <int kForm>
 moe_status launch_form(const GemmArgs& a, moe_dtype dt, moe_dtype out_dt, hipStream_t st) {
     if (dt == MOE_F32) return launch_tiles<float, float, kForm>(a, st);
-    if (out_dt == MOE_F32) return launch_tiles<uint16_t, float, kForm>(a, st);
-    return launch_tiles<uint16_t, uint16_t, kForm>(a, st);
+    if constexpr (kForm == kWeights)
+        return out_dt == MOE_F32 ? launch_weights<float>(a, st) : launch_weights<uint16_t>(a, st);
+    else
+        return out_dt == MOE_F32 ? launch_rows<kForm, float>(a, st) : launch_rows<kForm, uint16_t>(a, st);
 }
 
 }  // namespace

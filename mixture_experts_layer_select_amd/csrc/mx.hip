@@ -3,6 +3,7 @@
 // operands in that format.
 #include "ffn_dev.h"
 #include "mx_dev.h"
+#include "tile_dev.h"
 
 namespace moe {
 namespace {
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 
 // ============================================================================ grouped GEMMs
 // Items are (m-tile of at most 256 rows, n-block of 256 weight rows); one
-// workgroup of 8 waves per CU walks them (mx_item_at's order, a contiguous slice
+// workgroup of 8 waves per CU walks them (row_item_at's order, a contiguous slice
 // per XCD). Both operands of each K step of 256 (128 bytes of a row) arrive in
 // LDS by direct global->LDS loads; the E8M0 scales of two steps come in one
 // 16-byte piece per row and sit in registers for them. A load takes 8 rows of
@@ -109,7 +110,6 @@ constexpr int kMxTM = 256;     // tokens per tile
 constexpr int kMxTN = 256;     // weight rows per tile
 constexpr int kMxThreads = 512;
 constexpr int kMxStepB = 128;  // bytes of a row per K step of 256
-constexpr int kMxPanel = 4;    // m-tiles per item panel
 constexpr int kKB = 1024;
 
 struct MxScales {  // two K steps
@@ -117,87 +117,9 @@ struct MxScales {  // two K steps
     uint8_t x[kMxTM * 16];
 };
 
-// Tiles and rows of the groups, built by every workgroup once from the
-// device-resident offsets: first tile (tile_start) and first row (row0, clamped
-// to the buffer) of each group. A group's nt = ceil(m / height) tiles split its
-// m rows evenly. Looked up from LDS alone, since every item's start waits for it.
 constexpr int kMxMaxGroups = 513;  // E_local <= 512 and a shared group: checked by the C entry
-struct MxTiles {
-    int tile_start[kMxMaxGroups + 1];
-    int row0[kMxMaxGroups + 1];
-    int sums[3];
-};
+using MxTiles = RowTiles<kMxMaxGroups>;
 
-// All threads call (it holds barriers); returns the number of tiles. The height
-// is 256 rows, or 128 or 64 where all items then still run at once: a call so
-// small takes as long as its tallest tile (nine groups of 17 rows and one of 203
-// at H = 1280, I = 384: gate/up 14.2 us with one tile of 203 rows, 10.0 with four).
-__device__ __forceinline__ int mx_build_tiles(MxTiles& tm, const int32_t* __restrict__ offsets, int n_groups,
-                                              int max_rows, int NB) {
-    for (int g = threadIdx.x; g <= n_groups; g += kMxThreads) tm.row0[g] = clamp_row(offsets[g], max_rows);
-    __syncthreads();
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int height = kMxTM >> wave;  // waves 0 to 2 count tiles of 256, 128 and 64 rows
-    auto tiles_of = [&](int g, int h) {
-        return g < n_groups ? max(0, tm.row0[g + 1] - tm.row0[g] + h - 1) / h : 0;
-    };
-    if (wave < 3) {
-        int sum = 0;
-        for (int g = lane; g < n_groups; g += 64) sum += tiles_of(g, height);
-#pragma unroll
-        for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s);
-        if (lane == 0) tm.sums[wave] = sum;
-    }
-    __syncthreads();
-    const int h = tm.sums[2] <= (int)gridDim.x / NB ? 64 : tm.sums[1] <= (int)gridDim.x / NB ? 128 : kMxTM;
-    if (wave == 0) {  // 64 groups at a time
-        int run = 0;
-        for (int g0 = 0; g0 < n_groups; g0 += 64) {
-            const int g = g0 + lane, nt = tiles_of(g, h);
-            int sum = nt;
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) {
-                const int o = __shfl_up(sum, s);
-                if (lane >= s) sum += o;
-            }
-            if (g < n_groups) tm.tile_start[g] = run + sum - nt;
-            run += __shfl(sum, 63);
-        }
-        if (lane == 0) tm.tile_start[n_groups] = run;
-    }
-    __syncthreads();
-    return tm.tile_start[n_groups];
-}
-
-// Item -> tile and n-block, in panels of kMxPanel m-tiles of a group (the last
-// one may be shorter): all n-blocks of a panel, its m-tiles fastest, so the
-// workgroups of one XCD share both operands' slices of a K step through L2.
-__device__ __forceinline__ MTile mx_item_at(const MxTiles& tm, int n_groups, int item, int NB, int& nb) {
-    const int mt = item / NB;
-    int lo = 0, hi = n_groups - 1;  // the group: the last g with tile_start[g] <= mt
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tm.tile_start[mid] <= mt) lo = mid;
-        else hi = mid - 1;
-    }
-    const int t0 = __builtin_amdgcn_readfirstlane(tm.tile_start[lo]);
-    const int nt = __builtin_amdgcn_readfirstlane(tm.tile_start[lo + 1]) - t0;
-    const int r0 = __builtin_amdgcn_readfirstlane(tm.row0[lo]);
-    const int m = __builtin_amdgcn_readfirstlane(tm.row0[lo + 1]) - r0;
-    const int local = item - t0 * NB;
-    const int pi = local / (kMxPanel * NB);  // never past the last panel
-    const int ph = min(kMxPanel, nt - pi * kMxPanel);
-    const int idx = local - pi * kMxPanel * NB;
-    nb = idx / ph;
-    const int i = pi * kMxPanel + idx - nb * ph;
-    const int each = m / nt, more = m - each * nt;  // the first `more` tiles hold one row more
-    return MTile{__builtin_amdgcn_readfirstlane(lo), r0 + i * each + min(i, more), each + (i < more ? 1 : 0)};
-}
-
-// weight row (within the wave's 32) that MFMA row rho reads: lane (l31, hi)
-// then holds the D values of 16 consecutive weight rows 16 hi + [0, 16), so
-// it writes 16 neighbouring outputs
-__device__ __forceinline__ int mx_row_of(int rho) { return 16 * ((rho >> 2) & 1) + 4 * (rho >> 3) + (rho & 3); }
 // chunk swizzles: weight rows are read in mx_row_of's order, tokens in rows'
 __device__ __forceinline__ int mx_swz_w(int q) { return ((q & 3) ^ ((q >> 2) & 1)) | ((q >> 4) & 1) << 2; }
 __device__ __forceinline__ int mx_swz_x(int q) { return (q & 7) ^ ((q >> 3) & 1); }
@@ -236,7 +158,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     const int I = p.Nw / 2;  // SwiGLU: intermediate size
     // uniform, so that the item loop and the descriptors it carries stay scalar
     const int n_items =
-        __builtin_amdgcn_readfirstlane(mx_build_tiles(tm, p.offsets, p.n_groups, p.max_rows, p.NB)) * p.NB;
+        __builtin_amdgcn_readfirstlane(build_row_tiles<kMxThreads, kMxTM>(tm, p.offsets, p.n_groups, p.max_rows, p.NB)) * p.NB;
     const int xcd = blockIdx.x & 7;
     const int per_xcd = gridDim.x >> 3;
     const int i_lo = (int)((long)n_items * xcd / 8);
@@ -291,7 +213,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_gemm_kernel(MxGemm p) {
     const int w4 = wave & 3;
     auto find = [&](int item) MX_INLINE {
         Item c;
-        c.tile = mx_item_at(tm, p.n_groups, item, p.NB, c.nb);
+        c.tile = row_item_at(tm, p.n_groups, item, p.NB, c.nb);
         auto slot = [&](int r) MX_INLINE -> uint32_t {  // of the tile's row r, clamped to it
             r = min(r, c.tile.rows - 1);
             return kGather ? (uint32_t)p.src.row_slot[c.tile.row0 + r] : (uint32_t)r;
