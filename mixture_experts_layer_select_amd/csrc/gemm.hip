@@ -274,19 +274,72 @@ __device__ __forceinline__ void put16(float* o, int c0, int cols, int hi, const 
 // ---------------------------------------------------------------- rows: forward and input
 // Which tiles a call is cut into: every workgroup finds the same plan from the
 // device-resident offsets. A group's m rows split evenly into ceil(m / height)
-// tiles, its columns into blocks of `width`.
+// tiles, the columns into blocks of `width`. Looked up from LDS alone, since
+// every item's start waits for it.
 struct RowsPlan {
     RowTiles<kMaxGroups> t;
-    int width;
+    float cost[4];  // of the best width for each height
+    int tiles[4], width[4];
 };
 
-// All threads call; returns the number of tiles. kUnit: widths are multiples of it.
+// All threads call; returns the number of tiles, and the column blocks' width. Of the heights 64 to 256 and the widths
+// 64 to 256 (multiples of kUnit) it takes the pair with the shortest estimate: the rounds of items that a workgroup
+// walks times a step's time. A step of a tile of h x w columns (NX = ceil(h / 64), mt tiles of a group sharing the
+// weights) measured about 0.35 + 0.2 NX + (0.4 + 0.65 / mt) w / 256 us at up to 256 columns, the products' term
+// halved up to 128 columns (four waves of eight have work); an item's start and end cost about three steps.
 template <int kUnit>
 __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restrict__ offsets, int n_groups,
-                                         int max_rows, int cols, int nk) {
-    plan.width = kBig;
-    const int NB = (cols + kBig - 1) / kBig;
-    return build_row_tiles<kBigThreads, kBig>(plan.t, offsets, n_groups, max_rows, NB);
+                                         int max_rows, int cols, int nk, int& width) {
+    for (int g = threadIdx.x; g <= n_groups; g += kBigThreads) plan.t.row0[g] = clamp_row(offsets[g], max_rows);
+    __syncthreads();
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (wave < 4) {
+        const int h = 64 * (wave + 1);
+        int tiles = 0;
+        float nx = 0.f, share = 0.f;  // summed over the tiles: 64-row pieces, and parts of a group's weights
+        for (int g = lane; g < n_groups; g += 64) {
+            const int m = max(0, plan.t.row0[g + 1] - plan.t.row0[g]), nt = (m + h - 1) / h;
+            if (nt) {
+                tiles += nt;
+                nx += (float)(nt * (((m + nt - 1) / nt + 63) / 64));
+                share += 1.0f;
+            }
+        }
+#pragma unroll
+        for (int s = 32; s >= 1; s >>= 1) {
+            tiles += __shfl_xor(tiles, s);
+            nx += __shfl_xor(nx, s);
+            share += __shfl_xor(share, s);
+        }
+        const int w = kBig - kUnit * lane;
+        float cost = 3e38f;
+        if (w >= 64 && tiles) {
+            const int items = tiles * ((cols + w - 1) / w), per = gridDim.x >> 3;
+            const int rounds = ((items + 7) / 8 + per - 1) / per;
+            const float part = (float)w / kBig, each = 1.0f / (float)tiles;
+            const float step = 0.35f + 0.2f * nx * each * (w <= 128 ? 0.5f : 1.0f) + (0.4f + 0.65f * share * each) * part;
+            cost = (float)rounds * step * (float)(nk + 3);
+        }
+        float best = cost;
+#pragma unroll
+        for (int s = 32; s >= 1; s >>= 1) best = fminf(best, __shfl_xor(best, s));
+        const int first = __builtin_ctzll(__ballot(cost == best));
+        if (lane == 0) {
+            plan.cost[wave] = best;
+            plan.tiles[wave] = tiles;
+            plan.width[wave] = kBig - kUnit * first;
+        }
+    }
+    __syncthreads();
+    int pick = 3;
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+        if (plan.cost[i] < plan.cost[pick]) pick = i;
+    width = plan.width[pick];
+    const int n = plan.tiles[pick];
+    number_tiles(plan.t, n_groups, 64 * (pick + 1));
+    __syncthreads();
+    return n;
 }
 
 template <int kForm, typename TO>
@@ -297,6 +350,7 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
     __shared__ __attribute__((aligned(1024))) uint8_t p1[32 * 1024];
     __shared__ __attribute__((aligned(1024))) uint8_t q0[32 * 1024];
     __shared__ __attribute__((aligned(1024))) uint8_t q1[32 * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t x2[16 * 1024];
     __shared__ RowsPlan plan;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -307,9 +361,10 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
     const int nk = (n_k + kStepK - 1) / kStepK;
     const size_t w_size = (size_t)a.N * a.K;
     const bool apart = a.p_last != nullptr;
+    int width;
     const int n_tiles = __builtin_amdgcn_readfirstlane(
-        plan_rows<kPc ? 16 : 64>(plan, a.offsets, a.n_groups, a.max_rows, cols, nk));
-    const int width = __builtin_amdgcn_readfirstlane(plan.width);
+        plan_rows<kPc ? 16 : 64>(plan, a.offsets, a.n_groups, a.max_rows, cols, nk, width));
+    width = __builtin_amdgcn_readfirstlane(width);
     const int NB = (cols + width - 1) / width;
     const int n_items = n_tiles * NB;
     const int xcd = blockIdx.x & 7;
@@ -416,6 +471,10 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
         load_p(c, 0, p0);
         load_q(c, 0, q0);
         load_p(c, 1, p1);
+        if (c.rows <= 128) {  // three stages: all but Q of the last
+            load_q(c, 1, q0 + 16384);
+            load_p(c, 2, q1);
+        }
     };
     auto with_nx = [&](int rows, auto f) MX_INLINE {
         if (rows <= 64) f(C1{});
@@ -441,6 +500,10 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
         };
         auto run = [&](auto nx_c) MX_INLINE {
             constexpr int NX = decltype(nx_c)::value;
+            // Stages: two of a tile of more than 128 rows, (p0, q0) and (p1, q1); three of a shorter one, whose Q take half
+            // the room: (p0, q0), (p1, q0 + 16 KB), (q1, x2)
+            constexpr int kStages = NX > 2 ? 2 : 3;
+            constexpr int kFly = NX > 2 ? 0 : 4 + NX;  // loads that may be in flight behind the next step's
             f32x16 acc[2][NX] = {};
             u32x4 fp[2][2], fq[2][NX];
             auto read = [&](auto h_c, const uint8_t* P, const uint8_t* Q) MX_INLINE {
@@ -474,27 +537,36 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
                 col(C2{});
                 col(C3{});
             };
-            // a step from stage (P, Q), whose first fragments are in registers; (Pn, Qn) gets the rest of the next one
-            auto step = [&](int kc, uint8_t* P, uint8_t* Q, uint8_t* Pn, uint8_t* Qn) MX_INLINE {
+            // A step from stage (P, Q), whose first fragments are in registers; (Pn, Qn) holds the next one, Ql gets the
+            // rest of the last.
+            auto step = [&](int kc, uint8_t* P, uint8_t* Q, uint8_t* Pn, uint8_t* Qn, uint8_t* Ql) MX_INLINE {
                 read(C1{}, P, Q);
-                multiply(C0{}, kc + 1, Pn, Qn);
+                multiply(C0{}, kc + kStages - 1, nullptr, Ql);
                 read(C2{}, P, Q);
                 multiply(C1{}, 0, nullptr, nullptr);
                 read(C3{}, P, Q);
                 multiply(C2{}, 0, nullptr, nullptr);
-                wait_vmcnt<0>();  // the next step has landed
-                mx_barrier();     // and no wave reads this stage any more
+                wait_vmcnt<kFly>();  // the next step has landed
+                mx_barrier();        // and no wave reads this stage any more
                 read(C0{}, Pn, Qn);
-                multiply(C3{}, kc + 2, P, Q);
+                multiply(C3{}, kc + kStages, P, Q);
             };
-            wait_vmcnt<4>();
+            wait_vmcnt<kFly + 4>();
             mx_barrier();
             read(C0{}, p0, q0);
             for (int kc = 0;;) {
-                step(kc, p0, q0, p1, q1);
-                if (kc + 1 >= nk) break;
-                step(kc + 1, p1, q1, p0, q0);
-                kc += 2;
+                if constexpr (kStages == 3) {
+                    step(kc, p0, q0, p1, q0 + 16384, x2);
+                    if (kc + 1 >= nk) break;
+                    step(kc + 1, p1, q0 + 16384, q1, x2, q0);
+                    if (kc + 2 >= nk) break;
+                    step(kc + 2, q1, x2, p0, q0, q0 + 16384);
+                } else {
+                    step(kc, p0, q0, p1, q1, q1);
+                    if (kc + 1 >= nk) break;
+                    step(kc + 1, p1, q1, p0, q0, q0);
+                }
+                kc += kStages;
                 if (kc >= nk) break;
             }
             done();
@@ -511,18 +583,21 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
         if (64 * wn < cur.cols) {
             with_nx(cur.rows, run);
         } else {  // a wave without columns: its part of the loads
-            wait_vmcnt<4>();
-            mx_barrier();
-            auto step = [&](int kc, uint8_t* P, uint8_t* Q, uint8_t* Pn, uint8_t* Qn) MX_INLINE {
-                load_q(cur, kc + 1, Qn);
-                wait_vmcnt<0>();
+            auto idle = [&](auto nx_c) MX_INLINE {
+                constexpr int NX = decltype(nx_c)::value, kStages = NX > 2 ? 2 : 3, kFly = NX > 2 ? 0 : 4 + NX;
+                wait_vmcnt<kFly + 4>();
                 mx_barrier();
-                load_p(cur, kc + 2, P);
+                for (int kc = 0, s = 0; kc < nk; ++kc) {
+                    uint8_t* P = s == 0 ? p0 : s == 1 ? p1 : q1;
+                    uint8_t* Ql = kStages == 3 ? (s == 0 ? x2 : s == 1 ? q0 : q0 + 16384) : s == 0 ? q1 : q0;
+                    load_q(cur, kc + kStages - 1, Ql);
+                    wait_vmcnt<kFly>();
+                    mx_barrier();
+                    load_p(cur, kc + kStages, P);
+                    s = s + 1 == kStages ? 0 : s + 1;
+                }
             };
-            for (int kc = 0; kc < nk; kc += 2) {
-                step(kc, p0, q0, p1, q1);
-                if (kc + 1 < nk) step(kc + 1, p1, q1, p0, q0);
-            }
+            with_nx(cur.rows, idle);
             done();
         }
         if (!more) break;

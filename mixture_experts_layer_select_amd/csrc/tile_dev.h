@@ -20,6 +20,28 @@ struct RowTiles {
     int sums[3];
 };
 
+// first tile of each group for tiles of h rows, and their number; the first wave's work, row0 must be there
+template <int kGroups>
+__device__ __forceinline__ void number_tiles(RowTiles<kGroups>& tm, int n_groups, int h) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (wave == 0) {  // 64 groups at a time
+        int run = 0;
+        for (int g0 = 0; g0 < n_groups; g0 += 64) {
+            const int g = g0 + lane;
+            const int nt = g < n_groups ? max(0, tm.row0[g + 1] - tm.row0[g] + h - 1) / h : 0;
+            int sum = nt;
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) {
+                const int o = __shfl_up(sum, s);
+                if (lane >= s) sum += o;
+            }
+            if (g < n_groups) tm.tile_start[g] = run + sum - nt;
+            run += __shfl(sum, 63);
+        }
+        if (lane == 0) tm.tile_start[n_groups] = run;
+    }
+}
+
 // All kThreads threads call (it holds barriers); returns the number of tiles. The height
 // is kTile rows, or half or a quarter of it where all items then still run at once: a call so
 // small takes as long as its tallest tile (MXFP4, nine groups of 17 rows and one of 203
@@ -43,21 +65,7 @@ __device__ __forceinline__ int build_row_tiles(RowTiles<kGroups>& tm, const int3
     }
     __syncthreads();
     const int h = tm.sums[2] <= (int)gridDim.x / NB ? kTile / 4 : tm.sums[1] <= (int)gridDim.x / NB ? kTile / 2 : kTile;
-    if (wave == 0) {  // 64 groups at a time
-        int run = 0;
-        for (int g0 = 0; g0 < n_groups; g0 += 64) {
-            const int g = g0 + lane, nt = tiles_of(g, h);
-            int sum = nt;
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) {
-                const int o = __shfl_up(sum, s);
-                if (lane >= s) sum += o;
-            }
-            if (g < n_groups) tm.tile_start[g] = run + sum - nt;
-            run += __shfl(sum, 63);
-        }
-        if (lane == 0) tm.tile_start[n_groups] = run;
-    }
+    number_tiles(tm, n_groups, h);
     __syncthreads();
     return tm.tile_start[n_groups];
 }
