@@ -27,112 +27,75 @@ struct GemmArgs {
     int accumulate;
 };
 
-// ============================================================================ tiles of 128 x 128
-// 4 waves of 64 x 64, operands through registers into LDS, two stages. One
-// step takes 64 bytes of the contraction from each K-contiguous row, or 32
-// (fp32: 16) rows of 128 columns of a K-strided operand.
-constexpr int kT = 128;
-constexpr int kStepBytes = 64;
+// ============================================================================ fp32
+// Tiles of 64 x 64, 4 waves of a quarter each, operands through registers into
+// two LDS stages. A step takes 64 bytes of the contraction: of each row of a
+// K-contiguous operand, or 16 rows of a K-strided one; loads run kAhead steps
+// ahead in a register ring. Bound by the matrix cores (an fp32 product costs
+// sixteen bf16 ones), so blocks past a tile's rows are left out. 4096 rows of 8
+// groups, 2048 x 2048: 350 us forward and input (98 TFLOP/s), 320 weights; tiles
+// of 128 took 408, 408 and 283. 203 rows of 9 groups, 768 x 1280: 38, 26 and 15
+// us, tiles of 128 102, 63 and 17.
+constexpr int kT = 64;
+constexpr int kStepF = 16;  // contraction per step
+constexpr int kAhead = 2;    // four: the same
+constexpr int kF32Grid = 4;  // workgroups per CU
+constexpr int kRowC = 64 + 16;  // LDS bytes of a K-contiguous row
+constexpr int kRowS = kT * 4 + 16;  // and of a K-strided one
+constexpr int kStageF = kT * kRowC > kStepF * kRowS ? kT * kRowC : kStepF * kRowS;
 
-template <typename T>
-struct Step {
-    static constexpr int k = kStepBytes / sizeof(T);
-    static constexpr int vec = 16 / sizeof(T);                 // elements of a 16-byte piece
-    static constexpr int kc_row = kStepBytes + 16;             // LDS bytes of a K-contiguous row
-    static constexpr int ks_row = kT * (int)sizeof(T) + 16;    // and of a K-strided one
-    static constexpr int bytes = kT * kc_row > k * ks_row ? kT * kc_row : k * ks_row;
-};
-
-// this thread's two 16-byte pieces of a step's operand tile; what lies outside the operand is zero
-template <typename T, bool kContig>
-__device__ __forceinline__ void fetch(const T* base, size_t ld, int n_out, int out0, int n_k, int k0, u32x4* r) {
-    using S = Step<T>;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int piece = threadIdx.x + 256 * i;
-        int o, k;
-        if constexpr (kContig) {
-            o = out0 + (piece >> 2);
-            k = k0 + (piece & 3) * S::vec;
-        } else {
-            constexpr int per_row = kT / S::vec;
-            k = k0 + piece / per_row;
-            o = out0 + piece % per_row * S::vec;
-        }
-        r[i] = u32x4{0, 0, 0, 0};
-        if (o < n_out && k < n_k)
-            r[i] = *reinterpret_cast<const u32x4*>(base + (kContig ? (size_t)o * ld + k : (size_t)k * ld + o));
-    }
+// Where this thread's 16 bytes of a step's operand tile lie: output index and place in the contraction.
+template <bool kContig>
+__device__ __forceinline__ int piece_o() { return kContig ? threadIdx.x >> 2 : threadIdx.x % (kT / 4) * 4; }
+template <bool kContig>
+__device__ __forceinline__ int piece_k() { return kContig ? (threadIdx.x & 3) * 4 : threadIdx.x / (kT / 4); }
+// What lies outside the operand is loaded from its edge, without branches, and staged as zeros.
+template <bool kContig>
+__device__ __forceinline__ u32x4 fetch(const float* base, size_t ld, int n_out, int out0, int n_k, int k0) {
+    const int o = min(out0 + piece_o<kContig>(), n_out - (kContig ? 1 : 4));
+    const int k = min(k0 + piece_k<kContig>(), n_k - (kContig ? 4 : 1));
+    return *reinterpret_cast<const u32x4*>(base + (kContig ? (size_t)o * ld + k : (size_t)k * ld + o));
 }
-template <typename T, bool kContig>
-__device__ __forceinline__ void stage(uint8_t* l, const u32x4* r) {
-    using S = Step<T>;
+template <bool kContig>
+__device__ __forceinline__ void stage(uint8_t* l, int n_out, int out0, int n_k, int k0, u32x4 v) {
+    const int o = piece_o<kContig>(), k = piece_k<kContig>();
+    const bool in = out0 + o < n_out && k0 + k < n_k;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int piece = threadIdx.x + 256 * i;
-        constexpr int per_row = kT / S::vec;
-        const int at = kContig ? (piece >> 2) * S::kc_row + (piece & 3) * 16
-                               : piece / per_row * S::ks_row + piece % per_row * 16;
-        *reinterpret_cast<u32x4*>(l + at) = r[i];
-    }
+    for (int e = 0; e < 4; ++e) v[e] = in ? v[e] : 0u;
+    *reinterpret_cast<u32x4*>(l + (kContig ? o * kRowC + k * 4 : k * kRowS + o * 4)) = v;
 }
-// lane (li, lk) of a 16-wide block at output o0: its 16 bytes of the contraction, elements lk * vec + [0, vec)
-template <typename T, bool kContig>
-__device__ __forceinline__ u32x4 fragment(const uint8_t* l, int o0, int li, int lk) {
-    using S = Step<T>;
+// lane (li, lk) of a 16-wide block at output o0: elements 4 lk + [0, 4) of the step's contraction
+template <bool kContig>
+__device__ __forceinline__ f32x4 fragment(const uint8_t* l, int o0, int li, int lk) {
     if constexpr (kContig) {
-        return *reinterpret_cast<const u32x4*>(l + (o0 + li) * S::kc_row + lk * 16);
+        return *reinterpret_cast<const f32x4*>(l + (o0 + li) * kRowC + lk * 16);
     } else {
-        union {
-            T e[S::vec];
-            u32x4 v;
-        } u;
+        f32x4 v;
 #pragma unroll
-        for (int j = 0; j < S::vec; ++j)
-            u.e[j] = *reinterpret_cast<const T*>(l + (lk * S::vec + j) * S::ks_row + (o0 + li) * sizeof(T));
-        return u.v;
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(l + (lk * 4 + j) * kRowS + (o0 + li) * 4);
+        return v;
     }
 }
-__device__ __forceinline__ f32x4 mfma_step(u32x4 a, u32x4 b, f32x4 c, uint16_t) { return mfma_bf16(a, b, c); }
-__device__ __forceinline__ f32x4 mfma_step(u32x4 a, u32x4 b, f32x4 c, float) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[t]), __uint_as_float(b[t]), c, 0, 0, 0);
-    return c;
-}
 
-__device__ __forceinline__ void put4(uint16_t* o, f32x4 v, bool add) {
-    uint2* p = reinterpret_cast<uint2*>(o);
-    if (add) {
-        const uint2 old = *p;
-        v += f32x4{bf16_lo(old.x), bf16_hi(old.x), bf16_lo(old.y), bf16_hi(old.y)};
-    }
-    *p = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
-__device__ __forceinline__ void put4(float* o, f32x4 v, bool add) {
-    f32x4* p = reinterpret_cast<f32x4*>(o);
-    if (add) v += *p;
-    *p = v;
-}
-
-template <typename T, typename TO, int kForm>
-__global__ __launch_bounds__(256) void gemm_tile_kernel(GemmArgs a) {
-    using S = Step<T>;
+template <int kForm>
+__global__ __launch_bounds__(256, kF32Grid) void gemm_f32_kernel(GemmArgs a) {
     constexpr bool kPc = kForm == kForward, kQc = kForm != kWeights;
-    __shared__ __attribute__((aligned(16))) uint8_t lp[2][S::bytes], lq[2][S::bytes];
+    constexpr int kB = kT / 32;  // 16-wide blocks of a wave, each way
+    __shared__ __attribute__((aligned(16))) uint8_t lp[2][kStageF], lq[2][kStageF];
     __shared__ TileMap tm;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lk = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15, lk = lane >> 4;
+    const int wp = (wave & 1) * (kT / 2), wq = (wave >> 1) * (kT / 2);
     const int cols = kForm == kForward ? a.N : a.K;  // of the output
     const int NB = (cols + kT - 1) / kT, MB = (a.N + kT - 1) / kT;
-    const size_t w_size = (size_t)a.N * a.K;
+    const size_t w_size = (size_t)a.N * a.K, ldq = kForm == kForward ? a.K : a.N;
     const bool apart = kForm == kWeights ? a.out_last != nullptr : a.p_last != nullptr;
     int n_items;
     if constexpr (kForm == kWeights) n_items = a.n_groups * MB * NB;
     else n_items = build_tile_map(tm, a.offsets, a.n_groups, a.max_rows, kT) * NB;
 
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const T *p, *q;
-        TO* out;
+        const float *p, *q;
+        float* out;
         int nb, q0, rows, n_k;  // column block; first output row, rows that end the tile, length of the contraction
         if constexpr (kForm == kWeights) {
             const int g = item / (MB * NB), in = item % (MB * NB);
@@ -141,72 +104,88 @@ __global__ __launch_bounds__(256) void gemm_tile_kernel(GemmArgs a) {
             q0 = in / NB * kT;
             rows = a.N;
             n_k = max(0, r1 - r0);
-            p = (const T*)a.p + (size_t)r0 * a.K;
-            q = (const T*)a.q + (size_t)r0 * a.N;
-            out = apart && g == a.n_groups - 1 ? (TO*)a.out_last : (TO*)a.out + g * w_size;
+            p = (const float*)a.p + (size_t)r0 * a.K;
+            q = (const float*)a.q + (size_t)r0 * a.N;
+            out = apart && g == a.n_groups - 1 ? (float*)a.out_last : (float*)a.out + g * w_size;
         } else {
             const MTile t = item_at(tm, a.offsets, a.n_groups, a.max_rows, item, NB, kT, nb);
             n_k = kForm == kForward ? a.K : a.N;
-            p = apart && t.group == a.n_groups - 1 ? (const T*)a.p_last : (const T*)a.p + t.group * w_size;
-            q = (const T*)a.q + (size_t)t.row0 * n_k;
-            out = (TO*)a.out + (size_t)t.row0 * cols;
+            p = apart && t.group == a.n_groups - 1 ? (const float*)a.p_last : (const float*)a.p + t.group * w_size;
+            q = (const float*)a.q + (size_t)t.row0 * n_k;
+            out = (float*)a.out + (size_t)t.row0 * cols;
             q0 = 0;
             rows = t.rows;
         }
-        const size_t ldq = kForm == kForward ? a.K : a.N;
-        f32x4 acc[4][4] = {};
-        u32x4 rp[2], rq[2];
-        const int nk = (n_k + S::k - 1) / S::k;
-        auto load = [&](int kc) {
-            fetch<T, kPc>(p, a.K, cols, nb * kT, n_k, kc * S::k, rp);
-            fetch<T, kQc>(q, ldq, rows, q0, n_k, kc * S::k, rq);
+        const int nj = (rows - q0 - wq + 15) / 16;  // of this wave's row blocks, those that hold rows
+        f32x4 acc[kB][kB] = {};
+        u32x4 rp[kAhead], rq[kAhead];
+        const int nk = (n_k + kStepF - 1) / kStepF;
+        auto load = [&](int kc, int s) {
+            rp[s] = fetch<kPc>(p, a.K, cols, nb * kT, n_k, kc * kStepF);
+            rq[s] = fetch<kQc>(q, ldq, rows, q0, n_k, kc * kStepF);
+        };
+        auto put = [&](int kc, int s) {
+            stage<kPc>(lp[kc & 1], cols, nb * kT, n_k, kc * kStepF, rp[s]);
+            stage<kQc>(lq[kc & 1], rows, q0, n_k, kc * kStepF, rq[s]);
         };
         __syncthreads();  // the previous item's reads
         if (nk > 0) {
-            load(0);
-            stage<T, kPc>(lp[0], rp);
-            stage<T, kQc>(lq[0], rq);
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s) load(s, s);  // steps past the end load the edge again, unused
+            put(0, 0);
+            load(kAhead, 0);
         }
-        for (int kc = 0; kc < nk; ++kc) {
-            __syncthreads();
-            if (kc + 1 < nk) load(kc + 1);
-            u32x4 fp[4], fq[4];
+        for (int k0 = 0; k0 < nk; k0 += kAhead) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                fp[i] = fragment<T, kPc>(lp[kc & 1], 64 * (wave & 1) + 16 * i, li, lk);
-                fq[i] = fragment<T, kQc>(lq[kc & 1], 64 * (wave >> 1) + 16 * i, li, lk);
-            }
+            for (int s = 0; s < kAhead; ++s) {
+                const int kc = k0 + s;
+                if (kc >= nk) break;
+                barrier_only();  // step kc is staged; the loads ahead stay in flight
+                f32x4 fp[kB], fq[kB];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < kB; ++i) {
+                    fp[i] = fragment<kPc>(lp[kc & 1], wp + 16 * i, li, lk);
+                    fq[i] = fragment<kQc>(lq[kc & 1], wq + 16 * i, li, lk);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma_step(fp[i], fq[j], acc[i][j], T{});
-            if (kc + 1 < nk) {  // the other stage: its readers passed this step's barrier
-                stage<T, kPc>(lp[(kc + 1) & 1], rp);
-                stage<T, kQc>(lq[(kc + 1) & 1], rq);
+                for (int j = 0; j < kB; ++j)
+                    if (j < nj) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int i = 0; i < kB; ++i)
+                                acc[i][j] =
+                                    __builtin_amdgcn_mfma_f32_16x16x4f32(fp[i][t], fq[j][t], acc[i][j], 0, 0, 0);
+                    }
+                put(kc + 1, (s + 1) % kAhead);  // the other stage: its readers passed this step's barrier
+                load(kc + 1 + kAhead, (s + 1) % kAhead);
             }
         }
         // lane (li, lk): columns 4 lk + [0, 4) of the block at output row li
         if (kForm == kWeights && nk == 0 && a.accumulate) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = q0 + 64 * (wave >> 1) + 16 * j + li;
+        for (int j = 0; j < kB; ++j) {
+            const int r = q0 + wq + 16 * j + li;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = nb * kT + 64 * (wave & 1) + 16 * i + 4 * lk;
-                if (r < rows && c < cols) put4(out + (size_t)r * cols + c, acc[i][j], a.accumulate != 0);
+            for (int i = 0; i < kB; ++i) {
+                const int c = nb * kT + wp + 16 * i + 4 * lk;
+                if (r < rows && c < cols) {
+                    f32x4* o = reinterpret_cast<f32x4*>(out + (size_t)r * cols + c);
+                    *o = a.accumulate ? acc[i][j] + *o : acc[i][j];
+                }
             }
         }
     }
 }
 
-template <typename T, typename TO, int kForm>
-moe_status launch_tiles(const GemmArgs& a, hipStream_t st) {
+template <int kForm>
+moe_status launch_f32(const GemmArgs& a, hipStream_t st) {
     const long nb = ((kForm == kForward ? a.N : a.K) + kT - 1) / kT;
     const long tiles = kForm == kWeights ? (long)a.n_groups * ((a.N + kT - 1) / kT)
                                          : ((long)a.max_rows + kT - 1) / kT + std::min(a.n_groups, a.max_rows);
-    const int grid = (int)std::min(tiles * nb, (long)device_info().cu_count * 2);
-    hipLaunchKernelGGL((gemm_tile_kernel<T, TO, kForm>), dim3(grid), dim3(256), 0, st, a);
-    return check_launch("gemm_tile_kernel");
+    const int grid = (int)std::min(tiles * nb, (long)device_info().cu_count * kF32Grid);
+    hipLaunchKernelGGL(gemm_f32_kernel<kForm>, dim3(grid), dim3(256), 0, st, a);
+    return check_launch("gemm_f32_kernel");
 }
 
 // ============================================================================ bf16, an LDS ring
@@ -848,7 +827,7 @@ moe_status launch_weights(const GemmArgs& a, hipStream_t st) {
 
 template <int kForm>
 moe_status launch_form(const GemmArgs& a, moe_dtype dt, moe_dtype out_dt, hipStream_t st) {
-    if (dt == MOE_F32) return launch_tiles<float, float, kForm>(a, st);
+    if (dt == MOE_F32) return launch_f32<kForm>(a, st);
     if constexpr (kForm == kWeights)
         return out_dt == MOE_F32 ? launch_weights<float>(a, st) : launch_weights<uint16_t>(a, st);
     else

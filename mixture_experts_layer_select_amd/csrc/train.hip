@@ -6,6 +6,17 @@
 namespace moe {
 namespace {
 
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
+    return v;
+}
+
 // ============================================================================ dropout
 // The random numbers come from Philox4x32-10 (J. Salmon et al., "Parallel
 // random numbers: as easy as 1, 2, 3", 2011): a block of four words is a
@@ -136,8 +147,9 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const T* gu, const T* da, c
 // ============================================================================ gradient of the combine
 // out[t] = sum_j w[t,j] y[row(t,j)] + y[shared row t]:
 //   dy[row(t,j)] = w[t,j] dout[t],  dy[shared row t] = dout[t],  dw[t,j] = <dout[t], y[row(t,j)]>
-// A workgroup takes a token's picks [j0, j1) of blockIdx.y; the last one takes the shared row too. dy may be
-// y: a row belongs to one pick, and a thread reads its columns before it writes them.
+// A workgroup takes the picks [blockIdx.y per, + per) of a token, at most kPicks; the last one takes the shared row
+// too. dy may be y: a row belongs to one pick, and a thread reads its columns before it writes them.
+constexpr int kPicks = 8;
 struct CombineGrad {
     const void *dout, *y;
     const int32_t* slot_to_row;
@@ -149,49 +161,82 @@ struct CombineGrad {
     float* dw;  // null: y unread
 };
 
-template <typename T, bool kVec>
+// Columns c * 2048 + 8 tid + [0, 8) of the token's row stay in registers for all its picks. kChunks 0: H past the
+// registers, dout read anew for each pick.
+template <typename T, bool kVec, int kChunks>
 __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGrad p) {
-    __shared__ float red[4];
+    __shared__ float red[4][kPicks];
     const int t = p.t0 + (int)blockIdx.x, H = p.H;
     const T* d = (const T*)p.dout + (size_t)t * H;
-    const int j1 = min(p.k, ((int)blockIdx.y + 1) * p.per);
-    for (int j = blockIdx.y * p.per; j < j1; ++j) {
-        const size_t slot = (size_t)t * p.k + j;
-        const int row = p.slot_to_row[slot];
-        float sum = 0.f;
-        if (row >= 0) {
-            const float w = p.topk_w[slot];
-            const T* y = (const T*)p.y + (size_t)row * H;
-            T* dy = (T*)p.dy + (size_t)row * H;
-            for (int h = threadIdx.x * 8; h < H; h += 256 * 8) {
-                float v[8], o[8];
-                get8<kVec>(d, h, H, v);
-                if (p.dw) {
-                    get8<kVec>(y, h, H, o);
+    const int j0 = blockIdx.y * p.per, n = min(p.k - j0, p.per);
+    const size_t slot = (size_t)t * p.k + j0;
+    constexpr int kHold = kChunks ? kChunks : 1;
+    float v[kHold][8];
+    if constexpr (kChunks > 0) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v[i], o[i], sum);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= w;
-                put8<kVec>(dy, h, H, v);
-            }
+        for (int c = 0; c < kChunks; ++c) {
+            const int h = (c * 256 + threadIdx.x) * 8;
+            if (h < H) get8<kVec>(d, h, H, v[c]);
         }
-        if (p.dw) {
+    }
+    float sum[kPicks];
 #pragma unroll
-            for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s);
-            __syncthreads();
-            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
-            __syncthreads();
-            if (threadIdx.x == 0) p.dw[slot] = red[0] + red[1] + red[2] + red[3];
+    for (int j = 0; j < kPicks; ++j) {
+        sum[j] = 0.f;
+        const int row = j < n ? p.slot_to_row[slot + j] : -1;
+        if (row < 0) continue;
+        const float w = p.topk_w[slot + j];
+        const T* y = (const T*)p.y + (size_t)row * H;
+        T* dy = (T*)p.dy + (size_t)row * H;
+        auto chunk = [&](int h, const float* x) {
+            float o[8];
+            if (p.dw) {
+                get8<kVec>(y, h, H, o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[j] = __builtin_fmaf(x[i], o[i], sum[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = x[i] * w;
+            put8<kVec>(dy, h, H, o);
+        };
+        if constexpr (kChunks > 0) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int h = (c * 256 + threadIdx.x) * 8;
+                if (h < H) chunk(h, v[c]);
+            }
+        } else {
+            for (int h = threadIdx.x * 8; h < H; h += 256 * 8) {
+                get8<kVec>(d, h, H, v[0]);
+                chunk(h, v[0]);
+            }
         }
     }
     if (p.shared_group >= 0 && blockIdx.y + 1 == gridDim.y) {
         T* dy = (T*)p.dy + (size_t)(p.offsets[p.shared_group] + t) * H;
-        for (int h = threadIdx.x * 8; h < H; h += 256 * 8) {
-            float v[8];
-            get8<kVec>(d, h, H, v);
-            put8<kVec>(dy, h, H, v);
+        if constexpr (kChunks > 0) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int h = (c * 256 + threadIdx.x) * 8;
+                if (h < H) put8<kVec>(dy, h, H, v[c]);
+            }
+        } else {
+            for (int h = threadIdx.x * 8; h < H; h += 256 * 8) {
+                get8<kVec>(d, h, H, v[0]);
+                put8<kVec>(dy, h, H, v[0]);
+            }
         }
+    }
+    if (p.dw) {
+#pragma unroll
+        for (int j = 0; j < kPicks; ++j) {
+            if (j >= n) continue;
+            sum[j] = wave_sum(sum[j]);
+            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][j] = sum[j];
+        }
+        __syncthreads();
+        const int j = threadIdx.x;
+        if (j < n) p.dw[slot + j] = red[0][j] + red[1][j] + red[2][j] + red[3][j];
     }
 }
 
@@ -204,17 +249,6 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGrad p) {
 // Lane l owns experts 4l .. 4l + 3 of the output row and every 64th pick. An
 // expert picked twice gets both picks' sums.
 constexpr int kGateMaxE = 256;
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s);
-    return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
-    return v;
-}
 
 template <typename TO, bool kSigmoid, bool kRenorm>
 __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict__ logits,
@@ -305,6 +339,75 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
         if (4 * lane + i < E) store1(dlogits + t * E + 4 * lane + i, acc[i]);
 }
 
+// The same for at most eight picks where nothing runs over all E: a wave takes eight tokens, a pick in each lane, and
+// puts their rows together in LDS. 16384 tokens of 256 experts take 5.7 us so, 11.1 with a wave for each token.
+template <int kCtrl>
+__device__ __forceinline__ float lane_swap(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, false));
+}
+template <typename F>
+__device__ __forceinline__ float over_eight(float v, F f) {  // over eight neighbouring lanes, the same in each
+    v = f(v, lane_swap<0xb1>(v));   // lane ^ 1
+    v = f(v, lane_swap<0x4e>(v));   // lane ^ 2
+    return f(v, lane_swap<0x141>(v));  // half mirror: lane ^ 7, of the other four
+}
+
+template <typename TO, bool kSigmoid, bool kRenorm>
+__global__ __launch_bounds__(256) void route_grad_few_kernel(const float* __restrict__ logits,
+                                                             const int32_t* __restrict__ ids,
+                                                             const float* __restrict__ dtopk_w, int T, int E, int k,
+                                                             bool vec, TO* __restrict__ dlogits) {
+    __shared__ __attribute__((aligned(16))) float rows[4][8 * kGateMaxE];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 7;
+    float* row = rows[wave];
+    const long t0 = ((long)blockIdx.x * 4 + wave) * 8, t = t0 + (lane >> 3);
+    const bool pick = t < T && j < k;
+    int id = pick ? ids[t * k + j] : -1;
+    float dw = pick ? dtopk_w[t * k + j] : 0.f;
+    if ((unsigned)id >= (unsigned)E) id = -1;
+    const float l = id >= 0 ? logits[t * E + id] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4*>(row + i * kGateMaxE + 4 * lane) = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto add = [](float a, float b) { return a + b; };
+    auto most = [](float a, float b) { return fmaxf(a, b); };
+    if (id < 0) dw = 0.f;
+    float d;
+    if constexpr (kSigmoid) {
+        const float s = id >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.f;
+        if constexpr (kRenorm) {
+            const float sum = over_eight(s, add), dot = over_eight(s * dw, add) / sum;
+            d = s / sum * (1.0f - s) * (dw - dot);
+        } else {
+            d = s * (1.0f - s) * dw;
+        }
+    } else {
+        const float top = over_eight(id >= 0 ? l : -__builtin_inff(), most);
+        const float e = id >= 0 ? expf(l - top) : 0.f;
+        const float sum = over_eight(e, add), dot = over_eight(e * dw, add) / sum;
+        d = e / sum * (dw - dot);
+    }
+    // one pick of each token at a time, in order: an id that stands twice gets both
+    for (int i = 0; i < k; ++i)
+        if (j == i && id >= 0) row[(lane >> 3) * kGateMaxE + id] += d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (t0 + i >= T) break;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(row + i * kGateMaxE + 4 * lane);
+        TO* o = dlogits + (t0 + i) * E + 4 * lane;
+        if (vec) {
+            if (4 * lane < E) {
+                if constexpr (sizeof(TO) == 2)
+                    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                else *reinterpret_cast<f32x4*>(o) = v;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * lane + e < E) store1(o + e, v[e]);
+        }
+    }
+}
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 Dropout dropout_of(float p, const void* rng) {
@@ -360,17 +463,29 @@ moe_status launch_combine_grad(const void* dout, const void* y, moe_dtype dt, co
                                const float* topk_w, int T, int k, int H, const int32_t* offsets, int shared_group,
                                void* dy, float* dw, hipStream_t st) {
     const bool vec = H % 8 == 0 && aligned16(dout) && aligned16(y) && aligned16(dy);
-    constexpr int kMaxTokens = 1 << 21;
+    constexpr int kMaxTokens = 1 << 21;  // of one launch: a grid of 2^32 work items and more runs short
     for (int t0 = 0; t0 < T; t0 += kMaxTokens) {
         const int n = std::min(T - t0, kMaxTokens);
-        const int per = std::max(1, (int)std::min((long)k, (long)n * k / 1024));
+        // picks are spread over workgroups until there are about four of these per CU
+        const int per = std::max(1, (int)std::min((long)std::min(k, kPicks), (long)n * k / 1024));
         const CombineGrad p{dout, y, slot_to_row, topk_w, t0, T, k, H, offsets, shared_group, per, dy, dw};
         const dim3 grid(n, (k + per - 1) / per);
-#define CGRAD(T, VEC) hipLaunchKernelGGL((combine_grad_kernel<T, VEC>), grid, dim3(256), 0, st, p)
-        if (dt == MOE_BF16 && vec) CGRAD(uint16_t, true);
-        else if (dt == MOE_BF16) CGRAD(uint16_t, false);
-        else if (vec) CGRAD(float, true);
-        else CGRAD(float, false);
+#define CGRAD(T, VEC, CHUNKS) hipLaunchKernelGGL((combine_grad_kernel<T, VEC, CHUNKS>), grid, dim3(256), 0, st, p)
+#define CGRAD_OF(T, VEC)                  \
+    if (H <= 2048) CGRAD(T, VEC, 1);      \
+    else if (H <= 4096) CGRAD(T, VEC, 2); \
+    else if (H <= 8192) CGRAD(T, VEC, 4); \
+    else CGRAD(T, VEC, 0)
+        if (dt == MOE_BF16 && vec) {
+            CGRAD_OF(uint16_t, true);
+        } else if (dt == MOE_BF16) {
+            CGRAD_OF(uint16_t, false);
+        } else if (vec) {
+            CGRAD_OF(float, true);
+        } else {
+            CGRAD_OF(float, false);
+        }
+#undef CGRAD_OF
 #undef CGRAD
     }
     return check_launch("combine_grad_kernel");
@@ -378,6 +493,25 @@ moe_status launch_combine_grad(const void* dout, const void* y, moe_dtype dt, co
 
 moe_status launch_route_grad(const float* logits, const int32_t* ids, const float* dtopk_w, int T, int E, int k,
                              int scoring, int renorm, void* dlogits, moe_dtype out_dt, hipStream_t st) {
+    if (k <= 8 && (scoring == MOE_SIGMOID || renorm)) {
+        const dim3 few((T + 31) / 32);
+        const bool vec = E % 4 == 0 && aligned16(dlogits);
+#define GATE(TO, SIG, REN)                                                                                           \
+    hipLaunchKernelGGL((route_grad_few_kernel<TO, SIG, REN>), few, dim3(256), 0, st, logits, ids, dtopk_w, T, E, k, \
+                       vec, (TO*)dlogits)
+#define GATE_OF(TO)                                              \
+    if (scoring == MOE_SIGMOID && renorm) GATE(TO, true, true);  \
+    else if (scoring == MOE_SIGMOID) GATE(TO, true, false);      \
+    else GATE(TO, false, true)
+        if (out_dt == MOE_BF16) {
+            GATE_OF(uint16_t);
+        } else {
+            GATE_OF(float);
+        }
+#undef GATE_OF
+#undef GATE
+        return check_launch("route_grad_few_kernel");
+    }
     const dim3 grid((T + 3) / 4);
 #define GATE(TO, SIG, REN)                                                                                           \
     hipLaunchKernelGGL((route_grad_kernel<TO, SIG, REN>), grid, dim3(256), 0, st, logits, ids, dtopk_w, T, E, k, \
