@@ -241,7 +241,8 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGrad p) {
 }
 
 // ============================================================================ gradient of the gate
-// One wave per token. With D = sum_i w_i dw_i over the picks:
+// One wave per token. With D = sum_i w_i dw_i over the picks (of the finished weights, so that a single renormalised
+// pick's gradient is exactly 0):
 //   sigmoid, renormalised: w_j = s_j / sum s   dl_j = w_j (1 - s_j) (dw_j - D)
 //   sigmoid:               w_j = s_j           dl_j = s_j (1 - s_j) dw_j
 //   softmax, renormalised: over the picks      dl_j = w_j (dw_j - D)
@@ -277,15 +278,13 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
         for (int i = 0; i < kMax; ++i) {
             w[i] = id[i] >= 0 ? 1.0f / (1.0f + expf(-l[i])) : 0.f;
             sum += w[i];
-            dot = __builtin_fmaf(w[i], dw[i], dot);
         }
-        if constexpr (kRenorm) {
-            sum = wave_sum(sum);
-            dot = wave_sum(dot) / sum;
-        }
+        sum = kRenorm ? wave_sum(sum) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < kMax; ++i)
-            d[i] = kRenorm ? w[i] / sum * (1.0f - w[i]) * (dw[i] - dot) : w[i] * (1.0f - w[i]) * dw[i];
+        for (int i = 0; i < kMax; ++i) dot += w[i] / sum * dw[i];
+        dot = kRenorm ? wave_sum(dot) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kMax; ++i) d[i] = w[i] / sum * (1.0f - w[i]) * (dw[i] - dot);
     } else {
         float all[4], top = -__builtin_inff(), sum = 0.f, dot = 0.f;
         if constexpr (kRenorm) {
@@ -303,7 +302,6 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
         for (int i = 0; i < kMax; ++i) {
             w[i] = id[i] >= 0 ? expf(l[i] - top) : 0.f;
             if (kRenorm) sum += w[i];
-            dot = __builtin_fmaf(w[i], dw[i], dot);
         }
         if constexpr (!kRenorm) {
 #pragma unroll
@@ -313,7 +311,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
             }
         }
         sum = wave_sum(sum);
-        dot = wave_sum(dot) / sum;
+#pragma unroll
+        for (int i = 0; i < kMax; ++i) dot += w[i] / sum * dw[i];
+        dot = wave_sum(dot);
 #pragma unroll
         for (int i = 0; i < kMax; ++i) d[i] = kRenorm ? w[i] / sum * (dw[i] - dot) : w[i] / sum * dw[i];
         if constexpr (!kRenorm) {
@@ -375,16 +375,16 @@ __global__ __launch_bounds__(256) void route_grad_few_kernel(const float* __rest
     if constexpr (kSigmoid) {
         const float s = id >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.f;
         if constexpr (kRenorm) {
-            const float sum = over_eight(s, add), dot = over_eight(s * dw, add) / sum;
-            d = s / sum * (1.0f - s) * (dw - dot);
+            const float w = s / over_eight(s, add), dot = over_eight(w * dw, add);
+            d = w * (1.0f - s) * (dw - dot);
         } else {
             d = s * (1.0f - s) * dw;
         }
     } else {
         const float top = over_eight(id >= 0 ? l : -__builtin_inff(), most);
         const float e = id >= 0 ? expf(l - top) : 0.f;
-        const float sum = over_eight(e, add), dot = over_eight(e * dw, add) / sum;
-        d = e / sum * (dw - dot);
+        const float w = e / over_eight(e, add), dot = over_eight(w * dw, add);
+        d = w * (dw - dot);
     }
     // one pick of each token at a time, in order: an id that stands twice gets both
     for (int i = 0; i < k; ++i)

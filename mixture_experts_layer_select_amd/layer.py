@@ -43,6 +43,44 @@ class LayerBuffers:
     n: Optional[torch.Tensor] = None  # forward_block: the layer's normed input
 
 
+@dataclass
+class TrainStep:
+    """What backward needs of a forward_train: its inputs by reference, and the
+    layer's buffers for T training tokens, which the next forward_train of as
+    many tokens fills again."""
+    x: torch.Tensor
+    b: LayerBuffers
+    gu: torch.Tensor      # [T*k+T, 2I] gate and up rows; their gradient after backward
+    a: torch.Tensor       # [T*k+T, I] gated units
+    dx: torch.Tensor      # [T, H]
+    dtopk_w: torch.Tensor  # [T, k]
+    topk_ids: torch.Tensor
+    topk_w: torch.Tensor
+    routed_here: bool     # by this layer's router, all of whose experts it holds
+    dropout: float
+    out_dropout: float
+    rng: Optional[torch.Tensor]
+    serial: int
+
+    @property
+    def out(self) -> torch.Tensor:
+        return self.b.out
+
+
+@dataclass
+class LayerGrads:
+    """Gradients as backward returns them: of the inputs (dx in the activation
+    dtype; topk_w fp32), and of the weights in fp32, shaped as the weights."""
+    w13: torch.Tensor
+    w2: torch.Tensor
+    shared_w13: Optional[torch.Tensor] = None
+    shared_w2: Optional[torch.Tensor] = None
+    router_w: Optional[torch.Tensor] = None
+    router_bias: Optional[torch.Tensor] = None
+    dx: Optional[torch.Tensor] = None
+    topk_w: Optional[torch.Tensor] = None
+
+
 class MoELayer:
     """Weights of one GPU's expert share (+ optional shared expert and router).
 
@@ -121,9 +159,10 @@ class MoELayer:
                 and (r["scoring"] == L.SIGMOID or r.get("renormalize", True)))
 
     # ------------------------------------------------------------------ buffers
-    def buffers(self, T: int, device=None) -> LayerBuffers:
-        if T in self._bufs:
-            return self._bufs[T]
+    def buffers(self, T: int, device=None, key=None) -> LayerBuffers:
+        key = T if key is None else key
+        if key in self._bufs:
+            return self._bufs[key]
         device = device or self.w13.device
         k, H = self.k, self.H
         cap = T * k + T
@@ -161,7 +200,7 @@ class MoELayer:
         if self.uses_route_select(T):
             b.ws_route = torch.empty(L.moe_route_select_workspace_size(T, E), dtype=torch.uint8,
                                      device=device)
-        self._bufs[T] = b
+        self._bufs[key] = b
         return b
 
     # ------------------------------------------------------------------ steps
@@ -349,6 +388,173 @@ class MoELayer:
                            1 if gate is None else gate.shape[0], alpha, b.h, b.out, self.act_dt, stream)
         return b
 
+    # ------------------------------------------------------------------ training
+    def _check_train(self):
+        if self.fmt not in ("f32", "bf16"):
+            raise ValueError(f"training needs f32 or bf16 weights, not {self.fmt}")
+        unit = 8 if self.fmt == "bf16" else 4
+        sizes = dict(H=self.H, I=self.I)
+        if self.router is not None:
+            sizes["the router's experts"] = self.router["w"].shape[0]
+        for name, n in sizes.items():
+            if n % unit:
+                raise ValueError(f"training in {self.fmt}: {name} = {n} is not a multiple of {unit}")
+
+    def _check_rng(self, rng, *p):
+        if any(p):
+            if rng is None:
+                raise ValueError("dropout needs rng")
+            L.expect(rng, "rng", (torch.int64,), self.w13.device)
+            if tuple(rng.shape) != (2, 2):
+                raise ValueError(f"rng: shape {tuple(rng.shape)}, expected (2, 2)")
+
+    def forward_train(self, x: torch.Tensor, topk_ids=None, topk_w=None, *, dropout: float = 0.0, residual=None,
+                      out_dropout: float = 0.0, rng=None, stream=None) -> TrainStep:
+        """The layer with what its gradients need kept (f32 and bf16 weights):
+        out = residual + drop(combine(...)), with `dropout` inside the experts (on
+        the gated units) and `out_dropout` on the layer's output. rng: int64
+        [2, 2] on the device, seed and offset of the experts' dropout and of the
+        output's, read when the calls run and again by backward, so it changes
+        only after backward. x is read again by backward. One step per number of
+        tokens: the next forward_train of as many tokens takes its buffers."""
+        self._check_train()
+        self.check_inputs(x, topk_ids, topk_w)
+        self._check_rng(rng, dropout, out_dropout)
+        T = x.shape[0]
+        L.expect(residual, "residual", (x.dtype,), x.device)
+        if residual is not None and residual.shape != x.shape:
+            raise ValueError(f"residual: shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+        step = self._train_step(x, topk_ids, topk_w, dropout, out_dropout, rng)
+        b, r, cap, dt = step.b, self.router, T * self.k + T, self.act_dt
+        if topk_ids is None:  # backward needs every logit, so moe_route at every size
+            L.moe_route(x, r["w"], r.get("bias"), dt, T, self.H, r["w"].shape[0], self.k, r["scoring"],
+                        r.get("renormalize", True), b.logits, b.topk_ids, b.topk_w, stream)
+        self.permute(x, b, step.topk_ids, stream)
+        sh = self.shared or {}
+        L.moe_grouped_gemm(b.x_perm, self.w13, sh.get("w13"), dt, b.offsets, self.n_groups, cap, 2 * self.I, self.H,
+                           step.gu, dt, False, stream)
+        L.moe_swiglu(step.gu, dt, self._n_rows(b), cap, self.I, dropout, rng, step.a, stream)
+        L.moe_grouped_gemm(step.a, self.w2, sh.get("w2"), dt, b.offsets, self.n_groups, cap, self.H, self.I, b.y_perm,
+                           dt, False, stream)
+        self.combine(b, step.topk_w, stream)
+        if residual is not None or out_dropout:
+            L.moe_dropout(b.out, residual, dt, b.out.numel(), out_dropout, None if rng is None else rng[1], b.out,
+                          stream)
+        return step
+
+    def _n_rows(self, b: LayerBuffers):
+        return b.offsets[self.n_groups:]  # rows in use
+
+    def _train_step(self, x, topk_ids, topk_w, dropout, out_dropout, rng) -> TrainStep:
+        T, dev = x.shape[0], x.device
+        b = self.buffers(T, dev, ("train", T))
+        key = ("train buffers", T)
+        if key not in self._bufs:
+            cap = T * self.k + T
+            self._bufs[key] = dict(gu=torch.empty((cap, 2 * self.I), dtype=x.dtype, device=dev),
+                                   a=torch.empty((cap, self.I), dtype=x.dtype, device=dev),
+                                   dx=torch.empty_like(x), dtopk_w=torch.empty_like(b.topk_w))
+            self._bufs[("serial", T)] = 0
+        self._bufs[("serial", T)] += 1
+        here = topk_ids is None
+        return TrainStep(x=x, b=b, **self._bufs[key], topk_ids=b.topk_ids if here else topk_ids,
+                         topk_w=b.topk_w if here else topk_w,
+                         routed_here=here and self.router["w"].shape[0] == self.E_local, dropout=dropout,
+                         out_dropout=out_dropout, rng=rng, serial=self._bufs[("serial", T)])
+
+    def new_grads(self) -> LayerGrads:
+        """Zeroed weight gradients, to pass to backward."""
+        def zeros(t):
+            return None if t is None else torch.zeros(t.shape, dtype=torch.float32, device=t.device)
+        sh, r = self.shared or {}, self.router or {}
+        return LayerGrads(zeros(self.w13), zeros(self.w2), zeros(sh.get("w13")), zeros(sh.get("w2")), zeros(r.get("w")),
+                          zeros(r.get("bias")))
+
+    def backward(self, step: TrainStep, dout: torch.Tensor, grads: Optional[LayerGrads] = None,
+                 accumulate: bool = False, stream=None) -> LayerGrads:
+        """Gradients of a step from its output's gradient dout [T, H] (the
+        residual's is dout itself). The weights' go to `grads` (new_grads()
+        unless given), added to what is there with accumulate; dx and topk_w are
+        the layer's buffers. Where the step was routed by this layer's router
+        over experts that are all here, the gate's part is in dx and in router_w
+        and router_bias. Otherwise grads.topk_w is what its weights got here:
+        with routing handed in, the caller's to carry on; on an expert share,
+        summed over the GPUs that share the experts and given to gate_backward
+        (dx is then this share's part of a sum as well). A step's buffers hold its
+        gradients afterwards: one backward per step."""
+        T, b, dt, H, I = step.x.shape[0], step.b, self.act_dt, self.H, self.I
+        if step.serial != self._bufs[("serial", T)] or step.b is not self._bufs[("train", T)]:
+            raise RuntimeError("the step's buffers hold a later step or its gradients")
+        L.expect(dout, "dout", (step.x.dtype,), step.x.device)
+        if dout.shape != step.x.shape:
+            raise ValueError(f"dout: shape {tuple(dout.shape)}, expected {tuple(step.x.shape)}")
+        if grads is None:
+            if accumulate:
+                raise ValueError("accumulate needs the gradients to add to")
+            grads = self.new_grads()
+        self._bufs[("serial", T)] += 1
+        sh, cap, n = self.shared or {}, T * self.k + T, self.n_groups
+        if step.out_dropout:
+            L.moe_dropout(dout, None, dt, dout.numel(), step.out_dropout, step.rng[1], step.dx, stream)
+            dout = step.dx
+        dy = b.y_perm
+        L.moe_combine_grad(dout, b.y_perm, dt, b.slot_to_row, step.topk_w, T, self.k, H, b.offsets,
+                           self.E_local if self.shared is not None else -1, dy, step.dtopk_w, stream)
+        # a's buffer takes its gradient, and a again from gu, whose buffer takes its own
+        L.moe_grouped_gemm_dx(dy, self.w2, sh.get("w2"), dt, b.offsets, n, cap, H, I, step.a, dt, False, stream)
+        L.moe_swiglu_grad(step.gu, step.a, dt, self._n_rows(b), cap, I, step.dropout, step.rng, step.gu, step.a, stream)
+        L.moe_grouped_gemm_dw(dy, step.a, dt, b.offsets, n, cap, H, I, grads.w2, grads.shared_w2, L.F32, accumulate,
+                              stream)
+        L.moe_grouped_gemm_dw(step.gu, b.x_perm, dt, b.offsets, n, cap, 2 * I, H, grads.w13, grads.shared_w13, L.F32,
+                              accumulate, stream)
+        L.moe_grouped_gemm_dx(step.gu, self.w13, sh.get("w13"), dt, b.offsets, n, cap, 2 * I, H, dy, dt, False, stream)
+        # the rows are copies of their tokens' x: the copies' gradients summed
+        L.moe_combine(dy, dt, b.slot_to_row, self._ones(T, self.k, torch.float32), T, self.k, H, b.offsets,
+                      self.E_local if self.shared is not None else -1, step.dx, dt, stream)
+        grads.dx, grads.topk_w = step.dx, step.dtopk_w
+        if step.routed_here:
+            self.gate_backward(step, step.dtopk_w, grads, accumulate, stream)
+        return grads
+
+    def gate_backward(self, step: TrainStep, dtopk_w: torch.Tensor, grads: LayerGrads, accumulate: bool = False,
+                      stream=None):
+        """The gate's part of a step's gradients from those of its picks'
+        weights [T, k]: added to grads.dx, and router_w and router_bias. backward
+        calls it unless the experts are shared with other GPUs; there it belongs
+        into the sum of their dx once."""
+        r, T, dt, H = self.router, step.x.shape[0], self.act_dt, self.H
+        if r is None or step.topk_ids is not step.b.topk_ids:
+            raise ValueError("the step was not routed by this layer's router")
+        L.expect(dtopk_w, "dtopk_w", (torch.float32,), step.x.device)
+        if tuple(dtopk_w.shape) != (T, self.k):
+            raise ValueError(f"dtopk_w: shape {tuple(dtopk_w.shape)}, expected [{T}, {self.k}]")
+        E, key = r["w"].shape[0], ("gate", T)
+        if key not in self._bufs:
+            dev = step.x.device
+            self._bufs[key] = (torch.empty((T, E), dtype=step.x.dtype, device=dev),
+                               torch.tensor([0, T], dtype=torch.int32, device=dev),
+                               torch.zeros((E, 8), dtype=torch.float32, device=dev))
+        dlogits, offsets, dbias = self._bufs[key]
+        L.moe_route_grad(step.b.logits, step.topk_ids, dtopk_w, T, E, self.k, r["scoring"], r.get("renormalize", True),
+                         dlogits, dt, stream)
+        L.moe_grouped_gemm_dx(dlogits, r["w"], None, dt, offsets, 1, T, E, H, grads.dx, dt, True, stream)
+        L.moe_grouped_gemm_dw(dlogits, step.x, dt, offsets, 1, T, E, H, grads.router_w, None, L.F32, accumulate, stream)
+        if grads.router_bias is not None:  # column sums: a product with columns of ones
+            L.moe_grouped_gemm_dw(dlogits, self._ones(T, 8, step.x.dtype), dt, offsets, 1, T, E, 8, dbias, None, L.F32,
+                                  False, stream)
+            with self._on(stream):
+                (grads.router_bias.add_ if accumulate else grads.router_bias.copy_)(dbias[:, 0])
+
+    @staticmethod
+    def _on(stream):
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(L.stream_of(stream))
+
+    def _ones(self, rows: int, cols: int, dtype) -> torch.Tensor:
+        key = ("ones", rows, cols, dtype)
+        if key not in self._bufs:
+            self._bufs[key] = torch.ones((rows, cols), dtype=dtype, device=self.w13.device)
+        return self._bufs[key]
+
 
 def quantize_mxfp4(x: torch.Tensor, stream=None):
     """(codes [..., K/2], scale bytes [..., K/32]) of a bf16 or fp32 tensor
@@ -359,7 +565,7 @@ def quantize_mxfp4(x: torch.Tensor, stream=None):
     K = x.shape[-1] if x.dim() else 0
     if K == 0 or K % 32:
         raise ValueError(f"x: last dimension of shape {tuple(x.shape)} is not a multiple of 32 (32 or more)")
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(L.stream_of(stream)):
+    with MoELayer._on(stream):
         codes = torch.empty(x.shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device)
         scales = torch.empty(x.shape[:-1] + (K // 32,), dtype=torch.uint8, device=x.device)
     L.moe_quantize_mxfp4(x, L.dtype_code(x), x.numel() // K, K, codes, scales, stream)
