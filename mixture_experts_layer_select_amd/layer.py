@@ -416,7 +416,8 @@ class MoELayer:
         [2, 2] on the device, seed and offset of the experts' dropout and of the
         output's, read when the calls run and again by backward, so it changes
         only after backward. x is read again by backward. One step per number of
-        tokens: the next forward_train of as many tokens takes its buffers."""
+        tokens: the next forward_train of as many tokens takes its buffers. The
+        first of a size makes them and waits for the device; it is not captured."""
         self._check_train()
         self.check_inputs(x, topk_ids, topk_w)
         self._check_rng(rng, dropout, out_dropout)
@@ -447,14 +448,24 @@ class MoELayer:
 
     def _train_step(self, x, topk_ids, topk_w, dropout, out_dropout, rng) -> TrainStep:
         T, dev = x.shape[0], x.device
-        b = self.buffers(T, dev, ("train", T))
         key = ("train buffers", T)
         if key not in self._bufs:
-            cap = T * self.k + T
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"the first forward_train of {T} tokens makes the layer's buffers: run it once before "
+                                   "the capture")
+            b, cap = self.buffers(T, dev, ("train", T)), T * self.k + T
             self._bufs[key] = dict(gu=torch.empty((cap, 2 * self.I), dtype=x.dtype, device=dev),
                                    a=torch.empty((cap, self.I), dtype=x.dtype, device=dev),
                                    dx=torch.empty_like(x), dtopk_w=torch.empty_like(b.topk_w))
+            # constants: one for each pick and, for column sums, eight for each token; the gate's one group and its buffers
+            E = self.router["w"].shape[0] if self.router is not None else 0
+            self._bufs[("constants", T)] = (
+                torch.ones((T, self.k), dtype=torch.float32, device=dev), torch.ones((T, 8), dtype=x.dtype, device=dev),
+                torch.tensor([0, T], dtype=torch.int32, device=dev), torch.empty((T, E), dtype=x.dtype, device=dev),
+                torch.empty((E, 8), dtype=torch.float32, device=dev))
             self._bufs[("serial", T)] = 0
+            torch.cuda.current_stream().synchronize()  # the constants are there for every stream
+        b = self._bufs[("train", T)]
         self._bufs[("serial", T)] += 1
         here = topk_ids is None
         return TrainStep(x=x, b=b, **self._bufs[key], topk_ids=b.topk_ids if here else topk_ids,
@@ -509,7 +520,7 @@ class MoELayer:
                               accumulate, stream)
         L.moe_grouped_gemm_dx(step.gu, self.w13, sh.get("w13"), dt, b.offsets, n, cap, 2 * I, H, dy, dt, False, stream)
         # the rows are copies of their tokens' x: the copies' gradients summed
-        L.moe_combine(dy, dt, b.slot_to_row, self._ones(T, self.k, torch.float32), T, self.k, H, b.offsets,
+        L.moe_combine(dy, dt, b.slot_to_row, self._bufs[("constants", T)][0], T, self.k, H, b.offsets,
                       self.E_local if self.shared is not None else -1, step.dx, dt, stream)
         grads.dx, grads.topk_w = step.dx, step.dtopk_w
         if step.routed_here:
@@ -528,19 +539,14 @@ class MoELayer:
         L.expect(dtopk_w, "dtopk_w", (torch.float32,), step.x.device)
         if tuple(dtopk_w.shape) != (T, self.k):
             raise ValueError(f"dtopk_w: shape {tuple(dtopk_w.shape)}, expected [{T}, {self.k}]")
-        E, key = r["w"].shape[0], ("gate", T)
-        if key not in self._bufs:
-            dev = step.x.device
-            self._bufs[key] = (torch.empty((T, E), dtype=step.x.dtype, device=dev),
-                               torch.tensor([0, T], dtype=torch.int32, device=dev),
-                               torch.zeros((E, 8), dtype=torch.float32, device=dev))
-        dlogits, offsets, dbias = self._bufs[key]
+        E = r["w"].shape[0]
+        _, ones, offsets, dlogits, dbias = self._bufs[("constants", T)]
         L.moe_route_grad(step.b.logits, step.topk_ids, dtopk_w, T, E, self.k, r["scoring"], r.get("renormalize", True),
                          dlogits, dt, stream)
         L.moe_grouped_gemm_dx(dlogits, r["w"], None, dt, offsets, 1, T, E, H, grads.dx, dt, True, stream)
         L.moe_grouped_gemm_dw(dlogits, step.x, dt, offsets, 1, T, E, H, grads.router_w, None, L.F32, accumulate, stream)
         if grads.router_bias is not None:  # column sums: a product with columns of ones
-            L.moe_grouped_gemm_dw(dlogits, self._ones(T, 8, step.x.dtype), dt, offsets, 1, T, E, 8, dbias, None, L.F32,
+            L.moe_grouped_gemm_dw(dlogits, ones, dt, offsets, 1, T, E, 8, dbias, None, L.F32,
                                   False, stream)
             with self._on(stream):
                 (grads.router_bias.add_ if accumulate else grads.router_bias.copy_)(dbias[:, 0])
@@ -548,12 +554,6 @@ class MoELayer:
     @staticmethod
     def _on(stream):
         return contextlib.nullcontext() if stream is None else torch.cuda.stream(L.stream_of(stream))
-
-    def _ones(self, rows: int, cols: int, dtype) -> torch.Tensor:
-        key = ("ones", rows, cols, dtype)
-        if key not in self._bufs:
-            self._bufs[key] = torch.ones((rows, cols), dtype=dtype, device=self.w13.device)
-        return self._bufs[key]
 
 
 def quantize_mxfp4(x: torch.Tensor, stream=None):

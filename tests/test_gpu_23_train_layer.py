@@ -245,6 +245,29 @@ def test_stream(L):
         assert torch.equal(a, b)
 
 
+def test_other_stream_first(L):
+    """A layer whose first step runs on a stream of its own, and a capture without a step before it."""
+    layer, _ = make(L, "bf16", 8, 64, 32, 2)
+    again, _ = make(L, "bf16", 8, 64, 32, 2)
+    x = torch.randn((12, 64), device=DEV).to(BF)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        grads = layer.new_grads()
+    got = layer.backward(layer.forward_train(x, stream=s), x, grads, stream=s)
+    s.synchronize()
+    want = again.backward(again.forward_train(x), x)
+    for n in ("dx", "w13", "router_w", "router_bias"):
+        assert torch.equal(getattr(got, n), getattr(want, n)), n
+    third, _ = make(L, "bf16", 8, 64, 32, 2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(graph):
+            third.forward_train(x)
+    torch.cuda.synchronize()
+
+
 def test_no_tokens(L):
     layer, _ = make(L, "bf16", 8, 64, 32, 2)
     x = torch.empty((0, 64), device=DEV, dtype=BF)

@@ -127,3 +127,23 @@ def test_host_tensors_and_views_are_refused(L):
     t = torch.zeros(8, 8)
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         L.moe_dropout(t, None, L.F32, 64, 0.0, None, t, 0)
+
+
+def test_layer_refusals(L):
+    """Formats and sizes that forward_train does not take, found before the device is touched."""
+    def layer(fmt, E=8, H=64, I=32, router=8):
+        dt = dict(bf16=torch.bfloat16, f32=torch.float32, fp8=torch.uint8)[fmt]
+        kw = dict(w13_scale=torch.ones(E, 1, 1), w2_scale=torch.ones(E, 1, 1)) if fmt == "fp8" else {}
+        return L.MoELayer(fmt, H, I, 2, torch.zeros(E, 2 * I, H, dtype=dt), torch.zeros(E, H, I, dtype=dt),
+                          router=dict(w=torch.zeros(router, H, dtype=dt), bias=None, scoring=L.SIGMOID), **kw)
+    for args, err in (((dict(fmt="fp8", H=256, I=128)), "f32 or bf16"), (dict(fmt="bf16", E=9, router=9), "multiple of 8"),
+                      (dict(fmt="bf16", I=36), "multiple of 8"), (dict(fmt="f32", H=66), "multiple of 4")):
+        with pytest.raises(ValueError, match=err):
+            layer(**args).forward_train(torch.zeros(3, args.get("H", 64), dtype=torch.bfloat16))
+    ok = layer("bf16")
+    with pytest.raises(TypeError):
+        ok.forward_train(torch.zeros(3, 64))
+    with pytest.raises(ValueError, match="needs rng"):
+        ok.forward_train(torch.zeros(3, 64, dtype=torch.bfloat16), dropout=0.5)
+    g = ok.new_grads()
+    assert g.w13.shape == ok.w13.shape and g.w13.dtype == torch.float32 and g.router_bias is None and g.shared_w13 is None
