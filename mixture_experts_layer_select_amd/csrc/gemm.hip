@@ -262,14 +262,17 @@ struct RowsPlan {
     int tiles[4], width[4];
 };
 
-// All threads call; returns the number of tiles, and the column blocks' width. Of the heights 64 to 256 and the widths
-// 64 to 256 (multiples of kUnit) it takes the pair with the shortest estimate: the rounds of items that a workgroup
-// walks times a step's time. A step of a tile of h x w columns (NX = ceil(h / 64), mt tiles of a group sharing the
-// weights) measured about 0.35 + 0.2 NX + (0.4 + 0.65 / mt) w / 256 us at up to 256 columns, the products' term
-// halved up to 128 columns (four waves of eight have work); an item's start and end cost about three steps.
+// All threads call; returns the number of tiles, their height and the column blocks' width. Of the heights 64 to 256 and
+// the widths 64 to 256 (multiples of kUnit) it takes the pair with the shortest estimate: the rounds of items that a
+// workgroup walks times a step's time times the steps, of which an item's start and end are worth about three. A step
+// of a tile of h x w columns (NX = ceil(h / 64), mt tiles of a group sharing the weights) measured about
+// 0.35 + 0.2 NX + (0.4 + 0.65 / mt) w / 256 us where all CUs load at once; the products' term is half up to 128
+// columns (four waves of eight have work), the loads' term goes with the CUs in use. Tiles of 64 x 64 split
+// their contraction over the waves: a quarter of the steps, with the loads of a whole tile.
 template <int kUnit>
 __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restrict__ offsets, int n_groups,
-                                         int max_rows, int cols, int nk, int& width) {
+                                         int max_rows, int cols, int nk, int& width,
+                                         int& height) {
     for (int g = threadIdx.x; g <= n_groups; g += kBigThreads) plan.t.row0[g] = clamp_row(offsets[g], max_rows);
     __syncthreads();
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -296,9 +299,12 @@ __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restri
         if (w >= 64 && tiles) {
             const int items = tiles * ((cols + w - 1) / w), per = gridDim.x >> 3;
             const int rounds = ((items + 7) / 8 + per - 1) / per;
-            const float part = (float)w / kBig, each = 1.0f / (float)tiles;
-            const float step = 0.35f + 0.2f * nx * each * (w <= 128 ? 0.5f : 1.0f) + (0.4f + 0.65f * share * each) * part;
-            cost = (float)rounds * step * (float)(nk + 3);
+            const bool split = h == 64 && w == 64;
+            const float part = split ? 1.0f : (float)w / kBig, each = 1.0f / (float)tiles;
+            const float busy = fminf(1.0f, (float)items / (float)gridDim.x);
+            const float step = 0.35f + 0.2f * nx * each * (w <= 128 ? 0.5f : 1.0f) +
+                               busy * (0.4f + 0.65f * share * each + (split ? 0.3f : 0.f)) * part;
+            cost = (float)rounds * step * (float)(split ? (nk + 3) / 4 + 4 : nk + 3);
         }
         float best = cost;
 #pragma unroll
@@ -316,8 +322,9 @@ __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restri
     for (int i = 2; i >= 0; --i)
         if (plan.cost[i] < plan.cost[pick]) pick = i;
     width = plan.width[pick];
+    height = 64 * (pick + 1);
     const int n = plan.tiles[pick];
-    number_tiles(plan.t, n_groups, 64 * (pick + 1));
+    number_tiles(plan.t, n_groups, height);
     __syncthreads();
     return n;
 }
@@ -341,10 +348,11 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
     const int nk = (n_k + kStepK - 1) / kStepK;
     const size_t w_size = (size_t)a.N * a.K;
     const bool apart = a.p_last != nullptr;
-    int width;
+    int width, n_height;
     const int n_tiles = __builtin_amdgcn_readfirstlane(
-        plan_rows<kPc ? 16 : 64>(plan, a.offsets, a.n_groups, a.max_rows, cols, nk, width));
+        plan_rows<kPc ? 16 : 64>(plan, a.offsets, a.n_groups, a.max_rows, cols, nk, width, n_height));
     width = __builtin_amdgcn_readfirstlane(width);
+    n_height = __builtin_amdgcn_readfirstlane(n_height);
     const int NB = (cols + width - 1) / width;
     const int n_items = n_tiles * NB;
     const int xcd = blockIdx.x & 7;
@@ -371,12 +379,8 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
     // 128 bytes, or 16 i + 2 wave + [0, 2) of 512. Its 16-byte chunk of the row, by the swizzle:
     const int rc = 8 * wave + (lane >> 3), rs = 2 * wave + (lane >> 5);
     const int cp = kPc ? (lane & 7) ^ swz_p<TO>(rc) : (lane & 31) ^ (swz_k(rs) << 2), cq = (lane & 7) ^ swz_q(rc);
-    uint32_t vp[4], vq[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        vp[i] = ((uint32_t)(kPc ? 64 * i + rc : 16 * i + rs) * a.K + 8 * cp) * 2;
-        vq[i] = ((uint32_t)(64 * i + rc) * n_k + 8 * cq) * 2;
-    }
+    const uint32_t vp = ((uint32_t)(kPc ? rc : rs) * a.K + 8 * cp) * 2, vq = ((uint32_t)rc * n_k + 8 * cq) * 2;
+    const uint32_t next_p = (kPc ? 128u : 32u) * a.K, next_q = 128u * n_k;  // bytes from one piece to the next
 
     // An item by numbers alone; the addresses are made anew from them, as scalars, where they are used (carried
     // through the item loop they would be kept in vector registers, and every load would loop over its lanes).
@@ -417,15 +421,15 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
         const uint32_t so = (uint32_t)min(kc, nk - 1) * (kStepK * 2);  // never past the first row's end
         const int left = n_k - kc * kStepK;                            // of the contraction
         if constexpr (n >= 4) {
-            lds_buf16(buffer_rsrc(c.q, (uint32_t)c.rows * n_k * 2), vq[i] + (8 * cq < left ? 0u : kPast), so,
+            lds_buf16(buffer_rsrc(c.q, (uint32_t)c.rows * n_k * 2), vq + i * next_q + (8 * cq < left ? 0u : kPast), so,
                       Q + (8 * i + wave) * 1024);
         } else if constexpr (kPc) {
-            lds_buf16(buffer_rsrc(c.p, (uint32_t)c.cols * a.K * 2), vp[i] + (8 * cp < left ? 0u : kPast), so,
+            lds_buf16(buffer_rsrc(c.p, (uint32_t)c.cols * a.K * 2), vp + i * next_p + (8 * cp < left ? 0u : kPast), so,
                       P + (8 * i + wave) * 1024);
         } else {
             const int rows = max(0, min(kStepK, left));
             lds_buf16(buffer_rsrc(c.p + (size_t)kc * kStepK * a.K, rows ? (uint32_t)(rows * a.K - c.c0) * 2 : 0u),
-                      vp[i] + (8 * cp < c.cols ? 0u : kPast), 0, P + (8 * i + wave) * 1024);
+                      vp + i * next_p + (8 * cp < c.cols ? 0u : kPast), 0, P + (8 * i + wave) * 1024);
         }
     };
     auto load_p = [&](const Tile& c, int kc, uint8_t* P) MX_INLINE {
@@ -465,6 +469,95 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_rows_kernel(GemmArgs a) {
 
     int item = i_lo + (int)(blockIdx.x >> 3);
     if (item >= i_hi) return;
+
+    // Tiles of 64 x 64, for calls of few tiles, which are as long as their chain of steps: the contraction is split over
+    // the four waves of a row half. A step takes 256 of it; the 64 of P's rows (columns, K-strided) that another wave
+    // would compute hold the next 64 of the contraction instead, and Q's likewise. (203 rows of 9 groups, 768 x 1280,
+    // forward: 13.0 -> 11.1 us; one row of each of 33 groups, 128 x 4096: 26 -> 17.)
+    if (width == 64 && n_height == 64) {
+        constexpr int kLong = 4 * kStepK;
+        const int nl = (n_k + kLong - 1) / kLong;
+        for (; item < i_hi; item += per_xcd) {
+            const Tile cur = tile_of(find(item));
+            auto load = [&](int kc, uint8_t* P, uint8_t* Q) MX_INLINE {
+                const int left = n_k - kc * kLong;
+                const uint32_t so = (uint32_t)min(kc, nl - 1) * (kLong * 2);
+                const __amdgpu_buffer_rsrc_t dq = buffer_rsrc(cur.q, (uint32_t)cur.rows * n_k * 2);
+                const int rows = max(0, min(kLong, left));
+                const __amdgpu_buffer_rsrc_t dp =
+                    kPc ? buffer_rsrc(cur.p, (uint32_t)cur.cols * a.K * 2)
+                        : buffer_rsrc(cur.p + (size_t)kc * kLong * a.K, rows ? (uint32_t)(rows * a.K - cur.c0) * 2 : 0u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t v =
+                        kPc ? ((uint32_t)rc * a.K + 64 * i + 8 * cp) * 2 + (64 * i + 8 * cp < left ? 0u : kPast)
+                            : ((uint32_t)(64 * (cp >> 3) + 16 * i + rs) * a.K + 8 * (cp & 7)) * 2 +
+                                  (8 * (cp & 7) < cur.cols ? 0u : kPast);
+                    lds_buf16(dp, v, kPc ? so : 0, P + (8 * i + wave) * 1024);
+                    lds_buf16(dq, ((uint32_t)rc * n_k + 64 * i + 8 * cq) * 2 + (64 * i + 8 * cq < left ? 0u : kPast), so,
+                              Q + (8 * i + wave) * 1024);
+                }
+                asm volatile("" ::: "memory");  // in this order: the waits count the loads
+            };
+            f32x16 acc[2] = {};
+            auto multiply = [&](const uint8_t* P, const uint8_t* Q) MX_INLINE {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const u32x4 q = *reinterpret_cast<const u32x4*>(Q + wn * 8192 + offq[h]);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        u32x4 x;
+                        if constexpr (kPc) x = *reinterpret_cast<const u32x4*>(P + s * 4096 + offp[h]);
+                        else x = lds_read_tr(P + offp[s] + h * 8192);
+                        acc[s] = mfma32(x, q, acc[s]);
+                    }
+                }
+            };
+            load(0, p0, q0);
+            load(1, p1, q1);
+            auto step = [&](int kc, uint8_t* P, uint8_t* Q) MX_INLINE {
+                wait_vmcnt<8>();  // this step has landed, the next one flies
+                mx_barrier();
+                multiply(P, Q);
+                mx_barrier();  // no wave reads it any more
+                load(kc + 2, P, Q);
+            };
+            for (int kc = 0; kc < nl; kc += 2) {  // a step past the end multiplies zeros
+                step(kc, p0, q0);
+                step(kc + 1, p1, q1);
+            }
+            wait_vmcnt<0>();
+            mx_barrier();
+            // the sums of the four waves, in their order; a register of all lanes is a row of 256 bytes
+            float* red = reinterpret_cast<float*>(wave < 4 ? p0 : p1) + (wave & 3) * 2048;
+            if (wn > 0) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) red[(16 * s + r) * 64 + lane] = acc[s][r];
+            }
+            mx_barrier();
+            if (wn == 0) {
+#pragma unroll
+                for (int n = 1; n < 4; ++n) {
+                    const int from = 2 * n + wm;
+                    const float* other = reinterpret_cast<const float*>(from < 4 ? p0 : p1) + (from & 3) * 2048;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[s][r] += other[(16 * s + r) * 64 + lane];
+                }
+                const int m = 32 * wm + l31;
+                if (m < cur.rows) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        put16(cur.out + (size_t)m * cols + cur.c0, 32 * s, cur.cols, hi, acc[s], a.accumulate != 0);
+                }
+            }
+            mx_barrier();  // the sums are read before the next item's loads
+        }
+        return;
+    }
     Item at = find(item);
     first_loads(tile_of(at));
     for (;;) {
