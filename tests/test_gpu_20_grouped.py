@@ -255,3 +255,65 @@ def test_streams_graph_and_repeats(L):
             factor = 2.0 ** (i + 1) if f != "weights" else 4.0 ** (i + 1)
             n = len(counts) if f == "weights" else sum(counts)
             assert torch.equal(gout[f][:n].float(), eager[f][:n].float() * factor)
+
+
+@pytest.mark.parametrize("out_dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("form", ["forward", "input"])
+def test_few_tiles_long_contraction(L, form, accumulate, out_dt):
+    """Calls of few tiles split their contraction over waves: lengths around the long steps, several items a workgroup."""
+    for counts, out_cols, length in (([3, 0, 9], 64, 4096), ([64, 1], 200, 264), ([17], 72, 256), ([30, 40], 136, 1032),
+                                     ([2] * 40, 128, 2056), ([5, 60, 33], 64, 8)):
+        N, K = (out_cols, length) if form == "forward" else (length, out_cols)
+        x, dy, w, off = make(counts, N, K, BF)
+        out = empty_out(form, counts, N, K, out_dt, x.shape[0])
+        before = out.clone()
+        call(L, form, x, dy, w, off, N, K, out, accumulate=accumulate)
+        ref, mag = reference(form, x, dy, w, off)
+        R = sum(counts)
+        if accumulate:
+            ref, mag = ref + 37, mag + 37
+        check(out[:R], ref, mag, length)
+        assert torch.equal(out[R:], before[R:])
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_sizes(L, seed):
+    """Sizes over the whole range of tile heights and widths, rows from one to several tiles a group, each form in turn."""
+    import random
+    rng = random.Random(seed)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    form, f32 = FORMS[seed % 3], seed % 8 == 7
+    unit = 4 if f32 else 8
+    N, K = unit * log(2, 500), unit * log(2, 500)
+    n = rng.randint(1, 40)
+    mean = log(1, 600)
+    counts = [rng.choice((0, 1, rng.randint(0, mean), rng.randint(0, 2 * mean))) for _ in range(n)]
+    while sum(counts) * N * K > 2e11:
+        counts = [c // 2 for c in counts]
+    dt = F32 if f32 else BF
+    out_dt = F32 if f32 else rng.choice((BF, F32))
+    x, dy, w, off = make(counts, N, K, dt, seed=seed)
+    out = empty_out(form, counts, N, K, out_dt, x.shape[0])
+    call(L, form, x, dy, w, off, N, K, out)
+    ref, mag = reference(form, x, dy, w, off)
+    R = sum(counts)
+    check(out if form == "weights" else out[:R], ref, mag, contraction(form, N, K, off))
+    if form != "weights":
+        assert (out[R:] == 37).all()
+
+
+@pytest.mark.parametrize("form,counts,N,K", [
+    ("forward", [300] * 20, 1024, 192), ("forward", [120] * 40, 4096, 72), ("forward", [180] * 24, 2048, 136),
+    ("forward", [40] * 33, 4096, 320), ("input", [300] * 20, 192, 1024), ("input", [120] * 40, 72, 4096),
+    ("input", [180] * 24, 136, 2048), ("input", [40] * 33, 320, 4096), ("weights", [40] * 9, 1000, 904),
+    ("weights", [100, 0, 31, 33, 64, 1, 129, 2, 511], 520, 776)])
+def test_several_items_a_workgroup(L, form, counts, N, K):
+    """More items than CUs: each height and width, loads of the next item under the stores of the last."""
+    for out_dt in (BF, F32):
+        x, dy, w, off = make(counts, N, K, BF)
+        out = empty_out(form, counts, N, K, out_dt, x.shape[0])
+        call(L, form, x, dy, w, off, N, K, out)
+        ref, mag = reference(form, x, dy, w, off)
+        R = sum(counts)
+        check(out if form == "weights" else out[:R], ref, mag, contraction(form, N, K, off))
