@@ -415,6 +415,9 @@ Dropout dropout_of(float p, const void* rng) {
     return Dropout{(const uint64_t*)rng, t, 65536.0f / (float)(65536u - t)};
 }
 
+// tokens of one launch, at most: a grid of 2^32 work items and more runs short without an error
+constexpr int kTokens = 1 << 21;
+
 int blocks_for(long threads) {
     return (int)std::max(1L, std::min((threads + 255) / 256, (long)device_info().cu_count * 16));
 }
@@ -463,9 +466,9 @@ moe_status launch_combine_grad(const void* dout, const void* y, moe_dtype dt, co
                                const float* topk_w, int T, int k, int H, const int32_t* offsets, int shared_group,
                                void* dy, float* dw, hipStream_t st) {
     const bool vec = H % 8 == 0 && aligned16(dout) && aligned16(y) && aligned16(dy);
-    constexpr int kMaxTokens = 1 << 21;  // of one launch: a grid of 2^32 work items and more runs short
-    for (int t0 = 0; t0 < T; t0 += kMaxTokens) {
-        const int n = std::min(T - t0, kMaxTokens);
+    const int most = kTokens / ((k + kPicks - 1) / kPicks);
+    for (int t0 = 0; t0 < T;) {
+        const int n = std::min(T - t0, most);
         // picks are spread over workgroups until there are about four of these per CU
         const int per = std::max(1, (int)std::min((long)std::min(k, kPicks), (long)n * k / 1024));
         const CombineGrad p{dout, y, slot_to_row, topk_w, t0, T, k, H, offsets, shared_group, per, dy, dw};
@@ -487,12 +490,21 @@ moe_status launch_combine_grad(const void* dout, const void* y, moe_dtype dt, co
         }
 #undef CGRAD_OF
 #undef CGRAD
+        t0 += n;
     }
     return check_launch("combine_grad_kernel");
 }
 
 moe_status launch_route_grad(const float* logits, const int32_t* ids, const float* dtopk_w, int T, int E, int k,
                              int scoring, int renorm, void* dlogits, moe_dtype out_dt, hipStream_t st) {
+    for (; T > kTokens; T -= kTokens) {
+        const moe_status s = launch_route_grad(logits, ids, dtopk_w, kTokens, E, k, scoring, renorm, dlogits, out_dt, st);
+        if (s != MOE_OK) return s;
+        logits += (size_t)kTokens * E;
+        ids += (size_t)kTokens * k;
+        dtopk_w += (size_t)kTokens * k;
+        dlogits = (uint8_t*)dlogits + (size_t)kTokens * E * (out_dt == MOE_BF16 ? 2 : 4);
+    }
     if (k <= 8 && (scoring == MOE_SIGMOID || renorm)) {
         const dim3 few((T + 31) / 32);
         const bool vec = E % 4 == 0 && aligned16(dlogits);

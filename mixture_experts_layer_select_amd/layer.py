@@ -481,6 +481,17 @@ class MoELayer:
         return LayerGrads(zeros(self.w13), zeros(self.w2), zeros(sh.get("w13")), zeros(sh.get("w2")), zeros(r.get("w")),
                           zeros(r.get("bias")))
 
+    def _check_grads(self, grads: LayerGrads):
+        sh, r = self.shared or {}, self.router or {}
+        for name, like in (("w13", self.w13), ("w2", self.w2), ("shared_w13", sh.get("w13")),
+                           ("shared_w2", sh.get("w2")), ("router_w", r.get("w")), ("router_bias", r.get("bias"))):
+            t = getattr(grads, name)
+            if like is None:
+                continue
+            if t is None or t.shape != like.shape:
+                raise ValueError(f"grads.{name}: {'missing' if t is None else tuple(t.shape)}, expected {tuple(like.shape)}")
+            L.expect(t, f"grads.{name}", (torch.float32,), like.device)
+
     def backward(self, step: TrainStep, dout: torch.Tensor, grads: Optional[LayerGrads] = None,
                  accumulate: bool = False, stream=None) -> LayerGrads:
         """Gradients of a step from its output's gradient dout [T, H] (the
@@ -494,7 +505,7 @@ class MoELayer:
         (dx is then this share's part of a sum as well). A step's buffers hold its
         gradients afterwards: one backward per step."""
         T, b, dt, H, I = step.x.shape[0], step.b, self.act_dt, self.H, self.I
-        if step.serial != self._bufs[("serial", T)] or step.b is not self._bufs[("train", T)]:
+        if step.serial != self._bufs.get(("serial", T)) or step.b is not self._bufs.get(("train", T)):
             raise RuntimeError("the step's buffers hold a later step or its gradients")
         L.expect(dout, "dout", (step.x.dtype,), step.x.device)
         if dout.shape != step.x.shape:
@@ -503,6 +514,7 @@ class MoELayer:
             if accumulate:
                 raise ValueError("accumulate needs the gradients to add to")
             grads = self.new_grads()
+        self._check_grads(grads)
         self._bufs[("serial", T)] += 1
         sh, cap, n = self.shared or {}, T * self.k + T, self.n_groups
         if step.out_dropout:
@@ -539,6 +551,9 @@ class MoELayer:
         L.expect(dtopk_w, "dtopk_w", (torch.float32,), step.x.device)
         if tuple(dtopk_w.shape) != (T, self.k):
             raise ValueError(f"dtopk_w: shape {tuple(dtopk_w.shape)}, expected [{T}, {self.k}]")
+        self._check_grads(grads)
+        if grads.dx is None or grads.dx.shape != step.x.shape:
+            raise ValueError("grads.dx: backward's, of this step, is needed")
         E = r["w"].shape[0]
         _, ones, offsets, dlogits, dbias = self._bufs[("constants", T)]
         L.moe_route_grad(step.b.logits, step.topk_ids, dtopk_w, T, E, self.k, r["scoring"], r.get("renormalize", True),

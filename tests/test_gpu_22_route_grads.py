@@ -183,3 +183,37 @@ def test_route_grad_against_differences(L):
                 want = (d.double() * v.double()).sum()
                 size = float(dw.abs().sum())
                 assert abs(float(slope - want)) <= size * (h * h / 6 * 8 * float(v.abs().max()) ** 3 + 2.0 ** -21 / h)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_grad_many_tokens(L, sigmoid):
+    """More tokens than one grid of work items holds (2^26 of one wave each): the last ones, and some before."""
+    T, E, k = 2 ** 26 + 5, 4, 1
+    logits = torch.randn((T, E), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    ids = torch.randint(0, E, (T, k), device=DEV, dtype=torch.int32, generator=torch.Generator(device=DEV).manual_seed(2))
+    dw = torch.randn((T, k), device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))
+    out = torch.full((T, E), 5.0, device=DEV)
+    L.moe_route_grad(logits, ids, dw, T, E, k, L.SIGMOID if sigmoid else L.SOFTMAX, False, out, L.F32)
+    for at in (slice(0, 9), slice(2 ** 21 - 4, 2 ** 21 + 4), slice(T // 2, T // 2 + 9), slice(T - 9, T)):
+        part = torch.empty_like(out[at])
+        L.moe_route_grad(logits[at].contiguous(), ids[at].contiguous(), dw[at].contiguous(), len(part), E, k,
+                         L.SIGMOID if sigmoid else L.SOFTMAX, False, part, L.F32)
+        assert torch.equal(out[at], part)
+    assert not (out == 5).any()
+
+
+@pytest.mark.parametrize("k", [1, 17])
+def test_combine_grad_many_tokens(L, k):
+    """More tokens than one launch takes."""
+    T, H = 2 ** 21 // ((k + 7) // 8) + 3, 8
+    row = torch.arange(T * k, dtype=torch.int32, device=DEV).flip(0)
+    y = torch.randn((T * k + T, H), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    dout = torch.randint(-3, 4, (T, H), device=DEV).float()
+    w = torch.full((T, k), 0.5, device=DEV)
+    off = torch.tensor([0, T * k, T * k + T], dtype=torch.int32, device=DEV)
+    dy, dw = torch.full_like(y, 9.0), torch.empty_like(w)
+    L.moe_combine_grad(dout, y, L.F32, row, w, T, k, H, off, 1, dy, dw)
+    assert torch.equal(dy[T * k:], dout)
+    assert torch.equal(dy[:T * k], (dout * 0.5).repeat_interleave(k, 0).flip(0))
+    prod = y[row.long()].view(T, k, H).double() * dout[:, None].double()
+    assert ((dw.double() - prod.sum(2)).abs() <= 10 * 2.0 ** -24 * prod.abs().sum(2)).all()

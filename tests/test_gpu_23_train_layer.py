@@ -344,6 +344,18 @@ def test_refusals(L):
     for bad in (x.float(), x[:2], x.t().contiguous()):
         with pytest.raises((ValueError, TypeError)):
             layer.backward(step, bad)
+    grads = layer.new_grads()
+    for name, bad in (("w13", None), ("w2", grads.w2[:4]), ("router_w", grads.router_w.to(BF)),
+                      ("shared_w13", grads.shared_w13.t().contiguous().t())):
+        keep = getattr(grads, name)
+        setattr(grads, name, bad)
+        with pytest.raises((ValueError, TypeError), match=f"grads.{name}"):
+            layer.backward(step, x, grads)
+        setattr(grads, name, keep)
+    other, _ = make(L, "bf16", 8, 64, 32, 2)
+    with pytest.raises(RuntimeError):
+        other.backward(step, x)
+    layer.backward(step, x, grads)  # none of these touched the step
     fp8 = L.MoELayer("fp8", 256, 128, 2, torch.zeros((4, 256, 256), dtype=torch.uint8, device=DEV),
                      torch.zeros((4, 256, 128), dtype=torch.uint8, device=DEV), torch.ones((4, 2, 2), device=DEV),
                      torch.ones((4, 2, 1), device=DEV))
