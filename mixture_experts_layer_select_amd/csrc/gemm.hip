@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256, kF32Grid) void gemm_f32_kernel(GemmArgs a) {
     constexpr bool kPc = kForm == kForward, kQc = kForm != kWeights;
     constexpr int kB = kT / 32;  // 16-wide blocks of a wave, each way
     __shared__ __attribute__((aligned(16))) uint8_t lp[2][kStageF], lq[2][kStageF];
-    __shared__ TileMap tm;
+    __shared__ RowTiles<kMaxGroups> tm;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15, lk = lane >> 4;
     const int wp = (wave & 1) * (kT / 2), wq = (wave >> 1) * (kT / 2);
     const int cols = kForm == kForward ? a.N : a.K;  // of the output
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256, kF32Grid) void gemm_f32_kernel(GemmArgs a) {
     const bool apart = kForm == kWeights ? a.out_last != nullptr : a.p_last != nullptr;
     int n_items;
     if constexpr (kForm == kWeights) n_items = a.n_groups * MB * NB;
-    else n_items = build_tile_map(tm, a.offsets, a.n_groups, a.max_rows, kT) * NB;
+    else n_items = even_tiles<256>(tm, a.offsets, a.n_groups, a.max_rows, kT) * NB;
 
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
         const float *p, *q;
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256, kF32Grid) void gemm_f32_kernel(GemmArgs a) {
             q = (const float*)a.q + (size_t)r0 * a.N;
             out = apart && g == a.n_groups - 1 ? (float*)a.out_last : (float*)a.out + g * w_size;
         } else {
-            const MTile t = item_at(tm, a.offsets, a.n_groups, a.max_rows, item, NB, kT, nb);
+            const MTile t = row_item_at(tm, a.n_groups, item, NB, nb);
             n_k = kForm == kForward ? a.K : a.N;
             p = apart && t.group == a.n_groups - 1 ? (const float*)a.p_last : (const float*)a.p + t.group * w_size;
             q = (const float*)a.q + (size_t)t.row0 * n_k;

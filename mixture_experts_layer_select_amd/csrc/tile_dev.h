@@ -42,6 +42,17 @@ __device__ __forceinline__ void number_tiles(RowTiles<kGroups>& tm, int n_groups
     }
 }
 
+// the same for tiles of at most h rows, from the offsets; all kThreads threads call, returns the number of tiles
+template <int kThreads, int kGroups>
+__device__ __forceinline__ int even_tiles(RowTiles<kGroups>& tm, const int32_t* __restrict__ offsets, int n_groups,
+                                          int max_rows, int h) {
+    for (int g = threadIdx.x; g <= n_groups; g += kThreads) tm.row0[g] = clamp_row(offsets[g], max_rows);
+    __syncthreads();
+    number_tiles(tm, n_groups, h);
+    __syncthreads();
+    return tm.tile_start[n_groups];
+}
+
 // All kThreads threads call (it holds barriers); returns the number of tiles. The height
 // is kTile rows, or half or a quarter of it where all items then still run at once: a call so
 // small takes as long as its tallest tile (MXFP4, nine groups of 17 rows and one of 203
