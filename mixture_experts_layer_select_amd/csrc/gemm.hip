@@ -29,62 +29,93 @@ struct GemmArgs {
 
 // ============================================================================ fp32
 // Tiles of 64 x 64, 4 waves of a quarter each, operands through registers into
-// two LDS stages. A step takes 64 bytes of the contraction: of each row of a
-// K-contiguous operand, or 16 rows of a K-strided one; loads run kAhead steps
-// ahead in a register ring. Bound by the matrix cores (an fp32 product costs
-// sixteen bf16 ones), so blocks past a tile's rows are left out. 4096 rows of 8
-// groups, 2048 x 2048: 350 us forward and input (98 TFLOP/s), 320 weights; tiles
-// of 128 took 408, 408 and 283. 203 rows of 9 groups, 768 x 1280: 38, 26 and 15
-// us, tiles of 128 102, 63 and 17.
+// two LDS stages, loads kAhead steps ahead. A step takes kStep of the
+// contraction: of each row of a K-contiguous operand, or kStep rows of a
+// K-strided one. Bound by the matrix cores (an fp32 product costs sixteen bf16
+// ones), so blocks past a tile's rows are left out. 4096 rows of 8 groups, 2048 x
+// 2048: 350 us forward and input (98 TFLOP/s), 320 weights, with steps of 16;
+// tiles of 128 took 408, 408 and 283, steps of 32 390, 388 and 333.
+//
+// Calls of few tiles are as long as their chain of steps: they take steps of 32,
+// and in a tile of at most 32 rows the two waves that would have none take
+// the second half of each step, their sums joined at the end. 203 rows of 9
+// groups, 768 x 1280: forward 25 us, input 18, against 38 and 26; 200 rows of 32
+// groups, 1000 x 1000: 25 and 31, against 32 and 34.
 constexpr int kT = 64;
-constexpr int kStepF = 16;  // contraction per step
 constexpr int kAhead = 2;    // four: the same
 constexpr int kF32Grid = 4;  // workgroups per CU
-constexpr int kRowC = 64 + 16;  // LDS bytes of a K-contiguous row
-constexpr int kRowS = kT * 4 + 16;  // and of a K-strided one
-constexpr int kStageF = kT * kRowC > kStepF * kRowS ? kT * kRowC : kStepF * kRowS;
+template <int kStep>
+struct F32Step {
+    static constexpr int row_c = kStep * 4 + 16;  // LDS bytes of a K-contiguous row
+    static constexpr int row_s = kT * 4 + 16;     // and of a K-strided one
+    static constexpr int bytes = kT * row_c > kStep * row_s ? kT * row_c : kStep * row_s;
+    static constexpr int pieces = kStep / 16;     // 16-byte pieces of an operand that a thread loads
+    struct Regs {
+        u32x4 v[pieces];
+    };
+};
 
-// Where this thread's 16 bytes of a step's operand tile lie: output index and place in the contraction.
-template <bool kContig>
-__device__ __forceinline__ int piece_o() { return kContig ? threadIdx.x >> 2 : threadIdx.x % (kT / 4) * 4; }
-template <bool kContig>
-__device__ __forceinline__ int piece_k() { return kContig ? (threadIdx.x & 3) * 4 : threadIdx.x / (kT / 4); }
+// Where this thread's piece i of a step's operand tile lies: output index and place in the contraction.
+template <int kStep, bool kContig>
+__device__ __forceinline__ int piece_o(int i) {
+    return kContig ? (threadIdx.x + 256 * i) / (kStep / 4) : threadIdx.x % (kT / 4) * 4;
+}
+template <int kStep, bool kContig>
+__device__ __forceinline__ int piece_k(int i) {
+    return kContig ? (threadIdx.x & (kStep / 4 - 1)) * 4 : threadIdx.x / (kT / 4) + 16 * i;
+}
 // What lies outside the operand is loaded from its edge, without branches, and staged as zeros.
-template <bool kContig>
-__device__ __forceinline__ u32x4 fetch(const float* base, size_t ld, int n_out, int out0, int n_k, int k0) {
-    const int o = min(out0 + piece_o<kContig>(), n_out - (kContig ? 1 : 4));
-    const int k = min(k0 + piece_k<kContig>(), n_k - (kContig ? 4 : 1));
-    return *reinterpret_cast<const u32x4*>(base + (kContig ? (size_t)o * ld + k : (size_t)k * ld + o));
-}
-template <bool kContig>
-__device__ __forceinline__ void stage(uint8_t* l, int n_out, int out0, int n_k, int k0, u32x4 v) {
-    const int o = piece_o<kContig>(), k = piece_k<kContig>();
-    const bool in = out0 + o < n_out && k0 + k < n_k;
+template <int kStep, bool kContig>
+__device__ __forceinline__ typename F32Step<kStep>::Regs fetch(const float* base, size_t ld, int n_out, int out0, int n_k,
+                                                               int k0) {
+    typename F32Step<kStep>::Regs r;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = in ? v[e] : 0u;
-    *reinterpret_cast<u32x4*>(l + (kContig ? o * kRowC + k * 4 : k * kRowS + o * 4)) = v;
+    for (int i = 0; i < F32Step<kStep>::pieces; ++i) {
+        const int o = min(out0 + piece_o<kStep, kContig>(i), n_out - (kContig ? 1 : 4));
+        const int k = min(k0 + piece_k<kStep, kContig>(i), n_k - (kContig ? 4 : 1));
+        r.v[i] = *reinterpret_cast<const u32x4*>(base + (kContig ? (size_t)o * ld + k : (size_t)k * ld + o));
+    }
+    return r;
 }
-// lane (li, lk) of a 16-wide block at output o0: elements 4 lk + [0, 4) of the step's contraction
-template <bool kContig>
-__device__ __forceinline__ f32x4 fragment(const uint8_t* l, int o0, int li, int lk) {
+template <int kStep, bool kContig>
+__device__ __forceinline__ void stage(uint8_t* l, int n_out, int out0, int n_k, int k0,
+                                      const typename F32Step<kStep>::Regs& r) {
+    using S = F32Step<kStep>;
+#pragma unroll
+    for (int i = 0; i < S::pieces; ++i) {
+        const int o = piece_o<kStep, kContig>(i), k = piece_k<kStep, kContig>(i);
+        const bool in = out0 + o < n_out && k0 + k < n_k;
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = in ? r.v[i][e] : 0u;
+        *reinterpret_cast<u32x4*>(l + (kContig ? o * S::row_c + k * 4 : k * S::row_s + o * 4)) = v;
+    }
+}
+// lane (li, lk) of a 16-wide block at output o0: elements 16 h + 4 lk + [0, 4) of the step's contraction
+template <int kStep, bool kContig>
+__device__ __forceinline__ f32x4 fragment(const uint8_t* l, int o0, int h, int li, int lk) {
+    using S = F32Step<kStep>;
     if constexpr (kContig) {
-        return *reinterpret_cast<const f32x4*>(l + (o0 + li) * kRowC + lk * 16);
+        return *reinterpret_cast<const f32x4*>(l + (o0 + li) * S::row_c + h * 64 + lk * 16);
     } else {
         f32x4 v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(l + (lk * 4 + j) * kRowS + (o0 + li) * 4);
+        for (int j = 0; j < 4; ++j)
+            v[j] = *reinterpret_cast<const float*>(l + (16 * h + lk * 4 + j) * S::row_s + (o0 + li) * 4);
         return v;
     }
 }
 
-template <int kForm>
-__global__ __launch_bounds__(256, kF32Grid) void gemm_f32_kernel(GemmArgs a) {
+template <int kForm, int kStep>
+__global__ __launch_bounds__(256, kStep == 16 ? kF32Grid : 2) void gemm_f32_kernel(GemmArgs a) {
+    using S = F32Step<kStep>;
     constexpr bool kPc = kForm == kForward, kQc = kForm != kWeights;
     constexpr int kB = kT / 32;  // 16-wide blocks of a wave, each way
-    __shared__ __attribute__((aligned(16))) uint8_t lp[2][kStageF], lq[2][kStageF];
+    __shared__ __attribute__((aligned(16))) uint8_t lp[2][S::bytes], lq[2][S::bytes];
     __shared__ RowTiles<kMaxGroups> tm;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15, lk = lane >> 4;
-    const int wp = (wave & 1) * (kT / 2), wq = (wave >> 1) * (kT / 2);
+    const int lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 1;
+    const int wp = (wave & 1) * (kT / 2);
     const int cols = kForm == kForward ? a.N : a.K;  // of the output
     const int NB = (cols + kT - 1) / kT, MB = (a.N + kT - 1) / kT;
     const size_t w_size = (size_t)a.N * a.K, ldq = kForm == kForward ? a.K : a.N;
@@ -116,17 +147,19 @@ __global__ __launch_bounds__(256, kF32Grid) void gemm_f32_kernel(GemmArgs a) {
             q0 = 0;
             rows = t.rows;
         }
+        const bool split = kStep == 32 && rows - q0 <= kT / 2;
+        const int wq = split ? 0 : half * (kT / 2);
         const int nj = (rows - q0 - wq + 15) / 16;  // of this wave's row blocks, those that hold rows
         f32x4 acc[kB][kB] = {};
-        u32x4 rp[kAhead], rq[kAhead];
-        const int nk = (n_k + kStepF - 1) / kStepF;
+        typename S::Regs rp[kAhead], rq[kAhead];
+        const int nk = (n_k + kStep - 1) / kStep;
         auto load = [&](int kc, int s) {
-            rp[s] = fetch<kPc>(p, a.K, cols, nb * kT, n_k, kc * kStepF);
-            rq[s] = fetch<kQc>(q, ldq, rows, q0, n_k, kc * kStepF);
+            rp[s] = fetch<kStep, kPc>(p, a.K, cols, nb * kT, n_k, kc * kStep);
+            rq[s] = fetch<kStep, kQc>(q, ldq, rows, q0, n_k, kc * kStep);
         };
         auto put = [&](int kc, int s) {
-            stage<kPc>(lp[kc & 1], cols, nb * kT, n_k, kc * kStepF, rp[s]);
-            stage<kQc>(lq[kc & 1], rows, q0, n_k, kc * kStepF, rq[s]);
+            stage<kStep, kPc>(lp[kc & 1], cols, nb * kT, n_k, kc * kStep, rp[s]);
+            stage<kStep, kQc>(lq[kc & 1], rows, q0, n_k, kc * kStep, rq[s]);
         };
         __syncthreads();  // the previous item's reads
         if (nk > 0) {
@@ -141,25 +174,41 @@ __global__ __launch_bounds__(256, kF32Grid) void gemm_f32_kernel(GemmArgs a) {
                 const int kc = k0 + s;
                 if (kc >= nk) break;
                 barrier_only();  // step kc is staged; the loads ahead stay in flight
-                f32x4 fp[kB], fq[kB];
 #pragma unroll
-                for (int i = 0; i < kB; ++i) {
-                    fp[i] = fragment<kPc>(lp[kc & 1], wp + 16 * i, li, lk);
-                    fq[i] = fragment<kQc>(lq[kc & 1], wq + 16 * i, li, lk);
-                }
+                for (int h = 0; h < kStep / 16; ++h) {
+                    if (split && h != half) continue;
+                    f32x4 fp[kB], fq[kB];
 #pragma unroll
-                for (int j = 0; j < kB; ++j)
-                    if (j < nj) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-#pragma unroll
-                            for (int i = 0; i < kB; ++i)
-                                acc[i][j] =
-                                    __builtin_amdgcn_mfma_f32_16x16x4f32(fp[i][t], fq[j][t], acc[i][j], 0, 0, 0);
+                    for (int i = 0; i < kB; ++i) {
+                        fp[i] = fragment<kStep, kPc>(lp[kc & 1], wp + 16 * i, h, li, lk);
+                        fq[i] = fragment<kStep, kQc>(lq[kc & 1], wq + 16 * i, h, li, lk);
                     }
+#pragma unroll
+                    for (int j = 0; j < kB; ++j)
+                        if (j < nj) {
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                                for (int i = 0; i < kB; ++i)
+                                    acc[i][j] =
+                                        __builtin_amdgcn_mfma_f32_16x16x4f32(fp[i][t], fq[j][t], acc[i][j], 0, 0, 0);
+                        }
+                }
                 put(kc + 1, (s + 1) % kAhead);  // the other stage: its readers passed this step's barrier
                 load(kc + 1 + kAhead, (s + 1) % kAhead);
             }
+        }
+        if (split) {
+            __syncthreads();  // the last step's reads
+            f32x4* sums = reinterpret_cast<f32x4*>(lp[0]) + (wave & 1) * 64 * kB * kB;
+            static_assert(2 * 64 * kB * kB * 16 <= 2 * S::bytes, "the second halves' sums lie in P's stages");
+#pragma unroll
+            for (int n = 0; n < kB * kB; ++n)
+                if (half == 1) sums[n * 64 + lane] = acc[n / kB][n % kB];
+            __syncthreads();
+            if (half == 1) continue;
+#pragma unroll
+            for (int n = 0; n < kB * kB; ++n) acc[n / kB][n % kB] += sums[n * 64 + lane];
         }
         // lane (li, lk): columns 4 lk + [0, 4) of the block at output row li
         if (kForm == kWeights && nk == 0 && a.accumulate) continue;
@@ -184,11 +233,32 @@ moe_status launch_f32(const GemmArgs& a, hipStream_t st) {
     const long tiles = kForm == kWeights ? (long)a.n_groups * ((a.N + kT - 1) / kT)
                                          : ((long)a.max_rows + kT - 1) / kT + std::min(a.n_groups, a.max_rows);
     const int grid = (int)std::min(tiles * nb, (long)device_info().cu_count * kF32Grid);
-    hipLaunchKernelGGL(gemm_f32_kernel<kForm>, dim3(grid), dim3(256), 0, st, a);
+    if constexpr (kForm != kWeights) {
+        if (tiles * nb <= (long)device_info().cu_count * kF32Grid) {  // all at once
+            hipLaunchKernelGGL((gemm_f32_kernel<kForm, 32>), dim3(grid), dim3(256), 0, st, a);
+            return check_launch("gemm_f32_kernel");
+        }
+    }
+    hipLaunchKernelGGL((gemm_f32_kernel<kForm, 16>), dim3(grid), dim3(256), 0, st, a);
     return check_launch("gemm_f32_kernel");
 }
 
 // ============================================================================ bf16, an LDS ring
+// Tiles of up to 256 x 256 on 8 waves, one workgroup a CU: wave (wm, wn) of a 2 x 4 grid owns the 32-row blocks
+// 2j + wm and 64 columns, as 2 x NX blocks of 32 x 32 accumulators (NX = 1 to 4 by the tile's height). Both operands
+// of a step arrive in LDS by direct loads, a ring of steps ahead of the products; XCDs walk contiguous slices of the
+// items (row_item_at's order), so that tiles that run side by side share operands through L2.
+//
+// K-contiguous operands lie in rows of 128 bytes and are read 16 bytes a lane; K-strided ones in rows of 512 (256
+// columns of one row) and are read transposed: ds_read_b64_tr_b16 hands lane i of sixteen the
+// element i of four rows, and two such reads make its eight of the contraction. The swizzles spread both over the
+// banks (no conflicts counted).
+//
+// A step's barrier stands before its last quarter, whose fragments are in registers by then, so no wave waits at it
+// with idle matrix cores; the loads of a later step stand one behind each pair of products. In a burst behind the
+// barrier they kept waves from issuing products (one group of 8192^3, forward: 911 us; spread 836, and 801 with the
+// ring's rest behind its loop). There it runs at 1.37 PFLOP/s, dx at 1.40 and dw at 1.29, with a clock that falls to 1.4 to
+// 1.6 GHz under the products; a large library product of the same layouts reaches 1.39, 1.23 and 1.08.
 constexpr int kBig = 256;  // rows and columns of a tile
 constexpr int kBigThreads = 512;
 constexpr int kNonTemporal = 2;  // buffer stores' cache policy
@@ -729,6 +799,10 @@ moe_status launch_rows(const GemmArgs& a, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------- weights
+// dw of a group in tiles of 256 x 256, both operands K-strided, over the group's rows: steps of 32 of them in a ring of
+// four stages (steps of 64 in two took 906 us for 8192^3, these 881), since a training batch gives an expert only some
+// hundred rows and a ring of short steps ends closer to them. Tiles that short are bound by their stores: 16384 rows
+// of 32 experts, 7168 x 2048 in fp32, 654 us, 404 of them without the stores.
 template <typename TO>
 __global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a) {
     constexpr int kStepK = 32;  // rows of a step
