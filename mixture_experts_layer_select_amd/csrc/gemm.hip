@@ -370,18 +370,22 @@ struct RowsPlan {
 };
 
 // All threads call; returns the number of tiles, their height and the column blocks' width. Of the heights 64 to 256 and
-// the widths 64 to 256 (multiples of kUnit) it takes the pair with the shortest estimate: the rounds of items that a
-// workgroup walks times a step's time times the steps, of which an item's start and end are worth about three. A step
-// of a tile of h x w columns (NX = ceil(h / 64), mt tiles of a group sharing the weights) measured about
-// 0.35 + 0.2 NX + (0.4 + 0.65 / mt) w / 256 us where all CUs load at once; the products' term is half up to 128
-// columns (four waves of eight have work), the loads' term goes with the CUs in use. Tiles of 64 x 64 split
-// their contraction over the waves: a quarter of the steps, with the loads of a whole tile.
+// the widths 64 to 256 (multiples of kUnit; of 64 where the products bound it, since a wave's 64 columns cost the same
+// whether they are there or not) it takes the pair with the shortest estimate: the rounds of items that a workgroup
+// walks, times a step's time, times the steps and three for an item's start and end. A step of a tile of h x w columns
+// takes about 0.2 + 0.3 NX + (0.4 + 0.65 / mt) w / 256 us, NX = ceil(h / 64), mt tiles of a group sharing the weights:
+// 0.2 NX up to 128 columns (four waves of eight have products), the loads' term down to half where few CUs load. Tiles
+// of 64 x 64 split their contraction over the waves: a quarter of the steps, with the loads of a whole tile
+// (K-strided P in pieces of 128 bytes of a row instead of 512: 1.35 times as long where rounds follow one another).
+// All sixteen pairs of 64, 128, 192 and 256 were timed on 30 calls of 50 to 16384 rows and 300 to 7168 columns: the
+// plan's pair takes 1% longer than the fastest in the mean, 10% at most.
 template <int kUnit>
 __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restrict__ offsets, int n_groups,
                                          int max_rows, int cols, int nk, int& width,
                                          int& height) {
     for (int g = threadIdx.x; g <= n_groups; g += kBigThreads) plan.t.row0[g] = clamp_row(offsets[g], max_rows);
     __syncthreads();
+    constexpr float kSplitLoads = kUnit == 64 ? 1.35f : 1.0f;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     if (wave < 4) {
         const int h = 64 * (wave + 1);
@@ -403,15 +407,15 @@ __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restri
         }
         const int w = kBig - kUnit * lane;
         float cost = 3e38f;
-        if (w >= 64 && tiles) {
+        if (w >= 64 && tiles && (w % 64 == 0 || nx <= 2.0f * (float)tiles)) {
             const int items = tiles * ((cols + w - 1) / w), per = gridDim.x >> 3;
             const int rounds = ((items + 7) / 8 + per - 1) / per;
             const bool split = h == 64 && w == 64;
-            const float part = split ? 1.0f : (float)w / kBig, each = 1.0f / (float)tiles;
+            const float part = !split ? (float)w / kBig : rounds > 1 ? kSplitLoads : 1.0f, each = 1.0f / (float)tiles;
             const float busy = fminf(1.0f, (float)items / (float)gridDim.x);
-            const float step = 0.35f + 0.2f * nx * each * (w <= 128 ? 0.5f : 1.0f) +
-                               busy * (0.4f + 0.65f * share * each + (split ? 0.3f : 0.f)) * part;
-            cost = (float)rounds * step * (float)(split ? (nk + 3) / 4 + 4 : nk + 3);
+            const float step = 0.2f + nx * each * (w <= 128 ? 0.2f : 0.3f) +
+                               (0.5f + 0.5f * busy) * (0.4f + 0.65f * share * each) * part;
+            cost = (float)rounds * step * (float)(split ? (nk + 3) / 4 + 3 : nk + 3);
         }
         float best = cost;
 #pragma unroll
