@@ -25,6 +25,7 @@ struct GemmArgs {
     int n_groups, max_rows, N, K;
     void *out, *out_last;  // kWeights: dw of the routed groups and of the last one
     int accumulate;
+    int height;  // kWeights: rows of a tile, 64 to 256
 };
 
 // ============================================================================ fp32
@@ -803,7 +804,7 @@ moe_status launch_rows(const GemmArgs& a, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------- weights
-// dw of a group in tiles of 256 x 256, both operands K-strided, over the group's rows: steps of 32 of them in a ring of
+// dw of a group in tiles of `height` x 256, both operands K-strided, over the group's rows: steps of 32 of them in a ring of
 // four stages (steps of 64 in two took 906 us for 8192^3, these 881), since a training batch gives an expert only some
 // hundred rows and a ring of short steps ends closer to them. Tiles that short are bound by their stores: 16384 rows
 // of 32 experts, 7168 x 2048 in fp32, 654 us, 404 of them without the stores.
@@ -819,7 +820,7 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave & 1, wn = wave >> 1;
     const int l31 = lane & 31, hi = lane >> 5;
-    const int NB = (a.K + kBig - 1) / kBig, MB = (a.N + kBig - 1) / kBig;
+    const int NB = (a.K + kBig - 1) / kBig, MB = (a.N + a.height - 1) / a.height;
     const size_t w_size = (size_t)a.N * a.K;
     for (int g = threadIdx.x; g <= a.n_groups; g += kBigThreads) row0[g] = clamp_row(a.offsets[g], a.max_rows);
     __syncthreads();
@@ -864,8 +865,8 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a
         Tile t;
         t.n_k = max(0, r1 - r0);
         t.c0 = __builtin_amdgcn_readfirstlane(c.nb) * kBig;
-        t.o0 = __builtin_amdgcn_readfirstlane(c.mb) * kBig;
-        t.rows = min(kBig, a.N - t.o0);
+        t.o0 = __builtin_amdgcn_readfirstlane(c.mb) * a.height;
+        t.rows = min(a.height, a.N - t.o0);
         t.p = (const uint16_t*)a.p + (size_t)r0 * a.K;
         t.q = (const uint16_t*)a.q + (size_t)r0 * a.N;
         t.out = (a.out_last && group == a.n_groups - 1 ? (TO*)a.out_last : (TO*)a.out + group * w_size) +
@@ -873,7 +874,7 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a
         return t;
     };
     // Pieces 2n and 2n + 1 of step kc: P's for n = 0, Q's for n = 1. Rows past the group are not fetched and arrive as
-    // zeros; columns past the matrix bring the next row's, for outputs that are not kept.
+    // zeros; columns past x's row bring the next row's, for outputs that are not kept.
     auto two = [&](const Tile& c, int kc, uint8_t* S, auto n_c) MX_INLINE {
         constexpr bool kQ = decltype(n_c)::value == 1;
         const int ld = kQ ? a.N : a.K, o = kQ ? c.o0 : c.c0;
@@ -881,7 +882,7 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a
         const __amdgpu_buffer_rsrc_t d = buffer_rsrc((kQ ? c.q : c.p) + (size_t)kc * kStepK * ld + o,
                                                      left ? (uint32_t)(left * ld - o) * 2 : 0u);
         uint8_t* l = S + (kQ ? 16384 : 0) + wave * 1024;
-        const uint32_t v = kQ ? vq : vp;
+        const uint32_t v = kQ ? vq + (8 * cs < c.rows ? 0u : 0x40000000u) : vp;
         lds_buf16(d, v, 0, l);
         __builtin_amdgcn_sched_barrier(0);
         return [=]() MX_INLINE { lds_buf16(d, v + 32u * ld, 0, l + 8192); };
@@ -1032,10 +1033,28 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a
     }
 }
 
+// The height with the shortest estimate: the rounds of items that a workgroup walks, times a tile's stores (0.049 h us in
+// bf16, 1.6 times that in fp32) and its steps (0.3 + 0.0011 h us each), at the bound's rows for each group. 5000 rows of
+// one group, 256 x 7168: 93 us in tiles of 256 rows, 60 of 64; 16384 of 32, 7168 x 2048: 562 of 256, 1173 of 64; 150 of 16, 680 x
+// 680: 8.4 and 10.2, 7.9 of 192.
 template <typename TO>
-moe_status launch_weights(const GemmArgs& a, hipStream_t st) {
-    const long items = (long)a.n_groups * ((a.N + kBig - 1) / kBig) * ((a.K + kBig - 1) / kBig);
-    const int grid = (int)std::min((items + 7) / 8 * 8, (long)device_info().cu_count / 8 * 8);
+moe_status launch_weights(GemmArgs a, hipStream_t st) {
+    const int grid_max = device_info().cu_count / 8 * 8;
+    const float steps = (float)a.max_rows / (float)a.n_groups / 32.0f + 1.0f;
+    const long blocks = (long)a.n_groups * ((a.K + kBig - 1) / kBig);
+    long items = 0;
+    float best = 0.f;
+    for (int h = kBig; h >= 64; h -= 64) {
+        const long n = blocks * ((a.N + h - 1) / h);
+        const float rounds = (float)((n + grid_max - 1) / grid_max);
+        const float cost = rounds * (0.049f * h * (sizeof(TO) == 4 ? 1.6f : 1.0f) + steps * (0.3f + 0.0011f * h));
+        if (h == kBig || cost < best) {
+            best = cost;
+            items = n;
+            a.height = h;
+        }
+    }
+    const int grid = (int)std::min((items + 7) / 8 * 8, (long)grid_max);
     hipLaunchKernelGGL(gemm_weights_kernel<TO>, dim3(grid), dim3(kBigThreads), 0, st, a);
     return check_launch("gemm_weights_kernel");
 }
