@@ -513,7 +513,8 @@ class MoELayer:
         if grads is None:
             if accumulate:
                 raise ValueError("accumulate needs the gradients to add to")
-            grads = self.new_grads()
+            with self._on(stream):  # zeroed there, ahead of what is written
+                grads = self.new_grads()
         self._check_grads(grads)
         self._bufs[("serial", T)] += 1
         sh, cap, n = self.shared or {}, T * self.k + T, self.n_groups
