@@ -44,7 +44,7 @@ struct GemmArgs {
 // groups, 1000 x 1000: 25 and 31, against 32 and 34.
 constexpr int kT = 64;
 constexpr int kAhead = 2;    // four: the same
-constexpr int kF32Grid = 4;  // workgroups per CU
+constexpr int kF32Grid = 4;  // workgroups per CU; eight for dw, whose items are short (320 -> 308 us, others slower)
 template <int kStep>
 struct F32Step {
     static constexpr int row_c = kStep * 4 + 16;  // LDS bytes of a K-contiguous row
@@ -233,7 +233,7 @@ moe_status launch_f32(const GemmArgs& a, hipStream_t st) {
     const long nb = ((kForm == kForward ? a.N : a.K) + kT - 1) / kT;
     const long tiles = kForm == kWeights ? (long)a.n_groups * ((a.N + kT - 1) / kT)
                                          : ((long)a.max_rows + kT - 1) / kT + std::min(a.n_groups, a.max_rows);
-    const int grid = (int)std::min(tiles * nb, (long)device_info().cu_count * kF32Grid);
+    const int grid = (int)std::min(tiles * nb, (long)device_info().cu_count * (kForm == kWeights ? 8 : kF32Grid));
     if constexpr (kForm != kWeights) {
         if (tiles * nb <= (long)device_info().cu_count * kF32Grid) {  // all at once
             hipLaunchKernelGGL((gemm_f32_kernel<kForm, 32>), dim3(grid), dim3(256), 0, st, a);
