@@ -258,7 +258,7 @@ moe_status launch_f32(const GemmArgs& a, hipStream_t st) {
 // A step's barrier stands before its last quarter, whose fragments are in registers by then, so no wave waits at it
 // with idle matrix cores; the loads of a later step stand one behind each pair of products. In a burst behind the
 // barrier they kept waves from issuing products (one group of 8192^3, forward: 911 us; spread 836, and 801 with the
-// ring's rest behind its loop). There it runs at 1.37 PFLOP/s, dx at 1.40 and dw at 1.29, with a clock that falls to 1.4 to
+// ring's rest behind its loop). There it runs at 1.37 PFLOP/s, dx at 1.40 and dw at 1.31, with a clock that falls to 1.4 to
 // 1.6 GHz under the products; a large library product of the same layouts reaches 1.39, 1.23 and 1.08.
 constexpr int kBig = 256;  // rows and columns of a tile
 constexpr int kBigThreads = 512;
