@@ -366,9 +366,12 @@ __device__ __forceinline__ void put_block(__amdgpu_buffer_rsrc_t d, int ld, int 
 // every item's start waits for it.
 struct RowsPlan {
     RowTiles<kMaxGroups> t;
-    float cost[4];  // of the best width for each height
+    uint32_t cost[4];  // of the best width for each height
     int tiles[4], width[4];
 };
+
+// of whole numbers, for the estimate only; the division rounds correctly, so a whole quotient stays whole
+__device__ __forceinline__ float ceil_div(float a, float b) { return ceilf(a / b); }
 
 // All threads call; returns the number of tiles, their height and the column blocks' width. Of the heights 64 to 256 and
 // the widths 64 to 256 (multiples of kUnit; of 64 where the products bound it, since a wave's 64 columns cost the same
@@ -379,7 +382,9 @@ struct RowsPlan {
 // of 64 x 64 split their contraction over the waves: a quarter of the steps, with the loads of a whole tile
 // (K-strided P in pieces of 128 bytes of a row instead of 512: 1.35 times as long where rounds follow one another).
 // All sixteen pairs of 64, 128, 192 and 256 were timed on 30 calls of 50 to 16384 rows and 300 to 7168 columns: the
-// plan's pair takes 1% longer than the fastest in the mean, 10% at most.
+// plan's pair takes 1% longer than the fastest in the mean, 10% at most. Every workgroup waits for the search, about 1 us
+// of a call: sums by DPP moves, quotients in fp32 instead of integer divisions, and one minimum that carries its lane
+// (50 rows of each of 16 groups, 1000 x 1000, forward: 9.9 -> 9.3 us; 100 rows of 8, 2000 x 304: 8.7 -> 7.8).
 template <int kUnit>
 __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restrict__ offsets, int n_groups,
                                          int max_rows, int cols, int nk, int& width,
@@ -389,43 +394,41 @@ __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restri
     constexpr float kSplitLoads = kUnit == 64 ? 1.35f : 1.0f;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     if (wave < 4) {
-        const int h = 64 * (wave + 1);
+        const int parts = wave + 1, h = 64 * parts;
         int tiles = 0;
         float nx = 0.f, share = 0.f;  // summed over the tiles: 64-row pieces, and parts of a group's weights
         for (int g = lane; g < n_groups; g += 64) {
-            const int m = max(0, plan.t.row0[g + 1] - plan.t.row0[g]), nt = (m + h - 1) / h;
+            const int q = (max(0, plan.t.row0[g + 1] - plan.t.row0[g]) + 63) >> 6;  // pieces of 64 rows
+            const int nt = parts == 1 ? q : parts == 2 ? (q + 1) >> 1 : parts == 3 ? (q + 2) / 3 : (q + 3) >> 2;
             if (nt) {
                 tiles += nt;
-                nx += (float)(nt * (((m + nt - 1) / nt + 63) / 64));
+                nx += (float)nt * ceil_div((float)q, (float)nt);
                 share += 1.0f;
             }
         }
-#pragma unroll
-        for (int s = 32; s >= 1; s >>= 1) {
-            tiles += __shfl_xor(tiles, s);
-            nx += __shfl_xor(nx, s);
-            share += __shfl_xor(share, s);
-        }
+        tiles = wave_total(tiles);
+        nx = wave_total(nx);
+        share = wave_total(share);
         const int w = kBig - kUnit * lane;
-        float cost = 3e38f;
+        // the estimate's bits, the lane in the lowest six: the smallest is the best width's (positive floats sort as integers)
+        uint32_t cost = 0x7f000000u + lane;
         if (w >= 64 && tiles && (w % 64 == 0 || nx <= 2.0f * (float)tiles)) {
-            const int items = tiles * ((cols + w - 1) / w), per = gridDim.x >> 3;
-            const int rounds = ((items + 7) / 8 + per - 1) / per;
+            const float items = (float)tiles * ceil_div((float)cols, (float)w);
+            const float rounds = ceil_div(ceilf(0.125f * items), (float)(gridDim.x >> 3));
             const bool split = h == 64 && w == 64;
-            const float part = !split ? (float)w / kBig : rounds > 1 ? kSplitLoads : 1.0f, each = 1.0f / (float)tiles;
-            const float busy = fminf(1.0f, (float)items / (float)gridDim.x);
+            const float part = !split ? (float)w / kBig : rounds > 1.f ? kSplitLoads : 1.0f, each = 1.0f / (float)tiles;
+            const float busy = fminf(1.0f, items / (float)gridDim.x);
             const float step = 0.2f + nx * each * (w <= 128 ? 0.2f : 0.3f) +
                                (0.5f + 0.5f * busy) * (0.4f + 0.65f * share * each) * part;
-            cost = (float)rounds * step * (float)(split ? (nk + 3) / 4 + 3 : nk + 3);
+            const float c = rounds * step * (float)(split ? (nk + 3) / 4 + 3 : nk + 3);
+            cost = (__float_as_uint(c) & ~63u) + lane;
         }
-        float best = cost;
 #pragma unroll
-        for (int s = 32; s >= 1; s >>= 1) best = fminf(best, __shfl_xor(best, s));
-        const int first = __builtin_ctzll(__ballot(cost == best));
+        for (int s = 8; s >= 1; s >>= 1) cost = min(cost, (uint32_t)__shfl_xor((int)cost, s));  // 13 widths at most
         if (lane == 0) {
-            plan.cost[wave] = best;
+            plan.cost[wave] = cost >> 6;
             plan.tiles[wave] = tiles;
-            plan.width[wave] = kBig - kUnit * first;
+            plan.width[wave] = kBig - kUnit * (int)(cost & 63u);
         }
     }
     __syncthreads();

@@ -9,6 +9,27 @@ namespace {
 
 constexpr int kRowPanel = 4;   // m-tiles per item panel
 
+// Sums over a wave by DPP moves: a shuffle through LDS takes some 100 cycles a level, a DPP move under ten.
+// wave_scan: inclusive prefix sums; the total is lane 63's.
+template <typename T, int kCtrl, int kRows>
+__device__ __forceinline__ T dpp_or_zero(T v) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, kRows, 0xf, false));
+}
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {
+    v += dpp_or_zero<T, 0x111, 0xf>(v);  // row_shr 1, 2, 4, 8: within 16 lanes
+    v += dpp_or_zero<T, 0x112, 0xf>(v);
+    v += dpp_or_zero<T, 0x114, 0xf>(v);
+    v += dpp_or_zero<T, 0x118, 0xf>(v);
+    v += dpp_or_zero<T, 0x142, 0xa>(v);  // lane 15 to the next 16, in the second and fourth
+    v += dpp_or_zero<T, 0x143, 0xc>(v);  // lane 31 to the upper 32
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_total(T v) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wave_scan(v)), 63));
+}
+
 // Tiles and rows of the groups, built by every workgroup once from the
 // device-resident offsets: first tile (tile_start) and first row (row0, clamped
 // to the buffer) of each group. A group's nt = ceil(m / height) tiles split its
@@ -29,14 +50,9 @@ __device__ __forceinline__ void number_tiles(RowTiles<kGroups>& tm, int n_groups
         for (int g0 = 0; g0 < n_groups; g0 += 64) {
             const int g = g0 + lane;
             const int nt = g < n_groups ? max(0, tm.row0[g + 1] - tm.row0[g] + h - 1) / h : 0;
-            int sum = nt;
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) {
-                const int o = __shfl_up(sum, s);
-                if (lane >= s) sum += o;
-            }
+            const int sum = wave_scan(nt);
             if (g < n_groups) tm.tile_start[g] = run + sum - nt;
-            run += __shfl(sum, 63);
+            run += __builtin_amdgcn_readlane(sum, 63);
         }
         if (lane == 0) tm.tile_start[n_groups] = run;
     }
