@@ -384,7 +384,7 @@ __device__ __forceinline__ float ceil_div(float a, float b) { return ceilf(a / b
 // All sixteen pairs of 64, 128, 192 and 256 were timed on 30 calls of 50 to 16384 rows and 300 to 7168 columns: the
 // plan's pair takes 1% longer than the fastest in the mean, 10% at most. Every workgroup waits for the search, about 1 us
 // of a call: sums by DPP moves, quotients in fp32 instead of integer divisions, and one minimum that carries its lane
-// (50 rows of each of 16 groups, 1000 x 1000, forward: 9.9 -> 9.3 us; 100 rows of 8, 2000 x 304: 8.7 -> 7.8).
+// (50 rows of 16 groups, 1000 x 1000, forward: 9.9 -> 9.3 us; 100 rows of 8 groups, 2000 x 296: 8.7 -> 7.8).
 template <int kUnit>
 __device__ __forceinline__ int plan_rows(RowsPlan& plan, const int32_t* __restrict__ offsets, int n_groups,
                                          int max_rows, int cols, int nk, int& width,
