@@ -364,7 +364,7 @@ moe_status moe_combine_norm(const void* y_perm, moe_dtype y_dt, const int32_t* s
  *   own type: MOE_F32, or MOE_BF16 from bf16. Rows past offsets[n_groups] are neither
  *   read nor written. The output must not overlap the inputs.
  * Limits: N and K multiples of 8 (bf16) or 4 (fp32), at most 65536; matrices 16-byte
- * aligned; n_groups <= 1025. */
+ * aligned; n_groups <= 1025; max_rows <= 2^30. */
 moe_status moe_grouped_gemm(const void* x, const void* w, const void* w_last, moe_dtype dt,
                             const int32_t* expert_offsets, int n_groups, int max_rows, int N, int K, void* y,
                             moe_dtype y_dt, int accumulate, void* stream);

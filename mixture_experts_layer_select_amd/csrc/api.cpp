@@ -506,6 +506,8 @@ static moe_status check_grouped(const char* fn, moe_dtype dt, moe_dtype out_dt, 
     REQUIRE(out_dt == MOE_F32 || (out_dt == MOE_BF16 && dt == MOE_BF16), MOE_ERR_UNSUPPORTED,
             "%s: the output must be MOE_F32, or MOE_BF16 from MOE_BF16", fn);
     REQUIRE(n_groups <= 1025, MOE_ERR_UNSUPPORTED, "%s: n_groups=%d > 1025", fn, n_groups);
+    // the kernels round a group's rows up to whole tiles and steps in 32 bits
+    REQUIRE(max_rows <= 1 << 30, MOE_ERR_UNSUPPORTED, "%s: max_rows=%d > 2^30", fn, max_rows);
     const int unit = dt == MOE_BF16 ? 8 : 4;
     REQUIRE(N % unit == 0 && K % unit == 0 && N <= 65536 && K <= 65536, MOE_ERR_UNSUPPORTED,
             "%s: N and K must be multiples of %d (whole 16-byte pieces) up to 65536 (N=%d K=%d)", fn, unit, N, K);

@@ -71,6 +71,21 @@ def test_grouped_refusals(L, name):
         call(rows=0, a=None, b=None, off=None, out=None)
 
 
+@pytest.mark.parametrize("name", ["moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw"])
+@pytest.mark.parametrize("rows", [2 ** 30 + 1, 2 ** 31 - 256, 2 ** 31 - 1])
+def test_grouped_refuses_rows_past_32_bits(L, name, rows):
+    """A group's rows are rounded up to whole tiles in 32 bits. Narrow matrices keep the number of tiles small, so only
+    the rows' own limit refuses these; without pointers, a call that gets past it enqueues nothing either."""
+    f = getattr(L, name)
+    for n, status in ((rows, "UNSUPPORTED"), (2 ** 30, "INVALID_ARG")):
+        with pytest.raises(L.MoEError) as e:
+            if name.endswith("dw"):
+                f(None, None, L.BF16, None, 1, n, 8, 8, None, None, L.BF16, 0, 0)
+            else:
+                f(None, None, None, L.BF16, None, 1, n, 8, 8, None, L.BF16, 0, 0)
+        assert e.value.status == "MOE_ERR_" + status, (n, str(e.value))
+
+
 def test_dropout_refusals(L):
     def call(x=P, dt=L.BF16, n=100, p=0.5, rng=P, out=P):
         L.moe_dropout(x, None, dt, n, p, rng, out, 0)
