@@ -56,7 +56,8 @@ class TrainStep:
     dtopk_w: torch.Tensor  # [T, k]
     topk_ids: torch.Tensor
     topk_w: torch.Tensor
-    routed_here: bool     # by this layer's router, all of whose experts it holds
+    routed: bool          # by this layer's router
+    routed_here: bool     # and all of its experts are this layer's
     dropout: float
     out_dropout: float
     rng: Optional[torch.Tensor]
@@ -466,12 +467,17 @@ class MoELayer:
             self._bufs[("serial", T)] = 0
             torch.cuda.current_stream().synchronize()  # the constants are there for every stream
         b = self._bufs[("train", T)]
-        self._bufs[("serial", T)] += 1
+        self._bufs[("serial", T)] += 3  # its backward and gate_backward move it on by one each
         here = topk_ids is None
         return TrainStep(x=x, b=b, **self._bufs[key], topk_ids=b.topk_ids if here else topk_ids,
-                         topk_w=b.topk_w if here else topk_w,
+                         topk_w=b.topk_w if here else topk_w, routed=here,
                          routed_here=here and self.router["w"].shape[0] == self.E_local, dropout=dropout,
                          out_dropout=out_dropout, rng=rng, serial=self._bufs[("serial", T)])
+
+    def _holds(self, step: TrainStep, calls: int) -> bool:
+        """Whether this layer's buffers hold the step after `calls` of its backward and gate_backward."""
+        T = step.x.shape[0]
+        return step.b is self._bufs.get(("train", T)) and self._bufs[("serial", T)] == step.serial + calls
 
     def new_grads(self) -> LayerGrads:
         """Zeroed weight gradients, to pass to backward."""
@@ -505,7 +511,7 @@ class MoELayer:
         (dx is then this share's part of a sum as well). A step's buffers hold its
         gradients afterwards: one backward per step."""
         T, b, dt, H, I = step.x.shape[0], step.b, self.act_dt, self.H, self.I
-        if step.serial != self._bufs.get(("serial", T)) or step.b is not self._bufs.get(("train", T)):
+        if not self._holds(step, 0):
             raise RuntimeError("the step's buffers hold a later step or its gradients")
         L.expect(dout, "dout", (step.x.dtype,), step.x.device)
         if dout.shape != step.x.shape:
@@ -545,16 +551,24 @@ class MoELayer:
         """The gate's part of a step's gradients from those of its picks'
         weights [T, k]: added to grads.dx, and router_w and router_bias. backward
         calls it unless the experts are shared with other GPUs; there it belongs
-        into the sum of their dx once."""
+        into the sum of their dx once. It reads the step's logits and picks, so it
+        comes after the step's backward and before the next forward_train of as
+        many tokens, once. grads.dx may be another tensor than backward's (a sum
+        over GPUs)."""
         r, T, dt, H = self.router, step.x.shape[0], self.act_dt, self.H
-        if r is None or step.topk_ids is not step.b.topk_ids:
+        if r is None or not step.routed:
             raise ValueError("the step was not routed by this layer's router")
+        if not self._holds(step, 1):
+            raise RuntimeError("the layer's buffers hold this step's backward no longer, or not yet, or its gate's part "
+                               "is made already")
         L.expect(dtopk_w, "dtopk_w", (torch.float32,), step.x.device)
         if tuple(dtopk_w.shape) != (T, self.k):
             raise ValueError(f"dtopk_w: shape {tuple(dtopk_w.shape)}, expected [{T}, {self.k}]")
         self._check_grads(grads)
         if grads.dx is None or grads.dx.shape != step.x.shape:
             raise ValueError("grads.dx: backward's, of this step, is needed")
+        L.expect(grads.dx, "grads.dx", (step.x.dtype,), step.x.device)
+        self._bufs[("serial", T)] += 1
         E = r["w"].shape[0]
         _, ones, offsets, dlogits, dbias = self._bufs[("constants", T)]
         L.moe_route_grad(step.b.logits, step.topk_ids, dtopk_w, T, E, self.k, r["scoring"], r.get("renormalize", True),

@@ -1,0 +1,174 @@
+"""MoELayer's training calls without a GPU: which steps, tensors and sizes they refuse, before anything is enqueued. The
+library's calls are recorded instead of launched; calls without tensors (checks of sizes alone) reach the library."""
+import types
+
+import pytest
+import torch
+
+E, H, I, K, T = 8, 64, 32, 2, 6
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+
+    import mixture_experts_layer_select_amd as pkg
+    if not os.path.exists(pkg._lib.LIB_PATH):
+        pkg.build()
+    return pkg
+
+
+@pytest.fixture
+def calls(L, monkeypatch):
+    made = []
+
+    def recorded(name, real):
+        def call(*args, **kw):
+            if not any(isinstance(a, torch.Tensor) for a in args):
+                return real(*args, **kw)
+            made.append(name)
+        return call
+    for name in ("moe_route", "moe_route_select", "moe_permute", "moe_grouped_gemm", "moe_grouped_gemm_dx",
+                 "moe_grouped_gemm_dw", "moe_swiglu", "moe_swiglu_grad", "moe_dropout", "moe_combine",
+                 "moe_combine_grad", "moe_route_grad"):
+        monkeypatch.setattr(L._lib, name, recorded(name, getattr(L._lib, name)))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(synchronize=lambda: None))
+    return made
+
+
+def layer(L, router=E, bias=True, dt=BF, base=0, E_local=E):
+    r = None
+    if router:
+        r = dict(w=torch.zeros(router, H, dtype=dt), bias=torch.zeros(router) if bias else None, scoring=L.SIGMOID)
+    return L.MoELayer("bf16" if dt == BF else "f32", H, I, K, torch.zeros(E_local, 2 * I, H, dtype=dt),
+                      torch.zeros(E_local, H, I, dtype=dt), router=r, expert_base=base)
+
+
+def tokens(n=T, dt=BF):
+    return torch.zeros(n, H, dtype=dt)
+
+
+# ---------------------------------------------------------------- the gate's part of which step
+def share(L):
+    """Half of a router's experts: backward leaves the gate's part to gate_backward."""
+    return layer(L, router=2 * E)
+
+
+def test_gate_of_a_share(L, calls):
+    m = share(L)
+    step = m.forward_train(tokens())
+    grads = m.backward(step, tokens())
+    assert "moe_route_grad" not in calls
+    grads.dx = grads.dx.clone()  # as a sum over GPUs would be
+    m.gate_backward(step, grads.topk_w, grads)
+    assert calls.count("moe_route_grad") == 1
+
+
+def test_gate_refuses_a_stale_step(L, calls):
+    """A later forward_train of as many tokens took the logits and picks."""
+    m = share(L)
+    step = m.forward_train(tokens())
+    grads = m.backward(step, tokens())
+    m.forward_train(tokens(T + 1))  # another size: other buffers
+    later = m.forward_train(tokens())
+    del calls[:]
+    with pytest.raises(RuntimeError, match="no longer"):
+        m.gate_backward(step, grads.topk_w, grads)
+    assert not calls
+    m.backward(later, tokens(), grads)
+    with pytest.raises(RuntimeError, match="no longer"):
+        m.gate_backward(step, grads.topk_w, grads)
+    m.gate_backward(later, grads.topk_w, grads)
+
+
+@pytest.mark.parametrize("done", [0, 1, 2])
+@pytest.mark.parametrize("between", [1, 2, 3])
+def test_gate_refuses_every_older_step(L, calls, done, between):
+    """Whatever was done with the step and with the later ones: forward_train, its backward, its gate's part."""
+    m = share(L)
+    step = m.forward_train(tokens())
+    grads = m.backward(step, tokens()) if done else m.new_grads()
+    if done == 2:
+        m.gate_backward(step, grads.topk_w, grads)
+    for _ in range(between):
+        later = m.forward_train(tokens())
+        for then in (lambda: None, lambda: m.backward(later, tokens(), grads),
+                     lambda: m.gate_backward(later, torch.zeros(T, K), grads)):
+            then()
+            for call in (lambda: m.gate_backward(step, torch.zeros(T, K), grads), lambda: m.backward(step, tokens())):
+                with pytest.raises(RuntimeError):
+                    call()
+
+
+def test_gate_refuses_another_layers_step(L, calls):
+    one, two = share(L), share(L)
+    steps = [m.forward_train(tokens()) for m in (one, two)]
+    grads = [m.backward(s, tokens()) for m, s in zip((one, two), steps)]
+    del calls[:]
+    with pytest.raises(RuntimeError, match="no longer"):
+        one.gate_backward(steps[1], grads[1].topk_w, grads[0])
+    assert not calls
+    three = share(L)
+    with pytest.raises(RuntimeError, match="no longer"):
+        three.gate_backward(steps[1], grads[1].topk_w, grads[1])
+
+
+def test_gate_refuses_a_step_ahead_of_its_backward(L, calls):
+    m = share(L)
+    grads = m.backward(m.forward_train(tokens()), tokens())
+    step = m.forward_train(tokens())
+    del calls[:]
+    with pytest.raises(RuntimeError, match="not yet"):
+        m.gate_backward(step, grads.topk_w, grads)
+    assert not calls
+    m.backward(step, tokens(), grads)
+    m.gate_backward(step, grads.topk_w, grads)
+
+
+def test_gate_refuses_a_second_part(L, calls):
+    """Its part is added to dx: once for each step, and backward has added it where all experts are here."""
+    m = share(L)
+    step = m.forward_train(tokens())
+    grads = m.backward(step, tokens())
+    m.gate_backward(step, grads.topk_w, grads)
+    whole = layer(L)
+    all_here = whole.forward_train(tokens())
+    got = whole.backward(all_here, tokens())
+    assert calls.count("moe_route_grad") == 2
+    for a, s, g in ((m, step, grads), (whole, all_here, got)):
+        with pytest.raises(RuntimeError, match="already"):
+            a.gate_backward(s, g.topk_w, g)
+    assert calls.count("moe_route_grad") == 2
+
+
+def test_gate_refuses_given_routing_in_the_layers_own_buffers(L, calls):
+    """Picks of an earlier step handed in again are handed in: the logits need not be theirs."""
+    m = share(L)
+    first = m.forward_train(tokens())
+    step = m.forward_train(tokens(), first.topk_ids, first.topk_w)
+    grads = m.backward(step, tokens())
+    with pytest.raises(ValueError, match="not routed"):
+        m.gate_backward(step, grads.topk_w, grads)
+
+
+def test_gate_refuses_dx_of_another_type(L, calls):
+    m = share(L)
+    step = m.forward_train(tokens())
+    grads = m.backward(step, tokens())
+    dx, grads.dx = grads.dx, grads.dx.float()
+    with pytest.raises(TypeError, match="grads.dx"):
+        m.gate_backward(step, grads.topk_w, grads)
+    grads.dx = dx
+    m.gate_backward(step, grads.topk_w, grads)
+
+
+def test_a_step_refused_by_the_gate_keeps_its_backward(L, calls):
+    m = share(L)
+    step = m.forward_train(tokens())
+    with pytest.raises(RuntimeError):
+        m.gate_backward(step, torch.zeros(T, K), m.new_grads())
+    m.backward(step, tokens())
+    with pytest.raises(RuntimeError, match="later step"):
+        m.backward(step, tokens())
