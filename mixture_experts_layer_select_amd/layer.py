@@ -409,6 +409,19 @@ class MoELayer:
             if tuple(rng.shape) != (2, 2):
                 raise ValueError(f"rng: shape {tuple(rng.shape)}, expected (2, 2)")
 
+    def _check_apart(self, x, residual):
+        """The step writes its buffers before it reads the residual (which may lie in
+        what backward alone writes) and before backward reads x."""
+        forward, backward = self._bufs.get(("written", x.shape[0]), ((), ()))
+        for t, name, own in ((x, "x", forward + backward), (residual, "residual", forward)):
+            if t is None:
+                continue
+            first = t.data_ptr()
+            past = first + t.numel() * t.element_size()
+            if any(first < end and at < past for at, end in own):
+                raise ValueError(f"{name}: lies in the layer's buffers for {x.shape[0]} tokens, which the step writes (pass "
+                                 "a copy)")
+
     def forward_train(self, x: torch.Tensor, topk_ids=None, topk_w=None, *, dropout: float = 0.0, residual=None,
                       out_dropout: float = 0.0, rng=None, stream=None) -> TrainStep:
         """The layer with what its gradients need kept (f32 and bf16 weights):
@@ -426,6 +439,7 @@ class MoELayer:
         L.expect(residual, "residual", (x.dtype,), x.device)
         if residual is not None and residual.shape != x.shape:
             raise ValueError(f"residual: shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+        self._check_apart(x, residual)
         step = self._train_step(x, topk_ids, topk_w, dropout, out_dropout, rng)
         b, r, cap, dt = step.b, self.router, T * self.k + T, self.act_dt
         if topk_ids is None:  # backward needs every logit, so moe_route at every size
@@ -465,6 +479,11 @@ class MoELayer:
                 torch.tensor([0, T], dtype=torch.int32, device=dev), torch.empty((T, E), dtype=x.dtype, device=dev),
                 torch.empty((E, 8), dtype=torch.float32, device=dev))
             self._bufs[("serial", T)] = 0
+            # from where to where the buffers lie, those that backward alone writes apart
+            own = {n: (t.data_ptr(), t.data_ptr() + t.nbytes) for n, t in {**vars(b), **self._bufs[key]}.items()
+                   if isinstance(t, torch.Tensor)}
+            last = tuple(own.pop(n) for n in ("dx", "dtopk_w"))
+            self._bufs[("written", T)] = (tuple(own.values()), last)
             torch.cuda.current_stream().synchronize()  # the constants are there for every stream
         b = self._bufs[("train", T)]
         self._bufs[("serial", T)] += 3  # its backward and gate_backward move it on by one each

@@ -172,3 +172,27 @@ def test_a_step_refused_by_the_gate_keeps_its_backward(L, calls):
     m.backward(step, tokens())
     with pytest.raises(RuntimeError, match="later step"):
         m.backward(step, tokens())
+
+
+# ---------------------------------------------------------------- inputs in the layer's own buffers
+def test_inputs_in_the_steps_buffers_are_refused(L, calls):
+    """The next step of as many tokens writes its output before it reads the residual, and before backward reads x."""
+    m = layer(L)
+    step = m.forward_train(tokens())
+    del calls[:]
+    for kw, name in ((dict(x=tokens(), residual=step.out), "residual"), (dict(x=step.out), "x"),
+                     (dict(x=step.dx), "x"), (dict(x=step.b.x_perm[3:3 + T]), "x"),
+                     (dict(x=tokens(), residual=step.b.y_perm[1:1 + T]), "residual")):
+        with pytest.raises(ValueError, match=f"^{name}: lies in the layer's buffers for {T} tokens"):
+            m.forward_train(**kw)
+    assert not calls
+    m.backward(step, tokens())  # and the step is still the layer's
+
+
+def test_inputs_beside_the_steps_buffers_are_taken(L, calls):
+    m, other = layer(L), layer(L)
+    step = m.forward_train(tokens())
+    other.forward_train(step.out, residual=step.out)
+    m.forward_train(step.out[:T - 1], residual=step.out[1:])  # of another size: other buffers
+    m.forward_train(tokens(), residual=step.dx)  # which backward alone writes
+    m.forward_train(tokens(0), residual=tokens(0))
