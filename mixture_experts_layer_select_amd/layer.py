@@ -408,6 +408,9 @@ class MoELayer:
             L.expect(rng, "rng", (torch.int64,), self.w13.device)
             if tuple(rng.shape) != (2, 2):
                 raise ValueError(f"rng: shape {tuple(rng.shape)}, expected (2, 2)")
+            for each in p:
+                if each:  # the library's check of p alone: no elements, nothing to launch
+                    L.moe_dropout(None, None, self.act_dt, 0, each, rng.data_ptr(), None, 0)
 
     def _check_apart(self, x, residual):
         """The step writes its buffers before it reads the residual (which may lie in

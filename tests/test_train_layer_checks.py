@@ -196,3 +196,19 @@ def test_inputs_beside_the_steps_buffers_are_taken(L, calls):
     m.forward_train(step.out[:T - 1], residual=step.out[1:])  # of another size: other buffers
     m.forward_train(tokens(), residual=step.dx)  # which backward alone writes
     m.forward_train(tokens(0), residual=tokens(0))
+
+
+# ---------------------------------------------------------------- ahead of the first launch
+@pytest.mark.parametrize("name", ["dropout", "out_dropout"])
+@pytest.mark.parametrize("p", [1.0, -0.1, 0.999999, float("nan")])
+def test_dropout_is_refused_ahead_of_the_launches(L, calls, name, p):
+    m, rng = layer(L), torch.zeros((2, 2), dtype=torch.int64)
+    step = m.forward_train(tokens(), dropout=0.5, out_dropout=0.25, rng=rng)
+    del calls[:]
+    with pytest.raises(L.MoEError) as e:
+        m.forward_train(tokens(), rng=rng, **{name: p})
+    assert e.value.status == "MOE_ERR_INVALID_ARG" and not calls
+    m.backward(step, tokens())  # its buffers are not taken
+    with pytest.raises(L.MoEError):
+        m.forward_train(tokens(T + 3), rng=rng, **{name: p})
+    assert ("train", T + 3) not in m._bufs
