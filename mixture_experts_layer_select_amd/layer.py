@@ -390,12 +390,12 @@ class MoELayer:
         return b
 
     # ------------------------------------------------------------------ training
-    def _check_train(self):
+    def _check_train(self, routed: bool):
         if self.fmt not in ("f32", "bf16"):
             raise ValueError(f"training needs f32 or bf16 weights, not {self.fmt}")
         unit = 8 if self.fmt == "bf16" else 4
         sizes = dict(H=self.H, I=self.I)
-        if self.router is not None:
+        if routed and self.router is not None:  # the gate's products run along the experts
             sizes["the router's experts"] = self.router["w"].shape[0]
         for name, n in sizes.items():
             if n % unit:
@@ -435,7 +435,7 @@ class MoELayer:
         only after backward. x is read again by backward. One step per number of
         tokens: the next forward_train of as many tokens takes its buffers. The
         first of a size makes them and waits for the device; it is not captured."""
-        self._check_train()
+        self._check_train(topk_ids is None)
         self.check_inputs(x, topk_ids, topk_w)
         self._check_rng(rng, dropout, out_dropout)
         T = x.shape[0]

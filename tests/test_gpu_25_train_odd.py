@@ -1,0 +1,37 @@
+"""Training steps of odd layers: experts that are no multiple of the types' 16 bytes with the routing handed in."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def L():
+    import mixture_experts_layer_select_amd as pkg
+    return pkg
+
+
+def rand(seed, *shape, dt=BF, std=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(shape, generator=g, device=DEV) * std).to(dt)
+
+
+@pytest.mark.parametrize("fmt,E", [("bf16", 60), ("f32", 9)])
+def test_given_routing_beside_a_router_of_any_size(L, fmt, E):
+    """The same bits as a layer without a router."""
+    T, H, I, k, dt = 21, 64, 40, 4, BF if fmt == "bf16" else F32
+    w13, w2 = rand(1, E, 2 * I, H, dt=dt, std=H ** -0.5), rand(2, E, H, I, dt=dt, std=I ** -0.5)
+    x, dout = rand(3, T, H, dt=dt), rand(4, T, H, dt=dt)
+    ids = rand(5, T, E, dt=F32).topk(k, 1).indices.to(torch.int32)
+    tw = torch.rand((T, k), device=DEV)
+    got = []
+    for router in (None, dict(w=rand(6, E, H, dt=dt), bias=torch.zeros(E, device=DEV), scoring=L.SIGMOID)):
+        m = L.MoELayer(fmt, H, I, k, w13, w2, router=router)
+        step = m.forward_train(x, ids, tw)
+        out = step.out.clone()
+        g = m.backward(step, dout)
+        got.append((out, g.dx, g.w13, g.w2, g.topk_w))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and (a != 0).any()

@@ -212,3 +212,18 @@ def test_dropout_is_refused_ahead_of_the_launches(L, calls, name, p):
     with pytest.raises(L.MoEError):
         m.forward_train(tokens(T + 3), rng=rng, **{name: p})
     assert ("train", T + 3) not in m._bufs
+
+
+# ---------------------------------------------------------------- sizes
+@pytest.mark.parametrize("dt,experts", [(BF, 60), (BF, 9), (torch.float32, 6), (torch.float32, 9)])
+def test_any_number_of_experts_where_the_routing_is_given(L, calls, dt, experts):
+    """The gate's products run along the experts in whole 16 bytes; a step with its routing handed in makes none."""
+    m = layer(L, router=experts, dt=dt, E_local=experts)
+    with pytest.raises(ValueError, match=f"the router's experts = {experts} is not a multiple of"):
+        m.forward_train(tokens(dt=dt))
+    assert not calls
+    step = m.forward_train(tokens(dt=dt), torch.zeros((T, K), dtype=torch.int32), torch.ones(T, K))
+    grads = m.backward(step, tokens(dt=dt))
+    assert "moe_route" not in calls and "moe_route_grad" not in calls
+    with pytest.raises(ValueError, match="not routed"):
+        m.gate_backward(step, grads.topk_w, grads)
