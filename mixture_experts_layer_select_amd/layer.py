@@ -162,9 +162,11 @@ class MoELayer:
     # ------------------------------------------------------------------ buffers
     def buffers(self, T: int, device=None, key=None) -> LayerBuffers:
         key = T if key is None else key
-        if key in self._bufs:
-            return self._bufs[key]
-        device = device or self.w13.device
+        if key not in self._bufs:
+            self._bufs[key] = self._new_buffers(T, device or self.w13.device)
+        return self._bufs[key]
+
+    def _new_buffers(self, T: int, device) -> LayerBuffers:
         k, H = self.k, self.H
         cap = T * k + T
         i32 = dict(dtype=torch.int32, device=device)
@@ -201,7 +203,6 @@ class MoELayer:
         if self.uses_route_select(T):
             b.ws_route = torch.empty(L.moe_route_select_workspace_size(T, E), dtype=torch.uint8,
                                      device=device)
-        self._bufs[key] = b
         return b
 
     # ------------------------------------------------------------------ steps
@@ -471,23 +472,24 @@ class MoELayer:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError(f"the first forward_train of {T} tokens makes the layer's buffers: run it once before "
                                    "the capture")
-            b, cap = self.buffers(T, dev, ("train", T)), T * self.k + T
-            self._bufs[key] = dict(gu=torch.empty((cap, 2 * self.I), dtype=x.dtype, device=dev),
-                                   a=torch.empty((cap, self.I), dtype=x.dtype, device=dev),
-                                   dx=torch.empty_like(x), dtopk_w=torch.empty_like(b.topk_w))
+            b, cap = self._new_buffers(T, dev), T * self.k + T
+            rest = dict(gu=torch.empty((cap, 2 * self.I), dtype=x.dtype, device=dev),
+                        a=torch.empty((cap, self.I), dtype=x.dtype, device=dev),
+                        dx=torch.empty_like(x), dtopk_w=torch.empty_like(b.topk_w))
             # constants: one for each pick and, for column sums, eight for each token; the gate's one group and its buffers
             E = self.router["w"].shape[0] if self.router is not None else 0
-            self._bufs[("constants", T)] = (
+            constants = (
                 torch.ones((T, self.k), dtype=torch.float32, device=dev), torch.ones((T, 8), dtype=x.dtype, device=dev),
                 torch.tensor([0, T], dtype=torch.int32, device=dev), torch.empty((T, E), dtype=x.dtype, device=dev),
                 torch.empty((E, 8), dtype=torch.float32, device=dev))
-            self._bufs[("serial", T)] = 0
             # from where to where the buffers lie, those that backward alone writes apart
-            own = {n: (t.data_ptr(), t.data_ptr() + t.nbytes) for n, t in {**vars(b), **self._bufs[key]}.items()
+            own = {n: (t.data_ptr(), t.data_ptr() + t.nbytes) for n, t in {**vars(b), **rest}.items()
                    if isinstance(t, torch.Tensor)}
             last = tuple(own.pop(n) for n in ("dx", "dtopk_w"))
-            self._bufs[("written", T)] = (tuple(own.values()), last)
             torch.cuda.current_stream().synchronize()  # the constants are there for every stream
+            # all of them or, where memory ran out on the way, none
+            self._bufs.update({("train", T): b, key: rest, ("constants", T): constants, ("serial", T): 0,
+                               ("written", T): (tuple(own.values()), last)})
         b = self._bufs[("train", T)]
         self._bufs[("serial", T)] += 3  # its backward and gate_backward move it on by one each
         here = topk_ids is None

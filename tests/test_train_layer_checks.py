@@ -227,3 +227,23 @@ def test_any_number_of_experts_where_the_routing_is_given(L, calls, dt, experts)
     assert "moe_route" not in calls and "moe_route_grad" not in calls
     with pytest.raises(ValueError, match="not routed"):
         m.gate_backward(step, grads.topk_w, grads)
+
+
+# ---------------------------------------------------------------- buffers
+@pytest.mark.parametrize("name,at", [("empty", 3), ("empty", 12), ("empty_like", 1), ("empty_like", 2), ("ones", 1),
+                                     ("ones", 2), ("tensor", 1), ("empty", 15)])
+def test_memory_that_runs_out_on_the_first_step(L, calls, monkeypatch, name, at):
+    """The step fails with the allocation's own error, leaves nothing behind, and runs once there is memory."""
+    m, x, real, made = layer(L), tokens(), getattr(torch, name), []
+
+    def allocate(*args, **kw):
+        made.append(0)
+        if len(made) == at:
+            raise torch.OutOfMemoryError("out of memory")
+        return real(*args, **kw)
+    monkeypatch.setattr(torch, name, allocate)
+    with pytest.raises(torch.OutOfMemoryError):
+        m.forward_train(x)
+    assert not m._bufs and not calls
+    monkeypatch.setattr(torch, name, real)
+    m.backward(m.forward_train(x), tokens())
