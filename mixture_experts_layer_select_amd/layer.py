@@ -166,7 +166,9 @@ class MoELayer:
             self._bufs[key] = self._new_buffers(T, device or self.w13.device)
         return self._bufs[key]
 
-    def _new_buffers(self, T: int, device) -> LayerBuffers:
+    def _new_buffers(self, T: int, device, training: bool = False) -> LayerBuffers:
+        """For training without the workspaces of the steps that it does not call: the
+        fused experts' intermediate alone is as large as that many rows of I."""
         k, H = self.k, self.H
         cap = T * k + T
         i32 = dict(dtype=torch.int32, device=device)
@@ -175,7 +177,7 @@ class MoELayer:
         E = self.router["w"].shape[0] if self.router is not None else 0
         xdt = torch.uint8 if self.fmt == "fp8" else act
         ws_p = L.moe_permute_workspace_size(T, k, self.E_local)
-        ws_f = L.moe_expert_ffn_workspace_size(self.weights, cap)
+        ws_f = 0 if training else L.moe_expert_ffn_workspace_size(self.weights, cap)
         b = LayerBuffers(
             T=T,
             logits=torch.empty((T, E), **f32) if E else None,
@@ -200,7 +202,7 @@ class MoELayer:
             else:
                 b.x_tok = torch.empty((T, H), dtype=torch.uint8, device=device)
                 b.x_tok_scale = torch.empty((H // 128, T), **f32)
-        if self.uses_route_select(T):
+        if self.uses_route_select(T) and not training:
             b.ws_route = torch.empty(L.moe_route_select_workspace_size(T, E), dtype=torch.uint8,
                                      device=device)
         return b
@@ -472,7 +474,7 @@ class MoELayer:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError(f"the first forward_train of {T} tokens makes the layer's buffers: run it once before "
                                    "the capture")
-            b, cap = self._new_buffers(T, dev), T * self.k + T
+            b, cap = self._new_buffers(T, dev, training=True), T * self.k + T
             rest = dict(gu=torch.empty((cap, 2 * self.I), dtype=x.dtype, device=dev),
                         a=torch.empty((cap, self.I), dtype=x.dtype, device=dev),
                         dx=torch.empty_like(x), dtopk_w=torch.empty_like(b.topk_w))

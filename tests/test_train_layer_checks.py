@@ -247,3 +247,15 @@ def test_memory_that_runs_out_on_the_first_step(L, calls, monkeypatch, name, at)
     assert not m._bufs and not calls
     monkeypatch.setattr(torch, name, real)
     m.backward(m.forward_train(x), tokens())
+
+
+def test_training_holds_no_workspace_of_inference(L, calls):
+    """From 4096 tokens on inference routes through a workspace, and its experts keep their intermediate in another."""
+    m = L.MoELayer("bf16", 128, 128, 2, torch.zeros(E, 256, 128, dtype=BF), torch.zeros(E, 128, 128, dtype=BF),
+                   router=dict(w=torch.zeros(E, 128, dtype=BF), bias=None, scoring=L.SIGMOID))
+    x = torch.zeros(4096, 128, dtype=BF)
+    b = m.forward_train(x).b
+    assert b.ws_ffn.numel() <= 1 and b.ws_route is None and "moe_route" in calls
+    inference = m.buffers(4096)
+    assert inference is not b and inference.ws_route is not None
+    assert inference.ws_ffn.numel() == L.moe_expert_ffn_workspace_size(m.weights, 3 * 4096)
