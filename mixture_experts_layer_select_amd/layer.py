@@ -118,6 +118,7 @@ class MoELayer:
                                       sh.get("w2_scale"))
         self.n_groups = self.E_local + (1 if shared is not None else 0)
         self._bufs = {}
+        self._trains = set()  # (tokens, routed by the layer) whose sizes the training calls take
 
     def _check_mxfp4(self, sh: dict):
         """Codes and scale bytes of the sizes that the kernels read; the
@@ -393,9 +394,12 @@ class MoELayer:
         return b
 
     # ------------------------------------------------------------------ training
-    def _check_train(self, routed: bool):
+    def _check_train(self, T: int, routed: bool):
+        """Everything about the layer and T that a step's calls refuse, ahead of the first of them."""
         if self.fmt not in ("f32", "bf16"):
             raise ValueError(f"training needs f32 or bf16 weights, not {self.fmt}")
+        if (T, routed) in self._trains:
+            return
         unit = 8 if self.fmt == "bf16" else 4
         sizes = dict(H=self.H, I=self.I)
         if routed and self.router is not None:  # the gate's products run along the experts
@@ -403,6 +407,27 @@ class MoELayer:
         for name, n in sizes.items():
             if n % unit:
                 raise ValueError(f"training in {self.fmt}: {name} = {n} is not a multiple of {unit}")
+        if T * self.k + T > 1 << 30:
+            raise ValueError(f"training: {T} tokens of {self.k} picks are more than 2^30 rows")
+        sh, dt = self.shared or {}, self.act_dt
+        for name, t in (("w13", self.w13), ("w2", self.w2), ("shared w13", sh.get("w13")), ("shared w2", sh.get("w2"))):
+            self._check_aligned(t, name)
+        # the calls without tokens: they check their sizes, and launch nothing
+        if routed and self.router is not None:
+            r = self.router
+            L.moe_route(None, None, None, dt, 0, self.H, r["w"].shape[0], self.k, r["scoring"],
+                        r.get("renormalize", True), None, None, None, 0)
+        L.moe_permute(None, 0, self.k, self.expert_base, self.E_local, self.shared is not None, None, dt, self.H, dt, None,
+                      None, None, None, None, None, None, 0, 0)
+        for N, K in ((2 * self.I, self.H), (self.H, self.I)):
+            L.moe_grouped_gemm(None, None, None, dt, None, self.n_groups, 0, N, K, None, dt, False, 0)
+        L.moe_combine(None, dt, None, None, 0, self.k, self.H, None, -1, None, dt, 0)
+        self._trains.add((T, routed))
+
+    @staticmethod
+    def _check_aligned(t, name: str):
+        if t is not None and t.data_ptr() % 16:
+            raise ValueError(f"{name}: not 16-byte aligned, as the grouped products need it")
 
     def _check_rng(self, rng, *p):
         if any(p):
@@ -438,7 +463,7 @@ class MoELayer:
         only after backward. x is read again by backward. One step per number of
         tokens: the next forward_train of as many tokens takes its buffers. The
         first of a size makes them and waits for the device; it is not captured."""
-        self._check_train(topk_ids is None)
+        self._check_train(x.shape[0] if x.dim() else 0, topk_ids is None)
         self.check_inputs(x, topk_ids, topk_w)
         self._check_rng(rng, dropout, out_dropout)
         T = x.shape[0]

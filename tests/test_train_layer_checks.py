@@ -259,3 +259,53 @@ def test_training_holds_no_workspace_of_inference(L, calls):
     inference = m.buffers(4096)
     assert inference is not b and inference.ws_route is not None
     assert inference.ws_ffn.numel() == L.moe_expert_ffn_workspace_size(m.weights, 3 * 4096)
+
+
+def off_by_one(*shape):
+    """A tensor that begins one element behind an allocation."""
+    n = 1
+    for s in shape:
+        n *= s
+    return torch.zeros(n + 1, dtype=BF)[1:].view(shape)
+
+
+def test_sizes_are_refused_ahead_of_the_launches(L, calls):
+    """What the library's calls of a step refuse is refused with nothing launched and no buffers made."""
+    def step(m, n=3):
+        m.forward_train(torch.zeros(n, m.H, dtype=BF), torch.zeros((n, m.k), dtype=torch.int32), torch.zeros(n, m.k))
+
+    def plain(experts, h, i, k):
+        return L.MoELayer("bf16", h, i, k, torch.zeros(experts, 2 * i, h, dtype=BF), torch.zeros(experts, h, i, dtype=BF))
+    for m, match in ((plain(257, 8, 8, 2), "E_local=257"), (plain(1, 8, 8, 257), "k=257"),
+                     (plain(1, 65544, 8, 1), "K=65544"), (plain(1, 8, 32776, 1), "N=65552")):
+        with pytest.raises(L.MoEError, match=match) as e:
+            step(m)
+        assert e.value.status == "MOE_ERR_UNSUPPORTED" and not m._bufs, match
+    wide = layer(L, router=264)
+    with pytest.raises(L.MoEError, match="E=264"):
+        wide.forward_train(tokens())
+    step(wide)  # handed in
+    del calls[:]
+    with pytest.raises(L.MoEError, match="unknown scoring"):
+        m = layer(L)
+        m.router["scoring"] = 7
+        m.forward_train(tokens())
+    with pytest.raises(ValueError, match="expected .T, 64."):
+        layer(L).forward_train(torch.zeros((), dtype=BF))
+    m = plain(1, 8, 8, 255)
+    n = 2 ** 30 // 256 + 1
+    with pytest.raises(ValueError, match="more than 2.30 rows"):
+        m.forward_train(torch.empty(n, 8, dtype=BF), torch.empty((n, 255), dtype=torch.int32), torch.empty(n, 255))
+    assert not m._bufs and not calls
+
+
+@pytest.mark.parametrize("name", ["w13", "w2", "shared w13", "shared w2"])
+def test_weights_off_their_alignment_are_refused(L, calls, name):
+    def make(what, *shape):
+        return off_by_one(*shape) if what == name else torch.zeros(shape, dtype=BF)
+    m = L.MoELayer("bf16", H, I, K, make("w13", E, 2 * I, H), make("w2", E, H, I),
+                   shared=dict(w13=make("shared w13", 2 * I, H), w2=make("shared w2", H, I)),
+                   router=dict(w=torch.zeros(E, H, dtype=BF), bias=None, scoring=L.SIGMOID))
+    with pytest.raises(ValueError, match=f"^{name}: not 16-byte aligned"):
+        m.forward_train(tokens())
+    assert not calls and not m._bufs
