@@ -548,6 +548,8 @@ class MoELayer:
             if t is None or t.shape != like.shape:
                 raise ValueError(f"grads.{name}: {'missing' if t is None else tuple(t.shape)}, expected {tuple(like.shape)}")
             L.expect(t, f"grads.{name}", (torch.float32,), like.device)
+            if name != "router_bias":
+                self._check_aligned(t, f"grads.{name}")
 
     def backward(self, step: TrainStep, dout: torch.Tensor, grads: Optional[LayerGrads] = None,
                  accumulate: bool = False, stream=None) -> LayerGrads:
@@ -573,6 +575,8 @@ class MoELayer:
             with self._on(stream):  # zeroed there, ahead of what is written
                 grads = self.new_grads()
         self._check_grads(grads)
+        if step.routed_here:
+            self._check_aligned(self.router["w"], "the router's w")
         self._bufs[("serial", T)] += 1
         sh, cap, n = self.shared or {}, T * self.k + T, self.n_groups
         if step.out_dropout:
@@ -619,13 +623,19 @@ class MoELayer:
         if grads.dx is None or grads.dx.shape != step.x.shape:
             raise ValueError("grads.dx: backward's, of this step, is needed")
         L.expect(grads.dx, "grads.dx", (step.x.dtype,), step.x.device)
+        self._check_aligned(grads.dx, "grads.dx")
+        self._check_aligned(r["w"], "the router's w")
         self._bufs[("serial", T)] += 1
         E = r["w"].shape[0]
         _, ones, offsets, dlogits, dbias = self._bufs[("constants", T)]
         L.moe_route_grad(step.b.logits, step.topk_ids, dtopk_w, T, E, self.k, r["scoring"], r.get("renormalize", True),
                          dlogits, dt, stream)
         L.moe_grouped_gemm_dx(dlogits, r["w"], None, dt, offsets, 1, T, E, H, grads.dx, dt, True, stream)
-        L.moe_grouped_gemm_dw(dlogits, step.x, dt, offsets, 1, T, E, H, grads.router_w, None, L.F32, accumulate, stream)
+        x = step.x
+        if x.data_ptr() % 16:  # the other calls take any x
+            with self._on(stream):
+                x = x.clone()
+        L.moe_grouped_gemm_dw(dlogits, x, dt, offsets, 1, T, E, H, grads.router_w, None, L.F32, accumulate, stream)
         if grads.router_bias is not None:  # column sums: a product with columns of ones
             L.moe_grouped_gemm_dw(dlogits, ones, dt, offsets, 1, T, E, 8, dbias, None, L.F32,
                                   False, stream)

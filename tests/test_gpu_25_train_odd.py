@@ -35,3 +35,21 @@ def test_given_routing_beside_a_router_of_any_size(L, fmt, E):
         got.append((out, g.dx, g.w13, g.w2, g.topk_w))
     for a, b in zip(*got):
         assert torch.equal(a, b) and (a != 0).any()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f32"])
+def test_inputs_of_any_alignment(L, fmt):
+    """x, dout and the residual one element behind an allocation: the bits of aligned ones."""
+    T, E, H, I, k, dt = 19, 8, 72, 24, 2, BF if fmt == "bf16" else F32
+    w13, w2 = rand(1, E, 2 * I, H, dt=dt, std=H ** -0.5), rand(2, E, H, I, dt=dt, std=I ** -0.5)
+    m = L.MoELayer(fmt, H, I, k, w13, w2, router=dict(w=rand(3, E, H, dt=dt, std=0.2), bias=rand(4, E, dt=F32),
+                                                      scoring=L.SIGMOID))
+    tensors, got = [rand(s, T, H, dt=dt) for s in (5, 6, 7)], []
+    for off in (0, 1):
+        x, dout, res = (torch.empty(T * H + 1, device=DEV, dtype=dt)[off:off + T * H].view(T, H).copy_(t) for t in tensors)
+        step = m.forward_train(x, residual=res)
+        out = step.out.clone()
+        g = m.backward(step, dout)
+        got.append((out, step.topk_ids.clone(), g.dx.clone(), g.w13, g.w2, g.router_w, g.router_bias))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and (a != 0).any()

@@ -309,3 +309,45 @@ def test_weights_off_their_alignment_are_refused(L, calls, name):
     with pytest.raises(ValueError, match=f"^{name}: not 16-byte aligned"):
         m.forward_train(tokens())
     assert not calls and not m._bufs
+
+
+@pytest.mark.parametrize("name", ["w13", "w2", "shared_w13", "shared_w2", "router_w"])
+def test_gradients_off_their_alignment_are_refused(L, calls, name):
+    """Ahead of the launches: the step keeps its buffers and takes a backward with others."""
+    m = L.MoELayer("bf16", H, I, K, torch.zeros(E, 2 * I, H, dtype=BF), torch.zeros(E, H, I, dtype=BF),
+                   shared=dict(w13=torch.zeros(2 * I, H, dtype=BF), w2=torch.zeros(H, I, dtype=BF)),
+                   router=dict(w=torch.zeros(E, H, dtype=BF), bias=torch.zeros(E), scoring=L.SIGMOID))
+    step, grads = m.forward_train(tokens()), m.new_grads()
+    good = getattr(grads, name)
+    setattr(grads, name, torch.zeros(good.numel() + 1)[1:].view(good.shape))
+    del calls[:]
+    with pytest.raises(ValueError, match=f"^grads.{name}: not 16-byte aligned"):
+        m.backward(step, tokens(), grads)
+    assert not calls
+    setattr(grads, name, good)
+    grads.router_bias = torch.zeros(E + 1)[1:]  # any
+    m.backward(step, tokens(), grads)
+
+
+def test_a_router_off_its_alignment_is_refused_ahead_of_the_gradients(L, calls):
+    for m in (layer(L), share(L)):
+        m.router["w"] = off_by_one(*m.router["w"].shape)
+        step = m.forward_train(tokens())
+        del calls[:]
+        with pytest.raises(ValueError, match="^the router's w: not 16-byte aligned"):
+            grads = m.backward(step, tokens())
+            assert not step.routed_here
+            del calls[:]
+            m.gate_backward(step, grads.topk_w, grads)
+        assert not calls
+
+
+def test_dx_off_its_alignment_is_refused(L, calls):
+    m = share(L)
+    step = m.forward_train(tokens())
+    grads = m.backward(step, tokens())
+    dx, grads.dx = grads.dx, off_by_one(T, H)
+    with pytest.raises(ValueError, match="^grads.dx: not 16-byte aligned"):
+        m.gate_backward(step, grads.topk_w, grads)
+    grads.dx = dx
+    m.gate_backward(step, grads.topk_w, grads)
