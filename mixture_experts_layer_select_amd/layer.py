@@ -480,13 +480,13 @@ class MoELayer:
         sh = self.shared or {}
         L.moe_grouped_gemm(b.x_perm, self.w13, sh.get("w13"), dt, b.offsets, self.n_groups, cap, 2 * self.I, self.H,
                            step.gu, dt, False, stream)
-        L.moe_swiglu(step.gu, dt, self._n_rows(b), cap, self.I, dropout, rng, step.a, stream)
+        L.moe_swiglu(step.gu, dt, self._n_rows(b), cap, self.I, dropout, rng if dropout else None, step.a, stream)
         L.moe_grouped_gemm(step.a, self.w2, sh.get("w2"), dt, b.offsets, self.n_groups, cap, self.H, self.I, b.y_perm,
                            dt, False, stream)
         self.combine(b, step.topk_w, stream)
         if residual is not None or out_dropout:
-            L.moe_dropout(b.out, residual, dt, b.out.numel(), out_dropout, None if rng is None else rng[1], b.out,
-                          stream)
+            L.moe_dropout(b.out, residual, dt, b.out.numel(), out_dropout, rng[1] if out_dropout else None,
+                          b.out, stream)
         return step
 
     def _n_rows(self, b: LayerBuffers):
@@ -587,7 +587,8 @@ class MoELayer:
                            self.E_local if self.shared is not None else -1, dy, step.dtopk_w, stream)
         # a's buffer takes its gradient, and a again from gu, whose buffer takes its own
         L.moe_grouped_gemm_dx(dy, self.w2, sh.get("w2"), dt, b.offsets, n, cap, H, I, step.a, dt, False, stream)
-        L.moe_swiglu_grad(step.gu, step.a, dt, self._n_rows(b), cap, I, step.dropout, step.rng, step.gu, step.a, stream)
+        L.moe_swiglu_grad(step.gu, step.a, dt, self._n_rows(b), cap, I, step.dropout,
+                          step.rng if step.dropout else None, step.gu, step.a, stream)
         L.moe_grouped_gemm_dw(dy, step.a, dt, b.offsets, n, cap, H, I, grads.w2, grads.shared_w2, L.F32, accumulate,
                               stream)
         L.moe_grouped_gemm_dw(step.gu, b.x_perm, dt, b.offsets, n, cap, 2 * I, H, grads.w13, grads.shared_w13, L.F32,

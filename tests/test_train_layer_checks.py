@@ -351,3 +351,15 @@ def test_dx_off_its_alignment_is_refused(L, calls):
         m.gate_backward(step, grads.topk_w, grads)
     grads.dx = dx
     m.gate_backward(step, grads.topk_w, grads)
+
+
+@pytest.mark.parametrize("rng", [torch.zeros(1, dtype=torch.int64), torch.zeros(2, 2), torch.zeros(2, 4)[:, ::2]])
+def test_rng_is_not_looked_at_without_dropout(L, calls, monkeypatch, rng):
+    """No call is handed a tensor that nothing has checked."""
+    m = layer(L)
+    seen = []
+    for name in ("moe_swiglu", "moe_swiglu_grad", "moe_dropout"):
+        monkeypatch.setattr(L._lib, name, lambda *args: seen.append(any(a is rng for a in args)))
+    step = m.forward_train(tokens(), residual=tokens(), rng=rng)
+    m.backward(step, tokens())
+    assert len(seen) == 3 and not any(seen)
