@@ -247,9 +247,19 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGrad p) {
 //   sigmoid:               w_j = s_j           dl_j = s_j (1 - s_j) dw_j
 //   softmax, renormalised: over the picks      dl_j = w_j (dw_j - D)
 //   softmax:               over all E          dl_e = [e picked] w_e dw_e - p_e D
+// 1 - s is made from exp(-|l|) beside s, not from s: picks are confident, and the fp32 difference is off by 0.9% at a
+// logit of 12 and 0 at 18.
 // Lane l owns experts 4l .. 4l + 3 of the output row and every 64th pick. An
 // expert picked twice gets both picks' sums.
 constexpr int kGateMaxE = 256;
+
+struct Sigmoid {
+    float s, rest;  // 1 / (1 + exp(-l)) and 1 / (1 + exp(l)), each to a few units of its own last place
+};
+__device__ __forceinline__ Sigmoid sigmoid_of(float l) {
+    const float e = expf(-fabsf(l)), large = 1.0f / (1.0f + e), small = e / (1.0f + e);
+    return l >= 0.f ? Sigmoid{large, small} : Sigmoid{small, large};
+}
 
 template <typename TO, bool kSigmoid, bool kRenorm>
 __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict__ logits,
@@ -273,10 +283,12 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
     }
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, d[kMax];
     if constexpr (kSigmoid) {
-        float sum = 0.f, dot = 0.f;
+        float sum = 0.f, dot = 0.f, rest[kMax];
 #pragma unroll
         for (int i = 0; i < kMax; ++i) {
-            w[i] = id[i] >= 0 ? 1.0f / (1.0f + expf(-l[i])) : 0.f;
+            const Sigmoid s = sigmoid_of(l[i]);
+            w[i] = id[i] >= 0 ? s.s : 0.f;
+            rest[i] = s.rest;
             sum += w[i];
         }
         sum = kRenorm ? wave_sum(sum) : 1.0f;
@@ -284,7 +296,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
         for (int i = 0; i < kMax; ++i) dot += w[i] / sum * dw[i];
         dot = kRenorm ? wave_sum(dot) : 0.f;
 #pragma unroll
-        for (int i = 0; i < kMax; ++i) d[i] = w[i] / sum * (1.0f - w[i]) * (dw[i] - dot);
+        for (int i = 0; i < kMax; ++i) d[i] = w[i] / sum * rest[i] * (dw[i] - dot);
     } else {
         float all[4], top = -__builtin_inff(), sum = 0.f, dot = 0.f;
         if constexpr (kRenorm) {
@@ -373,12 +385,13 @@ __global__ __launch_bounds__(256) void route_grad_few_kernel(const float* __rest
     if (id < 0) dw = 0.f;
     float d;
     if constexpr (kSigmoid) {
-        const float s = id >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.f;
+        const Sigmoid sig = sigmoid_of(l);
+        const float s = id >= 0 ? sig.s : 0.f;
         if constexpr (kRenorm) {
             const float w = s / over_eight(s, add), dot = over_eight(w * dw, add);
-            d = w * (1.0f - s) * (dw - dot);
+            d = w * sig.rest * (dw - dot);
         } else {
-            d = s * (1.0f - s) * dw;
+            d = s * sig.rest * dw;
         }
     } else {
         const float top = over_eight(id >= 0 ? l : -__builtin_inff(), most);
