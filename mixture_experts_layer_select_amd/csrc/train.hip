@@ -351,6 +351,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const float* __restrict
         if (4 * lane + i < E) store1(dlogits + t * E + 4 * lane + i, acc[i]);
 }
 
+// Between what lanes of a wave write to LDS for one another and what these read of it: the wave's LDS accesses run in
+// their order, so this costs no wait, but each lane's own program does not show the compiler that they meet.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The same for at most eight picks where nothing runs over all E: a wave takes eight tokens, a pick in each lane, and
 // puts their rows together in LDS. 16384 tokens of 256 experts take 5.7 us so, 11.1 with a wave for each token.
 template <int kCtrl>
@@ -400,8 +408,11 @@ __global__ __launch_bounds__(256) void route_grad_few_kernel(const float* __rest
         d = w * (dw - dot);
     }
     // one pick of each token at a time, in order: an id that stands twice gets both
-    for (int i = 0; i < k; ++i)
+    wave_sync();
+    for (int i = 0; i < k; ++i) {
         if (j == i && id >= 0) row[(lane >> 3) * kGateMaxE + id] += d;
+        wave_sync();
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (t0 + i >= T) break;
