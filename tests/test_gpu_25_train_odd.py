@@ -53,3 +53,30 @@ def test_inputs_of_any_alignment(L, fmt):
         got.append((out, step.topk_ids.clone(), g.dx.clone(), g.w13, g.w2, g.router_w, g.router_bias))
     for a, b in zip(*got):
         assert torch.equal(a, b) and (a != 0).any()
+
+
+def test_residual_and_output_dropout_on_shares(L):
+    """The residual in one share's call and one mask for the output: the shares' outputs add up to the whole layer's, and so
+    do their gradients of x. fp32; the sums of the parts are taken in another order, of at most k + 2 terms, each of which went
+    through products of at most 64 terms."""
+    T, E, H, I, k = 24, 16, 64, 32, 4
+    w13, w2 = rand(1, E, 2 * I, H, dt=F32, std=H ** -0.5), rand(2, E, H, I, dt=F32, std=I ** -0.5)
+    router = dict(w=rand(3, E, H, dt=F32, std=0.2), bias=None, scoring=L.SIGMOID)
+    x, dout, res = (rand(s, T, H, dt=F32) for s in (4, 5, 6))
+    rng = torch.tensor([[1, 2], [3, 4]], device=DEV)
+    whole = L.MoELayer("f32", H, I, k, w13, w2, router=router)
+    step = whole.forward_train(x, residual=res, out_dropout=0.25, rng=rng)
+    out, grads = step.out.clone(), whole.backward(step, dout)
+    outs, dxs, parts = [], [], []
+    for base in (0, 8):
+        m = L.MoELayer("f32", H, I, k, w13[base:base + 8].contiguous(), w2[base:base + 8].contiguous(), router=router,
+                       expert_base=base)
+        step = m.forward_train(x, residual=None if base else res, out_dropout=0.25, rng=rng)
+        outs.append(step.out.clone())
+        parts.append((m, step, m.backward(step, dout)))
+        dxs.append(parts[-1][2].dx)
+    total = parts[0][2].topk_w + parts[1][2].topk_w
+    parts[0][0].gate_backward(parts[0][1], total, parts[0][2])
+    for got, want in ((sum(outs), out), (sum(dxs), grads.dx), (parts[0][2].router_w, grads.router_w)):
+        err = (got.double() - want.double()).norm() / want.double().norm()
+        assert err <= (k + 2 + 3 * 64) * 2.0 ** -24, float(err)
