@@ -257,7 +257,7 @@ struct Sigmoid {
     float s, rest;  // 1 / (1 + exp(-l)) and 1 / (1 + exp(l)), each to a few units of its own last place
 };
 __device__ __forceinline__ Sigmoid sigmoid_of(float l) {
-    const float e = expf(-fabsf(l)), large = 1.0f / (1.0f + e), small = e / (1.0f + e);
+    const float e = expf(-fabsf(l)), large = 1.0f / (1.0f + e), small = e * large;
     return l >= 0.f ? Sigmoid{large, small} : Sigmoid{small, large};
 }
 

@@ -437,7 +437,7 @@ class MoELayer:
             if tuple(rng.shape) != (2, 2):
                 raise ValueError(f"rng: shape {tuple(rng.shape)}, expected (2, 2)")
             for each in p:
-                if each:  # the library's check of p alone: no elements, nothing to launch
+                if not 0.0 <= each <= 0.99:  # the library's check of p alone: no elements, nothing to launch
                     L.moe_dropout(None, None, self.act_dt, 0, each, rng.data_ptr(), None, 0)
 
     def _check_apart(self, x, residual):
@@ -599,7 +599,7 @@ class MoELayer:
                       self.E_local if self.shared is not None else -1, step.dx, dt, stream)
         grads.dx, grads.topk_w = step.dx, step.dtopk_w
         if step.routed_here:
-            self.gate_backward(step, step.dtopk_w, grads, accumulate, stream)
+            self._gate_backward(step, step.dtopk_w, grads, accumulate, stream)
         return grads
 
     def gate_backward(self, step: TrainStep, dtopk_w: torch.Tensor, grads: LayerGrads, accumulate: bool = False,
@@ -611,7 +611,7 @@ class MoELayer:
         comes after the step's backward and before the next forward_train of as
         many tokens, once. grads.dx may be another tensor than backward's (a sum
         over GPUs)."""
-        r, T, dt, H = self.router, step.x.shape[0], self.act_dt, self.H
+        r, T = self.router, step.x.shape[0]
         if r is None or not step.routed:
             raise ValueError("the step was not routed by this layer's router")
         if not self._holds(step, 1):
@@ -626,6 +626,10 @@ class MoELayer:
         L.expect(grads.dx, "grads.dx", (step.x.dtype,), step.x.device)
         self._check_aligned(grads.dx, "grads.dx")
         self._check_aligned(r["w"], "the router's w")
+        self._gate_backward(step, dtopk_w, grads, accumulate, stream)
+
+    def _gate_backward(self, step: TrainStep, dtopk_w: torch.Tensor, grads: LayerGrads, accumulate: bool, stream):
+        r, T, dt, H = self.router, step.x.shape[0], self.act_dt, self.H
         self._bufs[("serial", T)] += 1
         E = r["w"].shape[0]
         _, ones, offsets, dlogits, dbias = self._bufs[("constants", T)]
