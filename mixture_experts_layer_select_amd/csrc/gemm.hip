@@ -1038,7 +1038,7 @@ __global__ __launch_bounds__(kBigThreads, 1) void gemm_weights_kernel(GemmArgs a
 
 // The height with the shortest estimate: the rounds of items that a workgroup walks, times a tile's stores (0.049 h us in
 // bf16, 1.6 times that in fp32) and its steps (0.3 + 0.0011 h us each), at the bound's rows for each group. 5000 rows of
-// one group, 256 x 7168: 93 us in tiles of 256 rows, 60 of 64; 16384 of 32, 7168 x 2048: 562 of 256, 1173 of 64; 150 of 16, 680 x
+// one group, 256 x 7168: 93 us in tiles of 256 rows, 48 of 64; 16384 of 32, 7168 x 2048: 562 of 256, 1173 of 64; 150 of 16, 680 x
 // 680: 8.4 and 10.2, 7.9 of 192.
 template <typename TO>
 moe_status launch_weights(GemmArgs a, hipStream_t st) {

@@ -473,7 +473,7 @@ class MoELayer:
         self._check_apart(x, residual)
         step = self._train_step(x, topk_ids, topk_w, dropout, out_dropout, rng)
         b, r, cap, dt = step.b, self.router, T * self.k + T, self.act_dt
-        if topk_ids is None:  # backward needs every logit, so moe_route at every size
+        if topk_ids is None:  # at every size by moe_route, which leaves the logits that the gate's gradient reads
             L.moe_route(x, r["w"], r.get("bias"), dt, T, self.H, r["w"].shape[0], self.k, r["scoring"],
                         r.get("renormalize", True), b.logits, b.topk_ids, b.topk_w, stream)
         self.permute(x, b, step.topk_ids, stream)
