@@ -461,8 +461,15 @@ class MoELayer:
         [2, 2] on the device, seed and offset of the experts' dropout and of the
         output's, read when the calls run and again by backward, so it changes
         only after backward. x is read again by backward. One step per number of
-        tokens: the next forward_train of as many tokens takes its buffers. The
-        first of a size makes them and waits for the device; it is not captured."""
+        tokens: the next forward_train of as many tokens takes its buffers, out
+        among them, so neither x nor residual may be in them. The first of a size
+        makes them and waits for the device; it is not captured.
+
+        Where this GPU holds a part of the router's experts, out is residual +
+        drop(this part's sum): hand the residual (and the shared expert) to one
+        GPU. out_dropout goes over the sum if all of them draw from the same
+        rng[1]. rng[0] counts this GPU's rows, so equal ones repeat each other's
+        masks inside the experts: give each GPU its own."""
         self._check_train(x.shape[0] if x.dim() else 0, topk_ids is None)
         self.check_inputs(x, topk_ids, topk_w)
         self._check_rng(rng, dropout, out_dropout)
